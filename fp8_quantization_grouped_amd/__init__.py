@@ -57,6 +57,12 @@ SIGNATURES = {
                                  _I64, _I64, _I64, _P, _I64, _I, _P, _SZ, _P]),
     "fp8_mx_grouped_gemm_wgrad": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64,
                                        _I64, _I64, _P, _I64, _I, _P, _SZ, _P]),
+    "fp8_block_quant_rowwise": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "fp8_block_quant_dual": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                  _P]),
+    "fp8_block_quant_weights": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P]),
+    "fp8_block_grouped_gemm": (_I, [_I, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64,
+                                    _P, _I32, _I64, _I64, _I64, _P, _I64, _I, _P, _SZ, _P]),
 }
 
 
@@ -378,4 +384,183 @@ def fp8_mx_grouped_gemm_wgrad(a: torch.Tensor, a_e8m0: torch.Tensor, b: torch.Te
                                          _ptr(offsets), groups, M, N, K, _ptr(c), c.stride(-2),
                                          _OUT[c.dtype], _ptr(ws), ws.numel(), _stream(a))
     _check("fp8_mx_grouped_gemm_wgrad", st)
+    return c
+
+
+# ------------------------------------------------------------- block-scaled FP8 (blocks of 128)
+
+BLOCK = 128
+_BYTES = (torch.uint8, torch.float8_e4m3fn)  # how e4m3fn bytes may be held
+
+
+def _want(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows_of(t: torch.Tensor, what: str, dtypes, shape=None, dev=None) -> torch.Tensor:
+    """t as a device tensor of one of dtypes with unit stride in its last dimension, rows that do
+    not overlap, and the given shape (None: any size) on device dev."""
+    _want(t.is_cuda and (dev is None or t.device == dev), f"{what} must be on the operands' GPU")
+    _want(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+    if shape is not None:
+        _want(len(shape) == t.dim() and all(n is None or n == m for n, m in zip(shape, t.shape)),
+              f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _want(t.dim() < 1 or t.shape[-1] <= 1 or t.stride(-1) == 1,
+          f"{what} must have unit stride in its last dimension")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Leading dimension of a matrix; the stride of a single or an empty row says nothing."""
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 and cols > 0 else 0 if cols == 0 else max(t.stride(0), cols)
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """The C entry point on the current stream of dev, with dev the current device."""
+    if dev.index == torch.cuda.current_device():
+        _check(name, getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _padded_bytes(rows: int, cols: int, dev) -> torch.Tensor:
+    """[rows, cols] bytes whose rows start on 16 bytes, as the GEMMs take them."""
+    return torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)[:, :cols]
+
+
+_BF16, _F32, _I32T = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+
+
+def fp8_block_quant_rowwise(x: torch.Tensor, q: torch.Tensor | None = None,
+                            scales: torch.Tensor | None = None):
+    """x: bf16 [rows, cols] in blocks of 1 x 128.  Returns (q [rows, cols] e4m3fn bytes, scales
+    float32 [ceil(cols/128), rows], the factors d with x ~ q * d).  Rows of a new q start on 16
+    bytes."""
+    _rows_of(x, "x", _BF16, (None, None))
+    rows, cols = x.shape
+    dev = x.device
+    q = _padded_bytes(rows, cols, dev) if q is None else _rows_of(q, "q", _BYTES, x.shape, dev)
+    if scales is None:
+        scales = torch.empty((_blocks(cols), rows), dtype=torch.float32, device=dev)
+    else:
+        _rows_of(scales, "scales", _F32, (_blocks(cols), rows), dev)
+    _call("fp8_block_quant_rowwise", dev, x.data_ptr(), rows, cols, _ld(x), q.data_ptr(), _ld(q),
+          scales.data_ptr(), _ld(scales) if cols else rows)
+    return q, scales
+
+
+def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
+                         s_rows: torch.Tensor | None = None, q_t: torch.Tensor | None = None,
+                         s_cols: torch.Tensor | None = None, transposed_only: bool = False):
+    """x: bf16 [rows, cols] in both layouts from one read.  Returns ((q [rows, cols], s_rows
+    [ceil(cols/128), rows]) as fp8_block_quant_rowwise would, (q_t [cols, rows], s_cols float32
+    [ceil(rows/128), cols]) in blocks of 128 rows of a column).  transposed_only: the second pair
+    alone is made, and the first is (None, None)."""
+    _rows_of(x, "x", _BF16, (None, None))
+    rows, cols = x.shape
+    dev = x.device
+    f32 = torch.float32
+    if transposed_only:
+        _want(q is None and s_rows is None, "transposed_only takes no q and s_rows")
+        row_args = (None, 0, None, 0)
+    else:
+        q = _padded_bytes(rows, cols, dev) if q is None else _rows_of(q, "q", _BYTES, x.shape, dev)
+        if s_rows is None:
+            s_rows = torch.empty((_blocks(cols), rows), dtype=f32, device=dev)
+        else:
+            _rows_of(s_rows, "s_rows", _F32, (_blocks(cols), rows), dev)
+        row_args = (q.data_ptr(), _ld(q), s_rows.data_ptr(), _ld(s_rows) if cols else rows)
+    if q_t is None:
+        q_t = _padded_bytes(cols, rows, dev)
+    else:
+        _rows_of(q_t, "q_t", _BYTES, (cols, rows), dev)
+    if s_cols is None:
+        s_cols = torch.empty((_blocks(rows), cols), dtype=f32, device=dev)
+    else:
+        _rows_of(s_cols, "s_cols", _F32, (_blocks(rows), cols), dev)
+    _call("fp8_block_quant_dual", dev, x.data_ptr(), rows, cols, _ld(x), *row_args, q_t.data_ptr(),
+          _ld(q_t) if cols else rows, s_cols.data_ptr(), _ld(s_cols) if rows else cols)
+    return (q, s_rows), (q_t, s_cols)
+
+
+def fp8_block_quant_weights(w: torch.Tensor, experts: int, q: torch.Tensor | None = None,
+                            q_t: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """w: bf16 [experts * rows, cols], each expert's matrix in blocks of 128 x 128.  Returns (q
+    [experts * rows, cols], q_t [cols, experts * rows] with the experts' transposes side by side,
+    scales float32 [experts, ceil(rows/128), ceil(cols/128)], which serve both)."""
+    _rows_of(w, "w", _BF16, (None, None))
+    _want(experts > 0 and w.shape[0] % experts == 0, "w must hold experts matrices of equal size")
+    rows, cols = w.shape[0] // experts, w.shape[1]
+    dev = w.device
+    q = _padded_bytes(*w.shape, dev) if q is None else _rows_of(q, "q", _BYTES, w.shape, dev)
+    if q_t is None:
+        q_t = _padded_bytes(cols, w.shape[0], dev)
+    else:
+        _rows_of(q_t, "q_t", _BYTES, (cols, w.shape[0]), dev)
+    shape = (experts, _blocks(rows), _blocks(cols))
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _rows_of(scales, "scales", _F32, shape, dev)
+        _want(scales.is_contiguous(), "scales must be contiguous")
+    _call("fp8_block_quant_weights", dev, w.data_ptr(), experts, rows, cols, _ld(w), q.data_ptr(),
+          _ld(q), q_t.data_ptr(), _ld(q_t) if cols else w.shape[0], scales.data_ptr())
+    return q, q_t, scales
+
+
+def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
+                           b_scales: torch.Tensor, offsets: torch.Tensor | None = None,
+                           c: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                           workspace: torch.Tensor | None = None):
+    """Block-scaled FP8 grouped GEMM (see the C header for the two modes).
+    Forward: a [M, K] with a_scales [ceil(K/128), M], b [groups, N, K] with b_scales [groups,
+    ceil(N/128), ceil(K/128)] (any strides: a transpose of the quantizer's factors, with b a view
+    of its transposed bytes, gives the data gradient); returns [M, N].
+    Weight gradient: a [K, M] with a_scales [ceil(M/128), K], b [N, M] with b_scales [ceil(M/128),
+    N]; returns [groups, K, N].
+    offsets: int32 [groups] cumulative group ends, None for one group.  The output is bfloat16 or
+    float32 (out_dtype, or the dtype of a given c).  gemm_offsets_status reads the offsets check
+    from a given workspace."""
+    _want(mode in (GEMM_FWD_MGROUPED, GEMM_WGRAD_KGROUPED), "unknown mode")
+    fwd = mode == GEMM_FWD_MGROUPED
+    _rows_of(a, "a", _BYTES, (None, None))
+    dev = a.device
+    rows, inner = a.shape  # forward M, K; weight gradient K, M
+    if offsets is not None:
+        _rows_of(offsets, "offsets", _I32T, (None,), dev)
+    groups = 1 if offsets is None else offsets.shape[0]
+    _rows_of(b, "b", _BYTES, (groups, None, inner) if fwd else (None, inner), dev)
+    N = b.shape[-2]
+    kb = _blocks(inner)
+    _rows_of(a_scales, "a_scales", _F32, (kb, rows), dev)
+    lda, ld_sa = _ld(a), max(_ld(a_scales), rows) if kb else rows
+    if fwd:
+        _want(b_scales.device == dev and b_scales.dtype == torch.float32
+              and tuple(b_scales.shape) == (groups, _blocks(N), kb),
+              f"b_scales must be float32 {(groups, _blocks(N), kb)} on the operands' GPU")
+        # a dimension of one entry has no stride that means anything
+        bgs = b.stride(0) if groups > 1 else 0
+        ldb = b.stride(1) if N > 1 else max(b.stride(1), inner)
+        sbg, sbn, sbk = (d if n > 1 else 0 for d, n in zip(b_scales.stride(), b_scales.shape))
+        M, K, shape = rows, inner, (rows, N)
+    else:
+        _rows_of(b_scales, "b_scales", _F32, (kb, N), dev)
+        bgs, ldb, sbg, sbn, sbk = 0, _ld(b), 0, 1, max(_ld(b_scales), N) if kb else N
+        M, K, shape = inner, rows, (groups, rows, N)
+    if c is None:
+        c = torch.empty(shape, dtype=out_dtype, device=dev)
+    c = _gemm_out(c, shape, out_dtype, dev)
+    _want(c.device == dev, "c must be on the operands' GPU")
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _call("fp8_block_grouped_gemm", dev, mode, a.data_ptr(), lda, a_scales.data_ptr(), ld_sa,
+          b.data_ptr(), ldb, bgs, b_scales.data_ptr(), sbn, sbk, sbg,
+          None if offsets is None else offsets.data_ptr(), groups, M, N, K, c.data_ptr(),
+          c.stride(-2) if c.shape[-2] > 1 else max(c.stride(-2), N), _OUT[c.dtype], ws, ws_bytes)
     return c

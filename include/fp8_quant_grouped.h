@@ -325,6 +325,82 @@ fp8q_status_t fp8_mx_grouped_gemm_wgrad(const uint8_t* a, int64_t lda, const uin
                                         fp8q_out_t out_dtype, void* workspace,
                                         size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Block-scaled FP8: one fp32 factor per block of 128.  Elements are OCP e4m3fn.  For a block
+ *   s = 448 / max(absmax, 1e-12f)  and  d = 1 / s   (IEEE quotients, each rounded once to fp32),
+ *   q = ENC(clamp(RN32(x * s), -448, 448)), round to nearest even;
+ * the STORED factor is d, the one that dequantization multiplies by (x ~ dec(q) * d): the products
+ * below use a factor per contraction block inside their sums, where a division has no place.
+ * Blocks are counted from index 0 of their matrix; the last one of a row, column or matrix may be
+ * shorter.
+ *
+ * fp8_block_quant_rowwise: blocks of 1 x 128 along each row (activations of the forward, output
+ * gradients of the data gradient).
+ *   x       bf16 [rows][ld_x], ld_x >= cols
+ *   q       u8   [rows][ld_q], ld_q >= cols
+ *   scales  fp32 [ceil(cols/128)][ld_s], ld_s >= rows: scales[b*ld_s + r] is d of row r, columns
+ *           128 b .. (a contraction step of the product reads 256 consecutive rows' factors)
+ * Any sizes and alignments; 16-byte aligned x, ld_x and cols multiples of 8, and 8-byte aligned q
+ * rows take the wide accesses.  rows == 0 or cols == 0 is a no-op. */
+fp8q_status_t fp8_block_quant_rowwise(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                      uint8_t* q, int64_t ld_q, float* scales, int64_t ld_s,
+                                      hipStream_t stream);
+
+/* Both layouts from one read of x: blocks of 1 x 128 along rows as above, and blocks of 128 x 1
+ * along columns with the bytes transposed (the operands of the weight gradient).
+ *   q, s_rows  as q, scales of fp8_block_quant_rowwise, bit for bit; both may be null together, for
+ *              the transposed layout alone (ld_q and ld_sr are then ignored)
+ *   q_t        u8   [cols][ld_qt], ld_qt >= rows: q_t[c*ld_qt + r]
+ *   s_cols     fp32 [ceil(rows/128)][ld_sc], ld_sc >= cols: d of column c, rows 128 b ..
+ * Row blocks are counted from row 0 and know nothing of token groups: a block that two groups
+ * share keeps its one factor, and the weight gradient sums each group's own rows of it. */
+fp8q_status_t fp8_block_quant_dual(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                   uint8_t* q, int64_t ld_q, float* s_rows, int64_t ld_sr,
+                                   uint8_t* q_t, int64_t ld_qt, float* s_cols, int64_t ld_sc,
+                                   hipStream_t stream);
+
+/* Expert weights in blocks of 128 x 128, both layouts from one read.
+ *   w       bf16 [experts*rows][ld_w], ld_w >= cols: experts matrices of rows x cols
+ *   q       u8   [experts*rows][ld_q], ld_q >= cols, or null
+ *   q_t     u8   [cols][ld_qt], ld_qt >= experts*rows, or null (not both): the matrices'
+ *           transposes side by side, expert e at columns e*rows ..
+ *   scales  fp32 [experts][ceil(rows/128)][ceil(cols/128)], contiguous; they serve both layouts
+ * experts <= 65535 (FP8Q_ERR_UNSUPPORTED beyond). */
+fp8q_status_t fp8_block_quant_weights(const uint16_t* w, int64_t experts, int64_t rows, int64_t cols,
+                                      int64_t ld_w, uint8_t* q, int64_t ld_q, uint8_t* q_t,
+                                      int64_t ld_qt, float* scales, hipStream_t stream);
+
+/* Block-scaled FP8 grouped GEMM.  Operand layouts, groups, offsets check and the modes are those
+ * of fp8_grouped_gemm; the factors enter per contraction block:
+ *
+ * mode FP8Q_GEMM_FWD_MGROUPED:
+ *   c[m,n] = sum_kb a_scales[kb*ld_sa + m] * b_scales[g*sb_group_stride + (n/128)*sb_n + kb*sb_k]
+ *                   * sum_{k in kb} dec(a[m,k]) * dec(b_g[n,k])        for m in group g
+ *   a u8 [M][lda] with a_scales fp32 [ceil(K/128)][ld_sa >= M]; b_g = b + g*b_group_stride, rows n
+ *   at stride ldb >= K.  Weights [G][N][K] quantized by fp8_block_quant_weights (rows = N,
+ *   cols = K): ldb = K, b_group_stride = N*K, sb_n = ceil(K/128), sb_k = 1,
+ *   sb_group_stride = ceil(N/128)*ceil(K/128).  The data gradient dX[m,k] is the same call with N
+ *   and K exchanged, b = q_t (ldb = G*N, b_group_stride = N) and sb_n, sb_k exchanged.
+ * mode FP8Q_GEMM_WGRAD_KGROUPED:
+ *   c[g,k,n] = sum_tb a_scales[tb*ld_sa + k] * b_scales[tb*sb_k + n]
+ *                     * sum_{m in g, m in tb} dec(a[k,m]) * dec(b[n,m])
+ *   a u8 [K][lda >= M], a_scales [ceil(M/128)][ld_sa >= K]; b u8 [N][ldb >= M], b_scales
+ *   [ceil(M/128)][sb_k >= N]; b_group_stride = sb_group_stride = 0, sb_n = 1.  An empty group
+ *   writes zeros; bytes of other groups and padding may hold any code.
+ *
+ * offsets may be null with groups == 1: one group of all M rows.  workspace may be null: the
+ * offsets check is then not reported (the kernel uses clamped offsets either way); otherwise
+ * fp8_grouped_gemm_workspace_size bytes.  Sums: each block's products on the matrix cores (see
+ * Accuracy at fp8_grouped_gemm) from zero, times the factors into an fp32 accumulator.
+ * Limits (FP8Q_ERR_UNSUPPORTED): as for fp8_grouped_gemm, and (N/128 + 1) * sb_n < 2^29. */
+fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uint8_t* a, int64_t lda,
+                                     const float* a_scales, int64_t ld_sa, const uint8_t* b,
+                                     int64_t ldb, int64_t b_group_stride, const float* b_scales,
+                                     int64_t sb_n, int64_t sb_k, int64_t sb_group_stride,
+                                     const int32_t* offsets, int32_t groups, int64_t M, int64_t N,
+                                     int64_t K, void* c, int64_t ldc, fp8q_out_t out_dtype,
+                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
