@@ -63,6 +63,13 @@ SIGNATURES = {
     "fp8_block_quant_weights": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P]),
     "fp8_block_grouped_gemm": (_I, [_I, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64,
                                     _P, _I32, _I64, _I64, _I64, _P, _I64, _I, _P, _SZ, _P]),
+    "moe_route_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "moe_route": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I32, _I, ctypes.c_float, _P,
+                       _P, _P, _SZ, _P]),
+    "fp8_moe_few_tokens_workspace_size": (_SZ, [_I64, _I64, _I32]),
+    "fp8_moe_few_tokens": (_I, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _I64, _I64, _P, _I64, _I64,
+                                _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64,
+                                _P, _SZ, _P]),
 }
 
 
@@ -564,3 +571,93 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
           None if offsets is None else offsets.data_ptr(), groups, M, N, K, c.data_ptr(),
           c.stride(-2) if c.shape[-2] > 1 else max(c.stride(-2), N), _OUT[c.dtype], ws, ws_bytes)
     return c
+
+
+# ------------------------------------------------- a mixture-of-experts layer for a few tokens
+
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+_SCORING = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+def moe_route_workspace_size(T: int, H: int, E: int) -> int:
+    return int(lib().moe_route_workspace_size(T, H, E))
+
+
+def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
+              bias: torch.Tensor | None = None, scoring: str = "softmax",
+              renormalize: bool = True, scale: float = 1.0, ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """The experts of each token: x bf16 [T, H], router bf16 [E, H], bias float32 [E] (added to the
+    scores for the choice alone).  scoring: "softmax" or "sigmoid".  Returns (ids int32 [T, top_k],
+    weights float32 [T, top_k]) in descending order; ties go to the lowest index."""
+    _rows_of(x, "x", _BF16, (None, None))
+    dev = x.device
+    T, H = x.shape
+    _rows_of(router, "router", _BF16, (None, H), dev)
+    E = router.shape[0]
+    _want(scoring in _SCORING, "scoring must be softmax or sigmoid")
+    _want(1 <= top_k <= E, "top_k must lie in [1, number of experts]")
+    if bias is not None:
+        _rows_of(bias, "bias", _F32, (E,), dev)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    else:
+        _want(_rows_of(ids, "ids", _I32T, (T, top_k), dev).is_contiguous(), "ids must be contiguous")
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    else:
+        _want(_rows_of(weights, "weights", _F32, (T, top_k), dev).is_contiguous(),
+              "weights must be contiguous")
+    if workspace is None:
+        workspace = torch.empty((moe_route_workspace_size(T, H, E),), dtype=torch.uint8, device=dev)
+    _call("moe_route", dev, x.data_ptr(), T, H, _ld(x), router.data_ptr(), E, _ld(router),
+          None if bias is None else bias.data_ptr(), _SCORING[scoring], top_k, int(renormalize),
+          scale, ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.nbytes)
+    return ids, weights
+
+
+def fp8_moe_few_tokens_workspace_size(T: int, I: int, top_k: int) -> int:
+    return int(lib().fp8_moe_few_tokens_workspace_size(T, I, top_k))
+
+
+def _expert_weights(w, s, what, shape, dev):
+    """The pointers and strides of block-scaled expert weights, as the C entry point takes them."""
+    _rows_of(w, what, _BYTES, shape, dev)
+    E, n, k = w.shape
+    _want(s.device == dev and s.dtype == torch.float32 and tuple(s.shape) == (E, _blocks(n), _blocks(k)),
+          f"{what}'s scales must be float32 {(E, _blocks(n), _blocks(k))} on the operands' GPU")
+    sg, sn, sk = (d if m > 1 else 0 for d, m in zip(s.stride(), s.shape))
+    return (w.data_ptr(), w.stride(1) if n > 1 else max(w.stride(1), k), w.stride(0) if E > 1 else 0,
+            s.data_ptr(), sn, sk, sg)
+
+
+def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                       w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor,
+                       y: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """The experts' feed-forward of a few tokens (at most 128): x bf16 [T, H]; ids int32 and
+    weights float32 [T, top_k] (moe_route's); w13 [E, 2I, H] and w2 [E, H, I] e4m3fn bytes with
+    scales [E, ceil(2I/128), ceil(H/128)] and [E, ceil(H/128), ceil(I/128)]
+    (fp8_block_quant_weights').  Returns y bf16 [T, H].  An id outside [0, E) adds nothing."""
+    _rows_of(x, "x", _BF16, (None, None))
+    dev = x.device
+    T, H = x.shape
+    _want(_rows_of(ids, "ids", _I32T, (T, None), dev).is_contiguous(), "ids must be contiguous")
+    top_k = ids.shape[1]
+    _want(_rows_of(weights, "weights", _F32, (T, top_k), dev).is_contiguous(),
+          "weights must be contiguous")
+    _want(w13.dim() == 3 and w13.shape[1] % 2 == 0, "w13 must be [E, 2I, H]")
+    E, I = w13.shape[0], w13.shape[1] // 2
+    args13 = _expert_weights(w13, s13, "w13", (E, 2 * I, H), dev)
+    args2 = _expert_weights(w2, s2, "w2", (E, H, I), dev)
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _rows_of(y, "y", _BF16, (T, H), dev)
+    if workspace is None:
+        need = fp8_moe_few_tokens_workspace_size(T, I, top_k)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _call("fp8_moe_few_tokens", dev, x.data_ptr(), T, H, _ld(x), ids.data_ptr(),
+          weights.data_ptr(), top_k, *args13, *args2, E, I, y.data_ptr(), _ld(y),
+          workspace.data_ptr(), workspace.nbytes)
+    return y

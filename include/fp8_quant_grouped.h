@@ -401,6 +401,53 @@ fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uint8_t* a, in
                                      int64_t K, void* c, int64_t ldc, fp8q_out_t out_dtype,
                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * A mixture-of-experts layer for a few tokens (decoding): routing, then the experts' SwiGLU
+ * feed-forward on block-scaled weights.
+ *
+ * moe_route: x bf16 [T][ld_x >= H], router bf16 [E][ld_r >= H].
+ *   logits[t,e] = sum_h x[t,h] * router[e,h]                                   (fp32 sums)
+ *   scores      = softmax over e, or 1 / (1 + exp(-logits))
+ *   choice      the top_k experts by scores + bias (bias fp32 [E], or null: by logits), in
+ *               descending order; ties go to the lowest index, NaN goes last
+ *   weights     the chosen scores (without the bias), divided by their sum if renormalize, times
+ *               scale
+ *   ids int32 [T][top_k], weights fp32 [T][top_k]; workspace moe_route_workspace_size bytes, any
+ *   content, 4-byte aligned.
+ * Limits (FP8Q_ERR_UNSUPPORTED): E <= 1024, top_k <= 32, H, ld_x and ld_r multiples of 8, x and
+ * router 16-byte aligned, T <= 1048560.  T == 0 is a no-op. */
+typedef enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 } fp8q_scoring_t;
+size_t moe_route_workspace_size(int64_t T, int64_t H, int64_t E);
+fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, const uint16_t* router,
+                        int64_t E, int64_t ld_r, const float* bias, fp8q_scoring_t scoring,
+                        int32_t top_k, int renormalize, float scale, int32_t* ids, float* weights,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* fp8_moe_few_tokens: for every token t
+ *   y[t] = sum_j weights[t,j] * W2_e h,  h = bf16( silu(G_e x_t) * (U_e x_t) ),  e = ids[t,j]
+ * with e4m3fn weights in blocks of 128 x 128 (fp8_block_quant_weights): [G_e; U_e] = w13[e] is
+ * 2I x H (gate rows first), W2_e = w2[e] is H x I.  Activations stay bf16; sums are fp32.  An id
+ * outside [0, E) adds nothing (an expert that lives elsewhere); a token with none gives zeros.
+ *   x bf16 [T][ld_x >= H]; ids int32, weights fp32 [T][top_k]
+ *   w13 rows at stride ld13 >= H, experts at w13_group_stride; w2 rows at ld2 >= I
+ *   s13, s2 fp32: the factor of row n and column k of expert e is
+ *     s[e*group_stride + (n/128)*s_n + (k/128)*s_k]
+ *   y bf16 [T][ld_y >= H]; workspace fp8_moe_few_tokens_workspace_size bytes (h), any content,
+ *   16-byte aligned.
+ * Two kernels; every sum has a fixed order.  Limits (FP8Q_ERR_UNSUPPORTED): T <= 128 (the grouped
+ * product takes more), E <= 1024, top_k <= 32, H and I multiples of 16, ld_x a multiple of 8, the
+ * weights' strides multiples of 16, x, w13 and w2 16-byte aligned.  T == 0 is a no-op. */
+size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t I, int32_t top_k);
+fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x,
+                                 const int32_t* ids, const float* weights, int32_t top_k,
+                                 const uint8_t* w13, int64_t ld13, int64_t w13_group_stride,
+                                 const float* s13, int64_t s13_n, int64_t s13_k,
+                                 int64_t s13_group_stride, const uint8_t* w2, int64_t ld2,
+                                 int64_t w2_group_stride, const float* s2, int64_t s2_n,
+                                 int64_t s2_k, int64_t s2_group_stride, int64_t E, int64_t I,
+                                 uint16_t* y, int64_t ld_y, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
