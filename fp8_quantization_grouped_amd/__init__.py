@@ -66,7 +66,7 @@ SIGNATURES = {
     "moe_route_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "moe_route": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I32, _I, ctypes.c_float, _P,
                        _P, _P, _SZ, _P]),
-    "fp8_moe_few_tokens_workspace_size": (_SZ, [_I64, _I64, _I32]),
+    "fp8_moe_few_tokens_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
     "fp8_moe_few_tokens": (_I, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _I64, _I64, _P, _I64, _I64,
                                 _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64,
                                 _P, _SZ, _P]),
@@ -617,8 +617,8 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     return ids, weights
 
 
-def fp8_moe_few_tokens_workspace_size(T: int, I: int, top_k: int) -> int:
-    return int(lib().fp8_moe_few_tokens_workspace_size(T, I, top_k))
+def fp8_moe_few_tokens_workspace_size(T: int, H: int, I: int, top_k: int) -> int:
+    return int(lib().fp8_moe_few_tokens_workspace_size(T, H, I, top_k))
 
 
 def _expert_weights(w, s, what, shape, dev):
@@ -655,7 +655,7 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     else:
         _rows_of(y, "y", _BF16, (T, H), dev)
     if workspace is None:
-        need = fp8_moe_few_tokens_workspace_size(T, I, top_k)
+        need = fp8_moe_few_tokens_workspace_size(T, H, I, top_k)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     _call("fp8_moe_few_tokens", dev, x.data_ptr(), T, H, _ld(x), ids.data_ptr(),
           weights.data_ptr(), top_k, *args13, *args2, E, I, y.data_ptr(), _ld(y),

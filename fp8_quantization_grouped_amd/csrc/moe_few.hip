@@ -6,9 +6,8 @@
 //            ([G_e; U_e] = w13[e], 2 I x H; W2_e = w2[e], H x I; one fp32 factor per 128 x 128)
 //
 // Bound: HBM.  With few tokens every chosen expert's 3 H I weight bytes are read for a handful of
-// multiplications each, so the kernels are built around streaming them once: no operand goes
-// through LDS, a lane's 16-byte weight loads feed the matrix cores directly, and the activations
-// (small, shared by all blocks) come from the caches.  The weights are widened to bf16 (exact) and
+// multiplications each, so the kernels are built around streaming them once: a lane's 16-byte
+// weight loads feed the matrix cores directly.  The weights are widened to bf16 (exact) and
 // multiply the bf16 activations as they are: nothing is quantized on the way, and the matrix
 // cores, which would be idle otherwise, take up to 16 tokens for the price of one.
 //
@@ -17,8 +16,8 @@
 // lane group l / 16 of a 64-byte piece of a weight row takes bytes 16 (l / 16) .. + 15, one 16-byte
 // load for two instructions.  Result register i of lane l is token 4 (l / 16) + i, weight row l % 16.
 //
-// Every sum has a fixed order: a block's waves split the contraction (gate and up) or the experts
-// (down) the same way for the same sizes and ids, and are added in wave order.
+// Every sum has a fixed order: a contraction's parts are added in wave order, a token's experts in
+// the order of its choices.
 #include "common.hpp"
 
 namespace fp8q {
@@ -198,12 +197,20 @@ struct MoeArgs {
     int64_t ld13, gs13, ld2, gs2;          // strides of rows and experts, bytes
     const float *s13, *s2;
     int64_t s13_n, s13_k, s13_g, s2_n, s2_k, s2_g;
-    uint16_t* h;                           // [T * top_k][I] bf16
+    float* h;                              // [T * top_k][I]
+    float* o;                              // [T * top_k][H] the experts' outputs
     uint16_t* y;
     int64_t ld_y;
     int T, H, I, E, top_k;
     bool by_choice;                        // gate/up blocks go by choice, not by expert
 };
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const uint8_t* base, int64_t bytes) {
+    const uint64_t a = (uint64_t)base;  // wave-uniform: keep the descriptor in scalar registers
+    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) |
+                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) << 32;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
 
 // Writes the first `cap` choices of expert e from rank `first` on to list, and returns their total
 // number; one wave's work, in choice order.
@@ -222,218 +229,272 @@ __device__ __forceinline__ int choices_of(const int32_t* __restrict__ ids, int n
     return count;
 }
 
-// acc[ct][m] += rows of `wrow[ct]` times token rows `xrow[m]` over the 128-blocks kb0..kb1 of a
-// contraction of K values.  Token tiles at or past mt are left out (their rows are not read).
-template <int CT, int MT>
-__device__ __forceinline__ void stream_blocks(f4_t (&acc)[CT][MT], const uint8_t* const (&wrow)[CT], const float* const (&srow)[CT],
-                                              int64_t s_k, const uint16_t* const (&xrow)[MT], int mt, int K, int kb0, int kb1, int g) {
-    constexpr int U = MT == 1 ? 2 : 1;  // blocks whose loads are in flight together
-    for (int kb = kb0; kb < kb1; kb += U) {
-        uint4 w[U][CT][2];
-        float s[U][CT];
-#pragma unroll
-        for (int u = 0; u < U; u++)
-#pragma unroll
-            for (int c = 0; c < CT; c++) {
-                s[u][c] = 0.0f;
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    const int k = (kb + u) * MB + 64 * hf + 16 * g;
-                    w[u][c][hf] = make_uint4(0, 0, 0, 0);
-                    if (kb + u < kb1 && k < K && wrow[c]) w[u][c][hf] = ld_nt16(wrow[c] + k);
-                }
-                if (kb + u < kb1 && wrow[c]) s[u][c] = srow[c][(kb + u) * s_k];
-            }
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            bf8_t b[CT][4];
-#pragma unroll
-            for (int c = 0; c < CT; c++)
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    b[c][2 * hf] = widen8(w[u][c][hf].x, w[u][c][hf].y);
-                    b[c][2 * hf + 1] = widen8(w[u][c][hf].z, w[u][c][hf].w);
-                }
-#pragma unroll
-            for (int m = 0; m < MT; m++) {
-                if (m < mt) {
-                    uint4 a[4];
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const int k = (kb + u) * MB + 64 * (q >> 1) + 16 * g + 8 * (q & 1);
-                        a[q] = make_uint4(0, 0, 0, 0);
-                        if (kb + u < kb1 && k < K && xrow[m]) a[q] = *reinterpret_cast<const uint4*>(xrow[m] + k);
-                    }
-#pragma unroll
-                    for (int c = 0; c < CT; c++) {
-                        f4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int q = 0; q < 4; q++) d = mma(as_bf8(a[q]), b[c][q], d);
-#pragma unroll
-                        for (int i = 0; i < 4; i++) acc[c][m][i] = fmaf(d[i], s[u][c], acc[c][m][i]);
-                    }
-                }
-            }
-        }
-    }
-}
+#ifndef MOE_D
+#define MOE_D 2
+#endif
+constexpr int MOE_LDS = 64 * 1024;  // staged activations of a block: two blocks share a CU
 
-// h[a] = silu(G x) * (U x) for 16 columns of one expert and all its choices a.  The block's NW
-// waves split H; their sums meet in LDS.
-template <int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void moe_gate_up_kernel(const MoeArgs p) {
-    __shared__ f4_t red[NW][2][64];
+// One expert's product with its chosen tokens.  DOWN = false: h[a] = silu(G x) * (U x), a wave's two
+// weight tiles being 16 gate rows and the same 16 up rows; DOWN = true: o[a] = W2 h[a], two
+// neighbouring tiles of 16 rows.  A block's 8 waves are 8 / S such pairs times S parts of the
+// contraction, whose sums meet in LDS.
+//
+// A wave streams its 32 weight rows through registers, D contraction blocks (4 KB each) ahead of the
+// matrix instructions; the block's waves share the tokens' activations, staged in LDS a chunk of
+// contraction blocks at a time.  h is kept in 32 bits: it is staged as two bf16 halves, high and
+// low, and multiplied twice, since the matrix cores wait for memory anyway.
+template <int MT, int S, bool DOWN, int D>
+__global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
+    constexpr int PAIRS = 8 / S, PL = DOWN ? 2 : 1;
+    __shared__ __align__(16) uint8_t stage[MOE_LDS];
     __shared__ uint16_t list[16 * MT];
     __shared__ int s_n;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % S;
     const int n = p.T * p.top_k;
+    const int K = DOWN ? p.I : p.H, rows = DOWN ? p.H : p.I;  // multiples of 16
     int e = blockIdx.y;
     if (p.by_choice) {  // the first choice of an expert has its block, the others end here
         e = p.ids[blockIdx.y];
         if (e < 0 || e >= p.E) return;
         bool earlier = false;
-        for (int a = threadIdx.x; a < (int)blockIdx.y; a += 64 * NW) earlier |= p.ids[a] == e;
+        for (int a = threadIdx.x; a < (int)blockIdx.y; a += 512) earlier |= p.ids[a] == e;
         if (__syncthreads_or(earlier)) return;
     }
-    const int col = blockIdx.x * 16 + r;  // I is a multiple of 16
-    const uint8_t* wrow[2];
-    const float* srow[2];
-#pragma unroll
-    for (int c = 0; c < 2; c++) {
-        const int row = c * p.I + col;
-        wrow[c] = p.w13 + e * p.gs13 + row * p.ld13;
-        srow[c] = p.s13 + e * p.s13_g + (row / MB) * p.s13_n;
-    }
-    const int kbs = (p.H + MB - 1) / MB, kb0 = kbs * wave / NW, kb1 = kbs * (wave + 1) / NW;
+    // first row of each tile; a tile never straddles a factor block, so its factors are uniform
+    const int pair = blockIdx.x * PAIRS + wave / S;
+    const int row0 = DOWN ? 32 * pair : 16 * pair, row1 = DOWN ? row0 + 16 : p.I + row0;
+    const bool on0 = row0 < rows, on1 = DOWN ? row1 < rows : on0;
+    const uint8_t* w = DOWN ? p.w2 + e * p.gs2 : p.w13 + e * p.gs13;
+    const int64_t ld = DOWN ? p.ld2 : p.ld13;
+    // a tile's 16 rows as a buffer: a lane past K, or a tile past the last row, reads zeros
+    const __amdgpu_buffer_rsrc_t wbuf[2] = {tile_buffer(w + row0 * ld, on0 ? 15 * ld + K : 0),
+                                            tile_buffer(w + row1 * ld, on1 ? 15 * ld + K : 0)};
+    const uint32_t lane_off = (uint32_t)(r * ld) + 16 * g;
+    const bool on[2] = {on0, on1};
+    const float* s = DOWN ? p.s2 + e * p.s2_g : p.s13 + e * p.s13_g;
+    const int64_t s_n_ = DOWN ? p.s2_n : p.s13_n, s_k = DOWN ? p.s2_k : p.s13_k;
+    const float* srow[2] = {s + (row0 / MB) * s_n_, s + (row1 / MB) * s_n_};
+    const int kbs = (K + MB - 1) / MB, kb0 = kbs * part / S, len = kbs * (part + 1) / S - kb0;
+    const int most = (kbs + S - 1) / S;  // the longest part's blocks
+
     for (int first = 0;; first += 16 * MT) {
         if (wave == 0) {
             const int c = choices_of(p.ids, n, e, first, 16 * MT, list, lane);
             if (lane == 0) s_n = c;
         }
         __syncthreads();
-        const int left = s_n - first;
+        const int left = __builtin_amdgcn_readfirstlane(s_n) - first;
         if (left <= 0) return;
         const int mt = left >= 16 * MT ? MT : (left + 15) / 16;
-        const uint16_t* xrow[MT];
+        const int toks = left < 16 * MT ? left : 16 * MT;
+        // rows of the staged chunk: lanes past the last take any row, their results are not used
+        int lr = 2;
+        while ((1 << lr) < toks) lr++;
+        // contraction blocks of each part in a chunk: a power of two, D or more (see launch_stream)
+        int lc = 0;
+        while ((MOE_LDS >> (lc + 1 + lr + 8)) >= PL * S && (1 << lc) < most) lc++;
+        if ((1 << lc) < D) lc = D == 4 ? 2 : 1;
+
+        uint4 wv[D][2][2];
+        auto load = [&](int d, int i) {  // block i of the part into register set d
 #pragma unroll
-        for (int m = 0; m < MT; m++)
-            xrow[m] = 16 * m + r < left ? p.x + (list[16 * m + r] / p.top_k) * p.ld_x : nullptr;
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    const int k = (kb0 + i) * MB + 64 * hf;
+                    const uint32_t off = k + 16 * g < K && i < len ? lane_off + k : 0x80000000u;
+                    wv[d][c][hf] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf[c], off, 0, 0));
+                }
+        };
+        auto stage_chunk = [&](int i0) {  // blocks i0 .. of every part
+            __syncthreads();
+            const int per = 16 << lr, total = (S << lc) * per;  // 16-byte pieces: (part, block), row, piece
+#pragma unroll 1
+            for (int t = threadIdx.x; t < total; t += 512) {
+                const int ch = t & 15, row = (t >> 4) & ((1 << lr) - 1), bl = t >> (4 + lr);
+                const int pt = bl >> lc, i = i0 + (bl & ((1 << lc) - 1));
+                const int kb = kbs * pt / S + i, k = kb * MB + 8 * ch;
+                if (row >= toks || kb >= kbs) continue;
+                const int a = list[row];
+                uint8_t* dst = stage + (((bl * PL << lr) + row) << 8) + ((ch ^ (row & 15)) << 4);
+                if (!DOWN) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (k < K) v = *reinterpret_cast<const uint4*>(p.x + (a / p.top_k) * p.ld_x + k);
+                    *reinterpret_cast<uint4*>(dst) = v;
+                } else {
+                    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (k < K) {
+                        const f4_t* src = reinterpret_cast<const f4_t*>(p.h + (int64_t)a * p.I + k);
+                        const f4_t f0 = src[0], f1 = src[1];
+#pragma unroll
+                        for (int q = 0; q < 4; q++) {
+                            f[q] = f0[q];
+                            f[4 + q] = f1[q];
+                        }
+                    }
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int q = 0; q < 8; q++) {
+                        hi[q] = to_bf16(f[q]);
+                        const float rest = f[q] - __uint_as_float(hi[q] << 16);
+                        lo[q] = to_bf16(rest == rest ? rest : 0.0f);  // inf - inf
+                    }
+                    *reinterpret_cast<uint4*>(dst) =
+                        make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+                    *reinterpret_cast<uint4*>(dst + (256 << lr)) =
+                        make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+                }
+            }
+            __syncthreads();
+        };
+
         f4_t acc[2][MT];
 #pragma unroll
         for (int c = 0; c < 2; c++)
 #pragma unroll
             for (int m = 0; m < MT; m++) acc[c][m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        stream_blocks<2, MT>(acc, wrow, srow, p.s13_k, xrow, mt, p.H, kb0, kb1, g);
+        float sv[2] = {0.0f, 0.0f};  // lane l: factors of blocks 64 j + l of the part
 #pragma unroll
-        for (int m = 0; m < MT; m++) {
-            if (m < mt) {
-                red[wave][0][lane] = acc[0][m];
-                red[wave][1][lane] = acc[1][m];
-                __syncthreads();
-                // thread t < 256 adds element (lane t % 64, register t / 64) of all waves
-                for (int t = threadIdx.x; t < 256; t += 64 * NW) {
-                    const int l = t & 63, i = t >> 6, row = 16 * m + 4 * (l >> 4) + i;
-                    float a = 0.0f, b = 0.0f;
+        for (int d = 0; d < D; d++) load(d, d);
+        for (int i0 = 0; i0 < most; i0 += D) {
+            if ((i0 & ((1 << lc) - 1)) == 0) stage_chunk(i0);
+            if ((i0 & 63) == 0) {
 #pragma unroll
-                    for (int w = 0; w < NW; w++) {
-                        a += red[w][0][l][i];
-                        b += red[w][1][l][i];
+                for (int c = 0; c < 2; c++)
+                    sv[c] = on[c] && i0 + lane < len ? srow[c][(kb0 + i0 + lane) * s_k] : 0.0f;
+            }
+#pragma unroll
+            for (int d = 0; d < D; d++) {
+                const int i = i0 + d;
+                if (i >= len) break;
+                const int bl = (part << lc) + (i & ((1 << lc) - 1));
+                f4_t sum[2][MT];
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    bf8_t b[2][2];
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        b[c][0] = widen8(wv[d][c][hf].x, wv[d][c][hf].y);
+                        b[c][1] = widen8(wv[d][c][hf].z, wv[d][c][hf].w);
                     }
-                    // h is rounded to bf16, as activations between two layers are: the down
-                    // product's operand has to be bf16 for the matrix cores
-                    if (row < left)
-                        p.h[(int64_t)list[row] * p.I + blockIdx.x * 16 + (l & 15)] = to_bf16(a / (1.0f + expf(-a)) * b);
+#pragma unroll
+                    for (int m = 0; m < MT; m++) {
+                        if (m < mt) {
+                            const int row = (16 * m + r) & ((1 << lr) - 1);
+                            if (hf == 0) sum[0][m] = sum[1][m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int pl = 0; pl < PL; pl++) {
+                                const uint8_t* src = stage + ((((bl * PL + pl) << lr) + row) << 8);
+#pragma unroll
+                                for (int q = 0; q < 2; q++) {
+                                    const int ch = 8 * hf + 2 * g + q;
+                                    const bf8_t a = as_bf8(*reinterpret_cast<const uint4*>(src + ((ch ^ (row & 15)) << 4)));
+                                    sum[0][m] = mma(a, b[0][q], sum[0][m]);
+                                    sum[1][m] = mma(a, b[1][q], sum[1][m]);
+                                }
+                            }
+                        }
+                    }
                 }
-                __syncthreads();
+                load(d, i + D);
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sv[c]), i & 63));
+#pragma unroll
+                    for (int m = 0; m < MT; m++) {
+                        if (m < mt) {
+#pragma unroll
+                            for (int q = 0; q < 4; q++) acc[c][m][q] = fmaf(sum[c][m][q], f, acc[c][m][q]);
+                        }
+                    }
+                }
             }
         }
-        if (left <= 16 * MT) return;
-    }
-}
-
-// y[:, 16 columns] over all chosen experts.  Units of work (chosen expert, part of I) go to the
-// block's waves in turn; each wave has its own sums of all tokens in LDS, added at the end.
-template <int MT, int TMAX, int NW>
-__global__ __launch_bounds__(64 * NW) void moe_down_kernel(const MoeArgs p) {
-    __shared__ float ysum[NW][TMAX][16];
-    __shared__ uint16_t lists[NW][16 * MT];
-    __shared__ uint16_t s_active[MOE_MAX_E];
-    __shared__ uint8_t s_flag[MOE_MAX_E];
-    __shared__ int s_n;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 15, g = lane >> 4;
-    const int n = p.T * p.top_k;
-    for (int i = t; i < p.E; i += 64 * NW) s_flag[i] = 0;
-    for (int i = lane; i < p.T * 16; i += 64) (&ysum[wave][0][0])[i] = 0.0f;
-    __syncthreads();
-    for (int a = t; a < n; a += 64 * NW) {
-        const int e = p.ids[a];
-        if (e >= 0 && e < p.E) s_flag[e] = 1;
-    }
-    __syncthreads();
-    if (wave == 0) {
-        int c = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 64) {
-            const bool on = e0 + lane < p.E && s_flag[e0 + lane];
-            const uint64_t m = __ballot(on);
-            if (on) s_active[c + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(e0 + lane);
-            c += __popcll(m);
+        if (S > 1) {
+            f4_t* red = reinterpret_cast<f4_t*>(stage);  // [wave][tile][m][lane]
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int m = 0; m < MT; m++) red[((wave * 2 + c) * MT + m) * 64 + lane] = acc[c][m];
+            __syncthreads();
+            if (part == 0) {
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+#pragma unroll
+                    for (int m = 0; m < MT; m++)
+#pragma unroll
+                        for (int q = 1; q < S; q++) acc[c][m] += red[(((wave + q) * 2 + c) * MT + m) * 64 + lane];
+            }
         }
-        if (lane == 0) s_n = c;
-    }
-    __syncthreads();
-    const int active = s_n, kbs = (p.I + MB - 1) / MB;
-    // parts of I so that every wave has a unit
-    int parts = 1;
-    while (parts < NW && active * parts < NW && 2 * parts <= kbs) parts *= 2;
-    const int row = blockIdx.x * 16 + r;
-    uint16_t* list = lists[wave];
-    for (int u = wave; u < active * parts; u += NW) {
-        const int e = s_active[u / parts], part = u % parts;
-        const uint8_t* wrow[1] = {row < p.H ? p.w2 + e * p.gs2 + row * p.ld2 : nullptr};
-        const float* srow[1] = {p.s2 + e * p.s2_g + (row / MB) * p.s2_n};
-        const int kb0 = kbs * part / parts, kb1 = kbs * (part + 1) / parts;
-        for (int first = 0;; first += 16 * MT) {
-            const int left = choices_of(p.ids, n, e, first, 16 * MT, list, lane) - first;
-            if (left <= 0) break;
-            const int mt = left >= 16 * MT ? MT : (left + 15) / 16;
-            const uint16_t* xrow[MT];
-#pragma unroll
-            for (int m = 0; m < MT; m++) xrow[m] = 16 * m + r < left ? p.h + (int64_t)list[16 * m + r] * p.I : nullptr;
-            f4_t acc[1][MT];
-#pragma unroll
-            for (int m = 0; m < MT; m++) acc[0][m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-            stream_blocks<1, MT>(acc, wrow, srow, p.s2_k, xrow, mt, p.I, kb0, kb1, g);
+        if (part == 0) {
 #pragma unroll
             for (int m = 0; m < MT; m++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int at = 16 * m + 4 * g + i;
-                    if (at < left) {
-                        const int a = list[at];
-                        // one wave owns these sums; an LDS addition, because a token may be listed
-                        // twice for one expert and then two lanes meet here
-                        atomicAdd(&ysum[wave][a / p.top_k][r], p.weights[a] * acc[0][m][i]);
+                    if (at < toks) {
+                        const int64_t a = list[at];
+                        const float u = acc[0][m][i], v = acc[1][m][i];
+                        if (!DOWN) {
+                            if (on0) p.h[a * p.I + row0 + r] = u / (1.0f + expf(-u)) * v;
+                        } else {
+                            if (on0) p.o[a * p.H + row0 + r] = u;
+                            if (on1) p.o[a * p.H + row1 + r] = v;
+                        }
                     }
                 }
-            if (left <= 16 * MT) break;
         }
-    }
-    __syncthreads();
-    for (int i = t; i < p.T * 16; i += 64 * NW) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < NW; w++) s += (&ysum[w][0][0])[i];
-        const int c = blockIdx.x * 16 + (i & 15);
-        if (c < p.H) p.y[(i >> 4) * p.ld_y + c] = to_bf16(s);
+        if (left <= 16 * MT) return;
+        __syncthreads();  // the list is written again
     }
 }
 
-template <int MT, int TMAX>
+// y[t] = sum_j weights[t,j] o[t,j], in order of j; 4 columns a thread.
+__global__ __launch_bounds__(256) void moe_join_kernel(const MoeArgs p) {
+    const int64_t n4 = (int64_t)p.T * p.H / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    const int64_t t = i * 4 / p.H, c = i * 4 - t * p.H;
+    f4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < p.top_k; j++) {
+        const int64_t a = t * p.top_k + j;
+        const int e = p.ids[a];
+        if (e < 0 || e >= p.E) continue;
+        const f4_t o = *reinterpret_cast<const f4_t*>(p.o + a * p.H + c);
+        const float w = p.weights[a];
+#pragma unroll
+        for (int q = 0; q < 4; q++) s[q] = fmaf(w, o[q], s[q]);
+    }
+    uint16_t* y = p.y + t * p.ld_y + c;
+#pragma unroll
+    for (int q = 0; q < 4; q++) y[q] = to_bf16(s[q]);
+}
+
+template <int MT, bool DOWN>
+static void launch_stream(const MoeArgs& p, hipStream_t stream) {
+    const int n = p.T * p.top_k, experts = n < p.E ? n : p.E;
+    const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
+    // parts of the contraction: 16 waves for every CU, each with 4 blocks or more; D blocks of every
+    // part have to fit the staging buffer: 2^8 bytes a row and plane, 16 MT rows
+    constexpr int D = MOE_D, most = MOE_LDS / (256 * 16 * MT * (DOWN ? 2 : 1) * D) < 8 ? MOE_LDS / (256 * 16 * MT * (DOWN ? 2 : 1) * D) : 8;
+    static_assert(most >= 1, "a chunk of D blocks fits");
+    int S = 1;
+    while (S < most && experts * pairs * S < 4096 && kbs >= 8 * S) S *= 2;
+    const dim3 grid((unsigned)((pairs * S + 7) / 8), (unsigned)(p.by_choice ? n : p.E)), block(512);
+    if (S == 1) moe_stream_kernel<MT, 1, DOWN, D><<<grid, block, 0, stream>>>(p);
+    else if (S == 2) moe_stream_kernel<MT, most < 2 ? most : 2, DOWN, D><<<grid, block, 0, stream>>>(p);
+    else if (S == 4) moe_stream_kernel<MT, most < 4 ? most : 4, DOWN, D><<<grid, block, 0, stream>>>(p);
+    else moe_stream_kernel<MT, most, DOWN, D><<<grid, block, 0, stream>>>(p);
+}
+
+template <int MT>
 static fp8q_status_t launch_moe(const MoeArgs& p, hipStream_t stream) {
-    const int n = p.T * p.top_k;
-    moe_gate_up_kernel<MT, 8><<<dim3((unsigned)(p.I / 16), (unsigned)(p.by_choice ? n : p.E)), dim3(512), 0, stream>>>(p);
+    launch_stream<MT, false>(p, stream);
     FP8Q_CHECK_LAUNCH();
-    moe_down_kernel<MT, TMAX, 8><<<dim3((unsigned)((p.H + 15) / 16)), dim3(512), 0, stream>>>(p);
+    launch_stream<MT, true>(p, stream);
+    FP8Q_CHECK_LAUNCH();
+    moe_join_kernel<<<dim3((unsigned)(((int64_t)p.T * p.H / 4 + 255) / 256)), dim3(256), 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
@@ -483,9 +544,10 @@ extern "C" fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int6
     return FP8Q_OK;
 }
 
-extern "C" size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t I, int32_t top_k) {
-    if (T <= 0 || I <= 0 || top_k <= 0) return 256;
-    return (size_t)T * (size_t)top_k * (size_t)I * 2;
+// Workspace: h, then the experts' outputs, both 32-bit.
+extern "C" size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t H, int64_t I, int32_t top_k) {
+    if (T <= 0 || H <= 0 || I <= 0 || top_k <= 0) return 256;
+    return (size_t)T * (size_t)top_k * (size_t)(I + H) * 4;
 }
 
 extern "C" fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, const int32_t* ids,
@@ -502,19 +564,18 @@ extern "C" fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_
         return FP8Q_ERR_INVALID_ARG;
     if (T == 0) return FP8Q_OK;
     if (!x || !ids || !weights || !w13 || !s13 || !w2 || !s2 || !y) return FP8Q_ERR_INVALID_ARG;
-    if (T > MOE_MAX_T || E > MOE_MAX_E || top_k > MOE_MAX_K || H % 16 || I % 16 || H > 0x3FFFFFFF || I > 0x3FFFFFFF ||
-        ld_x % 8 || ld13 % 16 || ld2 % 16 || w13_group_stride % 16 || w2_group_stride % 16 || !fp8q_aligned(x, 16) ||
+    if (T > MOE_MAX_T || E > MOE_MAX_E || top_k > MOE_MAX_K || H % 16 || I % 16 || H > 0x3FFFFFFF || I > 0x3FFFFFFF || ld13 >= (1 << 26) ||
+        ld2 >= (1 << 26) || ld_x % 8 || ld13 % 16 || ld2 % 16 || w13_group_stride % 16 || w2_group_stride % 16 || !fp8q_aligned(x, 16) ||
         !fp8q_aligned(w13, 16) || !fp8q_aligned(w2, 16))
         return FP8Q_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < fp8_moe_few_tokens_workspace_size(T, I, top_k)) return FP8Q_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < fp8_moe_few_tokens_workspace_size(T, H, I, top_k)) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     MoeArgs p{};
     p.x = x; p.ld_x = ld_x; p.ids = ids; p.weights = weights; p.w13 = w13; p.w2 = w2; p.ld13 = ld13; p.gs13 = w13_group_stride;
     p.ld2 = ld2; p.gs2 = w2_group_stride; p.s13 = s13; p.s2 = s2; p.s13_n = s13_n; p.s13_k = s13_k; p.s13_g = s13_group_stride;
-    p.s2_n = s2_n; p.s2_k = s2_k; p.s2_g = s2_group_stride; p.h = reinterpret_cast<uint16_t*>(workspace); p.y = y; p.ld_y = ld_y;
+    p.s2_n = s2_n; p.s2_k = s2_k; p.s2_g = s2_group_stride; p.h = reinterpret_cast<float*>(workspace);
+    p.o = p.h + T * top_k * I; p.y = y; p.ld_y = ld_y;
     p.T = (int)T; p.H = (int)H; p.I = (int)I; p.E = (int)E; p.top_k = top_k;
     p.by_choice = T * top_k < E;
-    if (T <= 16) return launch_moe<1, 16>(p, stream);
-    if (T <= 64) return launch_moe<2, 64>(p, stream);
-    return launch_moe<2, MOE_MAX_T>(p, stream);
+    return T <= 16 ? launch_moe<1>(p, stream) : launch_moe<2>(p, stream);
 }

@@ -424,20 +424,21 @@ fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, c
                         void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* fp8_moe_few_tokens: for every token t
- *   y[t] = sum_j weights[t,j] * W2_e h,  h = bf16( silu(G_e x_t) * (U_e x_t) ),  e = ids[t,j]
+ *   y[t] = sum_j weights[t,j] * W2_e (silu(G_e x_t) * (U_e x_t)),  e = ids[t,j]
  * with e4m3fn weights in blocks of 128 x 128 (fp8_block_quant_weights): [G_e; U_e] = w13[e] is
- * 2I x H (gate rows first), W2_e = w2[e] is H x I.  Activations stay bf16; sums are fp32.  An id
+ * 2I x H (gate rows first), W2_e = w2[e] is H x I.  Nothing is quantized: x stays bf16, and what lies
+ * between the two products and all sums are fp32 (or two bf16 halves of it).  An id
  * outside [0, E) adds nothing (an expert that lives elsewhere); a token with none gives zeros.
  *   x bf16 [T][ld_x >= H]; ids int32, weights fp32 [T][top_k]
  *   w13 rows at stride ld13 >= H, experts at w13_group_stride; w2 rows at ld2 >= I
  *   s13, s2 fp32: the factor of row n and column k of expert e is
  *     s[e*group_stride + (n/128)*s_n + (k/128)*s_k]
- *   y bf16 [T][ld_y >= H]; workspace fp8_moe_few_tokens_workspace_size bytes (h), any content,
+ *   y bf16 [T][ld_y >= H]; workspace fp8_moe_few_tokens_workspace_size bytes, any content,
  *   16-byte aligned.
- * Two kernels; every sum has a fixed order.  Limits (FP8Q_ERR_UNSUPPORTED): T <= 128 (the grouped
+ * Three kernels; every sum has a fixed order.  Limits (FP8Q_ERR_UNSUPPORTED): T <= 128 (the grouped
  * product takes more), E <= 1024, top_k <= 32, H and I multiples of 16, ld_x a multiple of 8, the
  * weights' strides multiples of 16, x, w13 and w2 16-byte aligned.  T == 0 is a no-op. */
-size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t I, int32_t top_k);
+size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t H, int64_t I, int32_t top_k);
 fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x,
                                  const int32_t* ids, const float* weights, int32_t top_k,
                                  const uint8_t* w13, int64_t ld13, int64_t w13_group_stride,
