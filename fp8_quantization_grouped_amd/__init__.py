@@ -405,17 +405,24 @@ def _want(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _rows_of(t: torch.Tensor, what: str, dtypes, shape=None, dev=None) -> torch.Tensor:
-    """t as a device tensor of one of dtypes with unit stride in its last dimension, rows that do
-    not overlap, and the given shape (None: any size) on device dev."""
-    _want(t.is_cuda and (dev is None or t.device == dev), f"{what} must be on the operands' GPU")
+def _rows_of(t: torch.Tensor, what: str, dtypes, shape, dev) -> None:
+    """Checks that t is a tensor on device dev of one of dtypes and of the given shape, with unit
+    stride in its last dimension."""
+    if (t.dtype in dtypes and t.device == dev and t.shape == shape
+            and (t.stride(-1) == 1 or t.shape[-1] <= 1) and dev.type == "cuda"):
+        return
+    _want(t.is_cuda and t.device == dev, f"{what} must be on the operands' GPU")
     _want(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
-    if shape is not None:
-        _want(len(shape) == t.dim() and all(n is None or n == m for n, m in zip(shape, t.shape)),
-              f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    _want(t.dim() < 1 or t.shape[-1] <= 1 or t.stride(-1) == 1,
-          f"{what} must have unit stride in its last dimension")
-    return t
+    _want(t.shape == shape, f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{what} must have unit stride in its last dimension")
+
+
+def _matrix(t: torch.Tensor, what: str, dtypes) -> torch.Size:
+    """Checks the first operand of a call, a matrix of any size; returns its shape."""
+    _want(t.dim() == 2, f"{what} must be a matrix")
+    shape = t.shape
+    _rows_of(t, what, dtypes, shape, t.device)
+    return shape
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -424,13 +431,21 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if rows > 1 and cols > 0 else 0 if cols == 0 else max(t.stride(0), cols)
 
 
+# the current stream's handle without a Stream object made for it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(name: str, dev: torch.device, *args) -> None:
     """The C entry point on the current stream of dev, with dev the current device."""
-    if dev.index == torch.cuda.current_device():
-        _check(name, getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream))
+    index = dev.index
+    if index == torch.cuda.current_device():
+        status = getattr(_lib or lib(), name)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            _check(name, getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream))
+            status = getattr(_lib or lib(), name)(*args, _raw_stream(index))
+    if status:
+        _check(name, status)
 
 
 def _blocks(n: int) -> int:
@@ -445,15 +460,23 @@ def _padded_bytes(rows: int, cols: int, dev) -> torch.Tensor:
 _BF16, _F32, _I32T = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 
 
+def _factors(s: torch.Tensor, what: str, shape, dev) -> None:
+    """Checks block factors, of any strides."""
+    if s.dtype is not torch.float32 or s.device != dev or s.shape != shape:
+        raise ValueError(f"{what} must be float32 {shape} on the operands' GPU")
+
+
 def fp8_block_quant_rowwise(x: torch.Tensor, q: torch.Tensor | None = None,
                             scales: torch.Tensor | None = None):
     """x: bf16 [rows, cols] in blocks of 1 x 128.  Returns (q [rows, cols] e4m3fn bytes, scales
     float32 [ceil(cols/128), rows], the factors d with x ~ q * d).  Rows of a new q start on 16
     bytes."""
-    _rows_of(x, "x", _BF16, (None, None))
-    rows, cols = x.shape
+    rows, cols = _matrix(x, "x", _BF16)
     dev = x.device
-    q = _padded_bytes(rows, cols, dev) if q is None else _rows_of(q, "q", _BYTES, x.shape, dev)
+    if q is None:
+        q = _padded_bytes(rows, cols, dev)
+    else:
+        _rows_of(q, "q", _BYTES, x.shape, dev)
     if scales is None:
         scales = torch.empty((_blocks(cols), rows), dtype=torch.float32, device=dev)
     else:
@@ -470,15 +493,17 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
     [ceil(cols/128), rows]) as fp8_block_quant_rowwise would, (q_t [cols, rows], s_cols float32
     [ceil(rows/128), cols]) in blocks of 128 rows of a column).  transposed_only: the second pair
     alone is made, and the first is (None, None)."""
-    _rows_of(x, "x", _BF16, (None, None))
-    rows, cols = x.shape
+    rows, cols = _matrix(x, "x", _BF16)
     dev = x.device
     f32 = torch.float32
     if transposed_only:
         _want(q is None and s_rows is None, "transposed_only takes no q and s_rows")
         row_args = (None, 0, None, 0)
     else:
-        q = _padded_bytes(rows, cols, dev) if q is None else _rows_of(q, "q", _BYTES, x.shape, dev)
+        if q is None:
+            q = _padded_bytes(rows, cols, dev)
+        else:
+            _rows_of(q, "q", _BYTES, x.shape, dev)
         if s_rows is None:
             s_rows = torch.empty((_blocks(cols), rows), dtype=f32, device=dev)
         else:
@@ -502,11 +527,14 @@ def fp8_block_quant_weights(w: torch.Tensor, experts: int, q: torch.Tensor | Non
     """w: bf16 [experts * rows, cols], each expert's matrix in blocks of 128 x 128.  Returns (q
     [experts * rows, cols], q_t [cols, experts * rows] with the experts' transposes side by side,
     scales float32 [experts, ceil(rows/128), ceil(cols/128)], which serve both)."""
-    _rows_of(w, "w", _BF16, (None, None))
+    _matrix(w, "w", _BF16)
     _want(experts > 0 and w.shape[0] % experts == 0, "w must hold experts matrices of equal size")
     rows, cols = w.shape[0] // experts, w.shape[1]
     dev = w.device
-    q = _padded_bytes(*w.shape, dev) if q is None else _rows_of(q, "q", _BYTES, w.shape, dev)
+    if q is None:
+        q = _padded_bytes(*w.shape, dev)
+    else:
+        _rows_of(q, "q", _BYTES, w.shape, dev)
     if q_t is None:
         q_t = _padded_bytes(cols, w.shape[0], dev)
     else:
@@ -537,21 +565,21 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
     from a given workspace."""
     _want(mode in (GEMM_FWD_MGROUPED, GEMM_WGRAD_KGROUPED), "unknown mode")
     fwd = mode == GEMM_FWD_MGROUPED
-    _rows_of(a, "a", _BYTES, (None, None))
+    rows, inner = _matrix(a, "a", _BYTES)  # forward M, K; weight gradient K, M
     dev = a.device
-    rows, inner = a.shape  # forward M, K; weight gradient K, M
+    groups = 1
     if offsets is not None:
-        _rows_of(offsets, "offsets", _I32T, (None,), dev)
-    groups = 1 if offsets is None else offsets.shape[0]
-    _rows_of(b, "b", _BYTES, (groups, None, inner) if fwd else (None, inner), dev)
+        _want(offsets.dim() == 1, "offsets must have one dimension")
+        groups = offsets.shape[0]
+        _rows_of(offsets, "offsets", _I32T, (groups,), dev)
+    _want(b.dim() == (3 if fwd else 2), "b must be [groups, N, K] in the forward, [N, M] else")
     N = b.shape[-2]
+    _rows_of(b, "b", _BYTES, (groups, N, inner) if fwd else (N, inner), dev)
     kb = _blocks(inner)
     _rows_of(a_scales, "a_scales", _F32, (kb, rows), dev)
     lda, ld_sa = _ld(a), max(_ld(a_scales), rows) if kb else rows
     if fwd:
-        _want(b_scales.device == dev and b_scales.dtype == torch.float32
-              and tuple(b_scales.shape) == (groups, _blocks(N), kb),
-              f"b_scales must be float32 {(groups, _blocks(N), kb)} on the operands' GPU")
+        _factors(b_scales, "b_scales", (groups, _blocks(N), kb), dev)
         # a dimension of one entry has no stride that means anything
         bgs = b.stride(0) if groups > 1 else 0
         ldb = b.stride(1) if N > 1 else max(b.stride(1), inner)
@@ -562,9 +590,11 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
         bgs, ldb, sbg, sbn, sbk = 0, _ld(b), 0, 1, max(_ld(b_scales), N) if kb else N
         M, K, shape = inner, rows, (groups, rows, N)
     if c is None:
+        _want(out_dtype in _OUT, "the output must be bfloat16 or float32")
         c = torch.empty(shape, dtype=out_dtype, device=dev)
-    c = _gemm_out(c, shape, out_dtype, dev)
-    _want(c.device == dev, "c must be on the operands' GPU")
+    else:
+        c = _gemm_out(c, shape, out_dtype, dev)
+        _want(c.device == dev, "c must be on the operands' GPU")
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     _call("fp8_block_grouped_gemm", dev, mode, a.data_ptr(), lda, a_scales.data_ptr(), ld_sa,
           b.data_ptr(), ldb, bgs, b_scales.data_ptr(), sbn, sbk, sbg,
@@ -591,11 +621,10 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     """The experts of each token: x bf16 [T, H], router bf16 [E, H], bias float32 [E] (added to the
     scores for the choice alone).  scoring: "softmax" or "sigmoid".  Returns (ids int32 [T, top_k],
     weights float32 [T, top_k]) in descending order; ties go to the lowest index."""
-    _rows_of(x, "x", _BF16, (None, None))
+    T, H = _matrix(x, "x", _BF16)
     dev = x.device
-    T, H = x.shape
-    _rows_of(router, "router", _BF16, (None, H), dev)
     E = router.shape[0]
+    _rows_of(router, "router", _BF16, (E, H), dev)
     _want(scoring in _SCORING, "scoring must be softmax or sigmoid")
     _want(1 <= top_k <= E, "top_k must lie in [1, number of experts]")
     if bias is not None:
@@ -603,12 +632,13 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     if ids is None:
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     else:
-        _want(_rows_of(ids, "ids", _I32T, (T, top_k), dev).is_contiguous(), "ids must be contiguous")
+        _rows_of(ids, "ids", _I32T, (T, top_k), dev)
+        _want(ids.is_contiguous(), "ids must be contiguous")
     if weights is None:
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     else:
-        _want(_rows_of(weights, "weights", _F32, (T, top_k), dev).is_contiguous(),
-              "weights must be contiguous")
+        _rows_of(weights, "weights", _F32, (T, top_k), dev)
+        _want(weights.is_contiguous(), "weights must be contiguous")
     if workspace is None:
         workspace = torch.empty((moe_route_workspace_size(T, H, E),), dtype=torch.uint8, device=dev)
     _call("moe_route", dev, x.data_ptr(), T, H, _ld(x), router.data_ptr(), E, _ld(router),
@@ -624,9 +654,8 @@ def fp8_moe_few_tokens_workspace_size(T: int, H: int, I: int, top_k: int) -> int
 def _expert_weights(w, s, what, shape, dev):
     """The pointers and strides of block-scaled expert weights, as the C entry point takes them."""
     _rows_of(w, what, _BYTES, shape, dev)
-    E, n, k = w.shape
-    _want(s.device == dev and s.dtype == torch.float32 and tuple(s.shape) == (E, _blocks(n), _blocks(k)),
-          f"{what}'s scales must be float32 {(E, _blocks(n), _blocks(k))} on the operands' GPU")
+    E, n, k = shape
+    _factors(s, f"the factors of {what}", (E, _blocks(n), _blocks(k)), dev)
     sg, sn, sk = (d if m > 1 else 0 for d, m in zip(s.stride(), s.shape))
     return (w.data_ptr(), w.stride(1) if n > 1 else max(w.stride(1), k), w.stride(0) if E > 1 else 0,
             s.data_ptr(), sn, sk, sg)
@@ -639,13 +668,13 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     weights float32 [T, top_k] (moe_route's); w13 [E, 2I, H] and w2 [E, H, I] e4m3fn bytes with
     scales [E, ceil(2I/128), ceil(H/128)] and [E, ceil(H/128), ceil(I/128)]
     (fp8_block_quant_weights').  Returns y bf16 [T, H].  An id outside [0, E) adds nothing."""
-    _rows_of(x, "x", _BF16, (None, None))
+    T, H = _matrix(x, "x", _BF16)
     dev = x.device
-    T, H = x.shape
-    _want(_rows_of(ids, "ids", _I32T, (T, None), dev).is_contiguous(), "ids must be contiguous")
+    _want(ids.dim() == 2, "ids must be a matrix")
     top_k = ids.shape[1]
-    _want(_rows_of(weights, "weights", _F32, (T, top_k), dev).is_contiguous(),
-          "weights must be contiguous")
+    _rows_of(ids, "ids", _I32T, (T, top_k), dev)
+    _rows_of(weights, "weights", _F32, (T, top_k), dev)
+    _want(ids.is_contiguous() and weights.is_contiguous(), "ids and weights must be contiguous")
     _want(w13.dim() == 3 and w13.shape[1] % 2 == 0, "w13 must be [E, 2I, H]")
     E, I = w13.shape[0], w13.shape[1] // 2
     args13 = _expert_weights(w13, s13, "w13", (E, 2 * I, H), dev)

@@ -55,12 +55,12 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "lds_dma.hpp"
 
 namespace fp8q {
 
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef float v4f_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int GT = 256;         // output tile edge (rows and columns)
 
@@ -83,42 +83,6 @@ __device__ __forceinline__ int lds_offB(int r, int ch) { return r * GK + ((ch ^ 
 // Row of the N-side tile that feeds MFMA row lr of column block j (see swzB).
 __device__ __forceinline__ int brow(int j, int lr) {
     return 32 * (j >> 1) + 8 * (lr >> 2) + 4 * (j & 1) + (lr & 3);
-}
-
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ i32x4_t make_rsrc4(const void* base, uint32_t bytes) {
-    const uint64_t a = (uint64_t)base;  // block-uniform: keep the descriptor in SGPRs
-    return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-                   __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
-                   __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
-}
-// 16 bytes per lane from a buffer straight into LDS at lds_base + 16*lane (lds_base is
-// wave-uniform).  Written as inline assembly so that the compiler does not order every later
-// LDS read after it: the waits are explicit (s_waitcnt vmcnt before the step's barrier).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t voff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds_base), "v"(voff), "s"(rsrc)
-                 : "memory", "m0");
-}
-#pragma clang diagnostic pop
-__device__ __forceinline__ void dma4(i32x4_t rsrc, uint32_t voff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds_base), "v"(voff), "s"(rsrc)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void wait_vm0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)p);
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
-                                             0x00020000);
 }
 
 // e4m3fnuz byte -> e4m3fn byte of the same value (four bytes at a time).

@@ -19,6 +19,7 @@
 // Every sum has a fixed order: a contraction's parts are added in wave order, a token's experts in
 // the order of its choices.
 #include "common.hpp"
+#include "lds_dma.hpp"
 
 namespace fp8q {
 
@@ -29,6 +30,7 @@ typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 constexpr int MB = 128;           // weight factor block
 constexpr int MOE_MAX_T = 128;    // tokens of one call
 constexpr int MOE_MAX_E = 1024;   // experts
+constexpr uint32_t OOB = 0x80000000u;  // past any buffer: the load gives zeros
 constexpr int MOE_MAX_K = 32;     // experts of one token
 
 // 8 e4m3fn bytes as bf16 (exact: 4 significant bits, exponents -9 .. 8).
@@ -67,20 +69,28 @@ struct RouteArgs {
 // Partial logits of 16 tokens x 16 experts over one split of H; the block's 4 waves share the split.
 __global__ __launch_bounds__(256) void route_logits_kernel(const RouteArgs p) {
     __shared__ f4_t red[4][64];
+    constexpr int U = 4;  // chunks whose loads are in flight together
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int e = blockIdx.x * 16 + r, t = blockIdx.z * 16 + r;
     const int chunks = (p.H + 31) / 32;                          // 32 k values of one instruction
     const int parts = p.splits * 4, me = blockIdx.y * 4 + wave;  // waves over H
     const int k0 = (int)((int64_t)chunks * me / parts), k1 = (int)((int64_t)chunks * (me + 1) / parts);
+    const uint16_t* xr = p.x + (t < p.T ? t : 0) * p.ld_x;
+    const uint16_t* wr = p.router + (e < p.E ? e : 0) * p.ld_r;  // rows past the last: results not used
     f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kc = k0; kc < k1; kc++) {
-        const int k = kc * 32 + 8 * g;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (k < p.H) {  // H is a multiple of 8
-            if (t < p.T) a = *reinterpret_cast<const uint4*>(p.x + t * p.ld_x + k);
-            if (e < p.E) b = *reinterpret_cast<const uint4*>(p.router + e * p.ld_r + k);
+    for (int kc = k0; kc < k1; kc += U) {
+        uint4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int k = (kc + u) * 32 + 8 * g;
+            a[u] = b[u] = make_uint4(0, 0, 0, 0);
+            if (kc + u < k1 && k < p.H) {  // H is a multiple of 8
+                a[u] = *reinterpret_cast<const uint4*>(xr + k);
+                b[u] = *reinterpret_cast<const uint4*>(wr + k);
+            }
         }
-        acc = mma(as_bf8(a), as_bf8(b), acc);
+#pragma unroll
+        for (int u = 0; u < U; u++) acc = mma(as_bf8(a[u]), as_bf8(b[u]), acc);
     }
     red[wave][lane] = acc;
     __syncthreads();
@@ -94,12 +104,97 @@ __global__ __launch_bounds__(256) void route_logits_kernel(const RouteArgs p) {
     }
 }
 
+// Scores, choice and weights of one token from its logits in LDS, by a whole block of at least E
+// threads: an expert's place is the number of experts that go before it.
+__device__ __forceinline__ void choose(const RouteArgs& p, int64_t t, const float* logit, float* by, float* chosen) {
+    const int e = threadIdx.x;
+    const float l = e < p.E ? logit[e] : 0.0f;
+    float score = 1.0f / (1.0f + expf(-l));
+    if (!p.sigmoid) {
+        float top = -INFINITY;
+        for (int j = 0; j < p.E; j++) top = fmaxf(top, logit[j]);
+        score = expf(l - top);
+        if (e < p.E) by[e] = score;
+        __syncthreads();
+        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // four sums in turn
+        for (int j = 0; j < p.E; j++) s4[j & 3] += by[j];
+        score /= (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        __syncthreads();
+    }
+    if (e < p.E) {
+        // without a bias the logits give the same order, and no ties that the scores' rounding makes
+        const float v = p.bias ? score + p.bias[e] : l;
+        by[e] = v == v ? v : -INFINITY;  // NaN goes last
+    }
+    __syncthreads();
+    int place = p.top_k;
+    if (e < p.E) {
+        const float v = by[e];
+        place = 0;
+        for (int j = 0; j < p.E; j++) place += by[j] > v || (by[j] == v && j < e);
+        if (place < p.top_k) chosen[place] = score;
+    }
+    __syncthreads();
+    if (place < p.top_k) {
+        float total = 0.0f;
+        for (int j = 0; j < p.top_k; j++) total += chosen[j];
+        // a sum that vanished (every chosen score underflowed) gives zeros, not 0 / 0; fmaxf drops
+        // a NaN: keep it visible
+        const float w = p.renorm ? score / fmaxf(total, 1e-30f) : score;
+        p.ids[t * p.top_k + place] = e;
+        p.weights[t * p.top_k + place] = (total == total ? w : total) * p.scale;
+    }
+}
+
+__global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs p) {
+    __shared__ float logit[256], by[256], chosen[MOE_MAX_K];
+    const int64_t t = blockIdx.x;
+    const int e = threadIdx.x;
+    if (e < p.E) {
+        float part[16], l = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 16; s++) part[s] = s < p.splits ? p.part[((int64_t)s * p.T + t) * p.E + e] : 0.0f;
+#pragma unroll
+        for (int s = 0; s < 16; s++) l += part[s];
+        logit[e] = l;
+    }
+    __syncthreads();
+    choose(p, t, logit, by, chosen);
+}
+
+// Small routers in one kernel: a block of 16 waves per token, each wave an expert at a time.
+__global__ __launch_bounds__(1024) void route_small_kernel(const RouteArgs p) {
+    __shared__ float logit[256], by[256], chosen[MOE_MAX_K];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint16_t* xr = p.x + t * p.ld_x;
+    for (int e = wave; e < p.E; e += 16) {
+        const uint16_t* wr = p.router + e * p.ld_r;
+        float acc = 0.0f;
+        for (int k = lane * 8; k < p.H; k += 512) {
+            const uint4 a = *reinterpret_cast<const uint4*>(xr + k), b = *reinterpret_cast<const uint4*>(wr + k);
+            const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                acc = fmaf(bf16_lo(u[q]), bf16_lo(v[q]), acc);
+                acc = fmaf(bf16_hi(u[q]), bf16_hi(v[q]), acc);
+            }
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
+        if (lane == 0) logit[e] = acc;
+    }
+    __syncthreads();
+    choose(p, t, logit, by, chosen);
+}
+
 // Order of choice: NaN last, then by value; the lower index wins a tie.
 __device__ __forceinline__ bool goes_before(float a, int ia, float b, int ib) {
     return a > b || (a == b && ia < ib);
 }
 
-// One wave per token: scores, top_k rounds of a wave-wide maximum, weights.
+// More experts: one wave per token, top_k rounds of a wave-wide maximum (the places above cost E^2
+// comparisons).
 template <int NV>  // experts per lane
 __global__ __launch_bounds__(64) void route_select_kernel(const RouteArgs p) {
     const int lane = threadIdx.x;
@@ -197,11 +292,12 @@ struct MoeArgs {
     int64_t ld13, gs13, ld2, gs2;          // strides of rows and experts, bytes
     const float *s13, *s2;
     int64_t s13_n, s13_k, s13_g, s2_n, s2_k, s2_g;
-    float* h;                              // [T * top_k][I]
+    uint16_t* h;                           // two planes of [T * top_k][I]: bf16 and what it leaves
     float* o;                              // [T * top_k][H] the experts' outputs
     uint16_t* y;
     int64_t ld_y;
     int T, H, I, E, top_k;
+    int pass;                              // tokens of an expert that one pass takes: a power of two
     bool by_choice;                        // gate/up blocks go by choice, not by expert
 };
 
@@ -212,27 +308,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const uint8_t* bas
     return __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
 
-// Writes the first `cap` choices of expert e from rank `first` on to list, and returns their total
-// number; one wave's work, in choice order.
-__device__ __forceinline__ int choices_of(const int32_t* __restrict__ ids, int n, int e, int first, int cap,
-                                          uint16_t* list, int lane) {
+// put(i, a) for the choices a of expert e with ranks first + i, i < cap, in choice order; returns how
+// many there are in all.  One wave's work.
+template <class F>
+__device__ __forceinline__ int choices_of(const int32_t* __restrict__ ids, int n, int e, int first, int cap, int lane, F put) {
     int count = 0;
     for (int a0 = 0; a0 < n; a0 += 64) {
         const int a = a0 + lane;
         const bool hit = a < n && ids[a] == e;
         const uint64_t m = __ballot(hit);
         const int rank = count + __popcll(m & ((1ull << lane) - 1)) - first;
-        if (hit && rank >= 0 && rank < cap) list[rank] = (uint16_t)a;
+        if (hit && rank >= 0 && rank < cap) put(rank, a);
         count += __popcll(m);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's lanes read each other's entries
     return count;
 }
 
-#ifndef MOE_D
-#define MOE_D 2
-#endif
-constexpr int MOE_LDS = 64 * 1024;  // staged activations of a block: two blocks share a CU
+constexpr int moe_lds(int nw) { return 8192 * nw; }  // staged activations of a block: 16 waves share a CU
 
 // One expert's product with its chosen tokens.  DOWN = false: h[a] = silu(G x) * (U x), a wave's two
 // weight tiles being 16 gate rows and the same 16 up rows; DOWN = true: o[a] = W2 h[a], two
@@ -240,26 +332,25 @@ constexpr int MOE_LDS = 64 * 1024;  // staged activations of a block: two blocks
 // contraction, whose sums meet in LDS.
 //
 // A wave streams its 32 weight rows through registers, D contraction blocks (4 KB each) ahead of the
-// matrix instructions; the block's waves share the tokens' activations, staged in LDS a chunk of
-// contraction blocks at a time.  h is kept in 32 bits: it is staged as two bf16 halves, high and
-// low, and multiplied twice, since the matrix cores wait for memory anyway.
-template <int MT, int S, bool DOWN, int D>
-__global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
-    constexpr int PAIRS = 8 / S, PL = DOWN ? 2 : 1;
-    __shared__ __align__(16) uint8_t stage[MOE_LDS];
-    __shared__ uint16_t list[16 * MT];
+// matrix instructions.  The block's waves share the tokens' activations, brought into LDS a chunk of
+// contraction blocks ahead, a few instructions a step, so that the weights' loads (which complete in
+// order with them) never wait for a burst.  h keeps 16 significant bits: two bf16 planes, each
+// multiplied, since the matrix cores wait for memory anyway.
+template <int MT, int S, bool DOWN, int NW>
+__global__ __launch_bounds__(64 * NW, 4) void moe_stream_kernel(const MoeArgs p) {
+    constexpr int D = 2, PAIRS = NW / S, PL = DOWN ? 2 : 1, NT = 64 * NW, LDS = moe_lds(NW);
+    __shared__ __align__(16) uint8_t stage[LDS];
+    __shared__ uint16_t list[16 * MT];     // choices of this pass
+    __shared__ uint32_t at_byte[16 * MT];  // and where their activations start
     __shared__ int s_n;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % S;
     const int n = p.T * p.top_k;
     const int K = DOWN ? p.I : p.H, rows = DOWN ? p.H : p.I;  // multiples of 16
     int e = blockIdx.y;
-    if (p.by_choice) {  // the first choice of an expert has its block, the others end here
+    if (p.by_choice) {  // the first choice of an expert has its block, the others end below
         e = p.ids[blockIdx.y];
         if (e < 0 || e >= p.E) return;
-        bool earlier = false;
-        for (int a = threadIdx.x; a < (int)blockIdx.y; a += 512) earlier |= p.ids[a] == e;
-        if (__syncthreads_or(earlier)) return;
     }
     // first row of each tile; a tile never straddles a factor block, so its factors are uniform
     const int pair = blockIdx.x * PAIRS + wave / S;
@@ -270,6 +361,10 @@ __global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
     // a tile's 16 rows as a buffer: a lane past K, or a tile past the last row, reads zeros
     const __amdgpu_buffer_rsrc_t wbuf[2] = {tile_buffer(w + row0 * ld, on0 ? 15 * ld + K : 0),
                                             tile_buffer(w + row1 * ld, on1 ? 15 * ld + K : 0)};
+    // activations: x, or the two planes of h
+    const uint32_t plane = (uint32_t)n * (uint32_t)p.I * 2;
+    const i32x4_t abuf = make_rsrc4(DOWN ? p.h : p.x, DOWN ? 2 * plane : (uint32_t)((p.T - 1) * p.ld_x + K) * 2);
+    const uint32_t stage_at = lds_addr(stage);
     const uint32_t lane_off = (uint32_t)(r * ld) + 16 * g;
     const bool on[2] = {on0, on1};
     const float* s = DOWN ? p.s2 + e * p.s2_g : p.s13 + e * p.s13_g;
@@ -278,76 +373,53 @@ __global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
     const int kbs = (K + MB - 1) / MB, kb0 = kbs * part / S, len = kbs * (part + 1) / S - kb0;
     const int most = (kbs + S - 1) / S;  // the longest part's blocks
 
-    for (int first = 0;; first += 16 * MT) {
+    for (int first = 0;; first += p.pass) {
+        uint4 wv[D][2][2];
+        auto load = [&](int d, int hf, int i) {  // half of block i of the part into register set d
+            const int k = (kb0 + i) * MB + 64 * hf;
+            const uint32_t off = k + 16 * g < K && i < len ? lane_off + k : OOB;
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+                wv[d][c][hf] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf[c], off, 0, 0));
+        };
+#pragma unroll
+        for (int d = 0; d < D; d++) {
+            load(d, 0, d);
+            load(d, 1, d);
+        }
+        // the weights are on their way while the tokens are looked up
         if (wave == 0) {
-            const int c = choices_of(p.ids, n, e, first, 16 * MT, list, lane);
+            const int c = choices_of(p.ids, n, e, first, p.pass, lane, [&](int i, int a) {
+                list[i] = (uint16_t)a;
+                at_byte[i] = (uint32_t)(DOWN ? a * p.I : a / p.top_k * (int)p.ld_x) * 2;
+            });
             if (lane == 0) s_n = c;
         }
         __syncthreads();
         const int left = __builtin_amdgcn_readfirstlane(s_n) - first;
-        if (left <= 0) return;
-        const int mt = left >= 16 * MT ? MT : (left + 15) / 16;
-        const int toks = left < 16 * MT ? left : 16 * MT;
+        if (left <= 0 || (p.by_choice && first == 0 && list[0] != blockIdx.y)) return;
+        const int toks = left < p.pass ? left : p.pass, mt = (toks + 15) / 16;
         // rows of the staged chunk: lanes past the last take any row, their results are not used
-        int lr = 2;
+        int lr = 0;
         while ((1 << lr) < toks) lr++;
-        // contraction blocks of each part in a chunk: a power of two, D or more (see launch_stream)
+        // contraction blocks of each part in a chunk, of which two are held: a power of two, and
+        // launch_stream sees to it that one fits
         int lc = 0;
-        while ((MOE_LDS >> (lc + 1 + lr + 8)) >= PL * S && (1 << lc) < most) lc++;
-        if ((1 << lc) < D) lc = D == 4 ? 2 : 1;
+        while ((LDS / 2 >> (lc + 1 + lr + 8)) >= PL * S && (1 << lc) < most) lc++;
 
-        uint4 wv[D][2][2];
-        auto load = [&](int d, int i) {  // block i of the part into register set d
-#pragma unroll
-            for (int c = 0; c < 2; c++)
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    const int k = (kb0 + i) * MB + 64 * hf;
-                    const uint32_t off = k + 16 * g < K && i < len ? lane_off + k : 0x80000000u;
-                    wv[d][c][hf] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf[c], off, 0, 0));
-                }
+        // One instruction of staging: 4 rows of 256 bytes, rows of a (part, block) and plane following
+        // each other, of the chunk that starts at block i0 of every part; q counts them.
+        auto bring = [&](int i0, int q, uint32_t to) {
+            const int unit = 4 * q + g, row = unit & ((1 << lr) - 1), rest = unit >> lr, bl = rest / PL;
+            const int kb = kbs * (bl >> lc) / S + i0 + (bl & ((1 << lc) - 1));
+            const int k = kb * MB + 8 * (r ^ (row & 15));
+            uint32_t off = OOB;
+            if (row < toks && k < K) off = at_byte[row] + 2 * k + (PL == 2 && (rest & 1) ? plane : 0);
+            dma16(abuf, off, to + q * 1024);
         };
-        auto stage_chunk = [&](int i0) {  // blocks i0 .. of every part
-            __syncthreads();
-            const int per = 16 << lr, total = (S << lc) * per;  // 16-byte pieces: (part, block), row, piece
-#pragma unroll 1
-            for (int t = threadIdx.x; t < total; t += 512) {
-                const int ch = t & 15, row = (t >> 4) & ((1 << lr) - 1), bl = t >> (4 + lr);
-                const int pt = bl >> lc, i = i0 + (bl & ((1 << lc) - 1));
-                const int kb = kbs * pt / S + i, k = kb * MB + 8 * ch;
-                if (row >= toks || kb >= kbs) continue;
-                const int a = list[row];
-                uint8_t* dst = stage + (((bl * PL << lr) + row) << 8) + ((ch ^ (row & 15)) << 4);
-                if (!DOWN) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (k < K) v = *reinterpret_cast<const uint4*>(p.x + (a / p.top_k) * p.ld_x + k);
-                    *reinterpret_cast<uint4*>(dst) = v;
-                } else {
-                    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (k < K) {
-                        const f4_t* src = reinterpret_cast<const f4_t*>(p.h + (int64_t)a * p.I + k);
-                        const f4_t f0 = src[0], f1 = src[1];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            f[q] = f0[q];
-                            f[4 + q] = f1[q];
-                        }
-                    }
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int q = 0; q < 8; q++) {
-                        hi[q] = to_bf16(f[q]);
-                        const float rest = f[q] - __uint_as_float(hi[q] << 16);
-                        lo[q] = to_bf16(rest == rest ? rest : 0.0f);  // inf - inf
-                    }
-                    *reinterpret_cast<uint4*>(dst) =
-                        make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-                    *reinterpret_cast<uint4*>(dst + (256 << lr)) =
-                        make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
-                }
-            }
-            __syncthreads();
-        };
+        const int bring_all = (((S * PL) << (lc + lr)) + 3) >> 2;     // instructions of a chunk
+        const int bring_step = ((bring_all + NW - 1) / NW + (1 << lc) - 1) >> lc;  // one wave's in a step
+        uint32_t buf = 0;  // the buffer being read
 
         f4_t acc[2][MT];
 #pragma unroll
@@ -355,10 +427,10 @@ __global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
 #pragma unroll
             for (int m = 0; m < MT; m++) acc[c][m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
         float sv[2] = {0.0f, 0.0f};  // lane l: factors of blocks 64 j + l of the part
-#pragma unroll
-        for (int d = 0; d < D; d++) load(d, d);
+#pragma unroll 1
+        for (int q = wave; q < bring_all; q += NW) bring(0, q, stage_at);
+        wait_vm0();
         for (int i0 = 0; i0 < most; i0 += D) {
-            if ((i0 & ((1 << lc) - 1)) == 0) stage_chunk(i0);
             if ((i0 & 63) == 0) {
 #pragma unroll
                 for (int c = 0; c < 2; c++)
@@ -367,9 +439,27 @@ __global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
 #pragma unroll
             for (int d = 0; d < D; d++) {
                 const int i = i0 + d;
-                if (i >= len) break;
-                const int bl = (part << lc) + (i & ((1 << lc) - 1));
-                f4_t sum[2][MT];
+                if (i >= most) break;
+                const int i1 = i & ((1 << lc) - 1), next = i - i1 + (1 << lc);
+                if (i1 == 0) {
+                    // this chunk has landed, in every wave: only the last step's 4 weight loads are
+                    // younger than its instructions; and the buffer read until now is free
+                    if (i > 0) {
+                        asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+                        buf ^= LDS / 2;
+                    }
+                    __syncthreads();
+                }
+                if (next < most) {
+#pragma unroll 1
+                    for (int q = 0; q < bring_step; q++) {
+                        const int at = wave + NW * (i1 * bring_step + q);
+                        if (at < bring_all) bring(next, at, stage_at + (buf ^ (LDS / 2)));
+                    }
+                }
+                const int bl = (part << lc) + i1;
+                const float f0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sv[0]), i & 63));
+                const float f1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sv[1]), i & 63));
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
                     bf8_t b[2][2];
@@ -378,34 +468,28 @@ __global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
                         b[c][0] = widen8(wv[d][c][hf].x, wv[d][c][hf].y);
                         b[c][1] = widen8(wv[d][c][hf].z, wv[d][c][hf].w);
                     }
+                    load(d, hf, i + D);
 #pragma unroll
                     for (int m = 0; m < MT; m++) {
-                        if (m < mt) {
+                        if (m < mt && i < len) {
                             const int row = (16 * m + r) & ((1 << lr) - 1);
-                            if (hf == 0) sum[0][m] = sum[1][m] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                            f4_t sum0 = {0.0f, 0.0f, 0.0f, 0.0f}, sum1 = sum0;
 #pragma unroll
                             for (int pl = 0; pl < PL; pl++) {
-                                const uint8_t* src = stage + ((((bl * PL + pl) << lr) + row) << 8);
+                                const uint8_t* src = stage + buf + ((((bl * PL + pl) << lr) + row) << 8);
 #pragma unroll
                                 for (int q = 0; q < 2; q++) {
                                     const int ch = 8 * hf + 2 * g + q;
                                     const bf8_t a = as_bf8(*reinterpret_cast<const uint4*>(src + ((ch ^ (row & 15)) << 4)));
-                                    sum[0][m] = mma(a, b[0][q], sum[0][m]);
-                                    sum[1][m] = mma(a, b[1][q], sum[1][m]);
+                                    sum0 = mma(a, b[0][q], sum0);
+                                    sum1 = mma(a, b[1][q], sum1);
                                 }
                             }
-                        }
-                    }
-                }
-                load(d, i + D);
 #pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sv[c]), i & 63));
-#pragma unroll
-                    for (int m = 0; m < MT; m++) {
-                        if (m < mt) {
-#pragma unroll
-                            for (int q = 0; q < 4; q++) acc[c][m][q] = fmaf(sum[c][m][q], f, acc[c][m][q]);
+                            for (int q = 0; q < 4; q++) {
+                                acc[0][m][q] = fmaf(sum0[q], f0, acc[0][m][q]);
+                                acc[1][m][q] = fmaf(sum1[q], f1, acc[1][m][q]);
+                            }
                         }
                     }
                 }
@@ -438,7 +522,13 @@ __global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
                         const int64_t a = list[at];
                         const float u = acc[0][m][i], v = acc[1][m][i];
                         if (!DOWN) {
-                            if (on0) p.h[a * p.I + row0 + r] = u / (1.0f + expf(-u)) * v;
+                            const float h = u / (1.0f + expf(-u)) * v;
+                            const uint16_t hi = to_bf16(h);
+                            const float rest = h - __uint_as_float((uint32_t)hi << 16);
+                            if (on0) {
+                                p.h[a * p.I + row0 + r] = hi;
+                                p.h[(int64_t)n * p.I + a * p.I + row0 + r] = to_bf16(rest == rest ? rest : 0.0f);  // inf - inf
+                            }
                         } else {
                             if (on0) p.o[a * p.H + row0 + r] = u;
                             if (on1) p.o[a * p.H + row1 + r] = v;
@@ -446,7 +536,7 @@ __global__ __launch_bounds__(512, 4) void moe_stream_kernel(const MoeArgs p) {
                     }
                 }
         }
-        if (left <= 16 * MT) return;
+        if (left <= p.pass) return;
         __syncthreads();  // the list is written again
     }
 }
@@ -457,14 +547,22 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const MoeArgs p) {
     if (i >= n4) return;
     const int64_t t = i * 4 / p.H, c = i * 4 - t * p.H;
     f4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < p.top_k; j++) {
-        const int64_t a = t * p.top_k + j;
-        const int e = p.ids[a];
-        if (e < 0 || e >= p.E) continue;
-        const f4_t o = *reinterpret_cast<const f4_t*>(p.o + a * p.H + c);
-        const float w = p.weights[a];
+    for (int j0 = 0; j0 < p.top_k; j0 += 8) {  // 8 loads in flight
+        f4_t o[8];
+        float w[8];
+        bool on[8];
 #pragma unroll
-        for (int q = 0; q < 4; q++) s[q] = fmaf(w, o[q], s[q]);
+        for (int j = 0; j < 8; j++) {
+            const int64_t a = t * p.top_k + (j0 + j < p.top_k ? j0 + j : p.top_k - 1);
+            const int e = p.ids[a];
+            on[j] = j0 + j < p.top_k && e >= 0 && e < p.E;
+            w[j] = p.weights[a];
+            o[j] = *reinterpret_cast<const f4_t*>(p.o + a * p.H + c);  // unwritten where !on[j]
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) s[q] = on[j] ? fmaf(w[j], o[j][q], s[q]) : s[q];
     }
     uint16_t* y = p.y + t * p.ld_y + c;
 #pragma unroll
@@ -475,17 +573,16 @@ template <int MT, bool DOWN>
 static void launch_stream(const MoeArgs& p, hipStream_t stream) {
     const int n = p.T * p.top_k, experts = n < p.E ? n : p.E;
     const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
-    // parts of the contraction: 16 waves for every CU, each with 4 blocks or more; D blocks of every
-    // part have to fit the staging buffer: 2^8 bytes a row and plane, 16 MT rows
-    constexpr int D = MOE_D, most = MOE_LDS / (256 * 16 * MT * (DOWN ? 2 : 1) * D) < 8 ? MOE_LDS / (256 * 16 * MT * (DOWN ? 2 : 1) * D) : 8;
-    static_assert(most >= 1, "a chunk of D blocks fits");
+    // parts of the contraction: 16 waves for every CU, each with 4 blocks or more; one block of every
+    // part has to fit half the staging buffer (2^8 bytes a row and plane)
+    constexpr int NW = MT == 1 ? 4 : 8, PL = DOWN ? 2 : 1, SMAX = MT == 1 ? NW : 8 / (MT * PL);
+    static_assert(moe_lds(NW) / 2 >= SMAX * PL * (MT == 1 ? 1 : 16 * MT) * 256, "a block of every part fits");
     int S = 1;
-    while (S < most && experts * pairs * S < 4096 && kbs >= 8 * S) S *= 2;
-    const dim3 grid((unsigned)((pairs * S + 7) / 8), (unsigned)(p.by_choice ? n : p.E)), block(512);
-    if (S == 1) moe_stream_kernel<MT, 1, DOWN, D><<<grid, block, 0, stream>>>(p);
-    else if (S == 2) moe_stream_kernel<MT, most < 2 ? most : 2, DOWN, D><<<grid, block, 0, stream>>>(p);
-    else if (S == 4) moe_stream_kernel<MT, most < 4 ? most : 4, DOWN, D><<<grid, block, 0, stream>>>(p);
-    else moe_stream_kernel<MT, most, DOWN, D><<<grid, block, 0, stream>>>(p);
+    while (2 * S <= SMAX && 2 * S * PL * p.pass * 256 <= moe_lds(NW) / 2 && experts * pairs * S < 4096 && kbs >= 8 * S) S *= 2;
+    const dim3 grid((unsigned)((pairs * S + NW - 1) / NW), (unsigned)(p.by_choice ? n : p.E)), block(64 * NW);
+    if (S == 1) moe_stream_kernel<MT, 1, DOWN, NW><<<grid, block, 0, stream>>>(p);
+    else if (S == 2) moe_stream_kernel<MT, SMAX < 2 ? 1 : 2, DOWN, NW><<<grid, block, 0, stream>>>(p);
+    else moe_stream_kernel<MT, SMAX, DOWN, NW><<<grid, block, 0, stream>>>(p);
 }
 
 template <int MT>
@@ -499,6 +596,10 @@ static fp8q_status_t launch_moe(const MoeArgs& p, hipStream_t stream) {
     return FP8Q_OK;
 }
 
+// One block takes a token's whole router: 4 x 256 in 3.4 us against 5.5 us in two launches, but 64 x
+// 2048 in 15 us against 10 us.
+static bool route_is_small(int64_t H, int64_t E) { return E <= 256 && E * H <= (1 << 14); }
+
 static int route_splits(int64_t T, int64_t H, int64_t E) {
     // enough blocks for the chip's CUs, at least 8 instructions' worth of H for each of a block's waves
     const int64_t blocks = ((T + 15) / 16) * ((E + 15) / 16);
@@ -511,7 +612,7 @@ static int route_splits(int64_t T, int64_t H, int64_t E) {
 }  // namespace fp8q
 
 extern "C" size_t moe_route_workspace_size(int64_t T, int64_t H, int64_t E) {
-    if (T <= 0 || H <= 0 || E <= 0) return 256;
+    if (T <= 0 || H <= 0 || E <= 0 || fp8q::route_is_small(H, E)) return 256;
     return (size_t)fp8q::route_splits(T, H, E) * (size_t)T * (size_t)E * 4;
 }
 
@@ -528,17 +629,21 @@ extern "C" fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int6
     if (E > MOE_MAX_E || top_k > MOE_MAX_K || H % 8 || ld_x % 8 || ld_r % 8 || !fp8q_aligned(x, 16) ||
         !fp8q_aligned(router, 16) || H > 0x3FFFFFFF || T > 16LL * 65535)
         return FP8Q_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < moe_route_workspace_size(T, H, E)) return FP8Q_ERR_WORKSPACE;
+    if ((!workspace || workspace_bytes < moe_route_workspace_size(T, H, E)) && !route_is_small(H, E)) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 4)) return FP8Q_ERR_INVALID_ARG;
     RouteArgs p{};
     p.x = x; p.ld_x = ld_x; p.router = router; p.ld_r = ld_r; p.bias = bias; p.part = reinterpret_cast<float*>(workspace);
     p.ids = ids; p.weights = weights; p.T = (int)T; p.E = (int)E; p.H = (int)H; p.top_k = top_k;
     p.splits = route_splits(T, H, E); p.sigmoid = scoring == FP8Q_SCORE_SIGMOID; p.renorm = renormalize != 0; p.scale = scale;
+    if (route_is_small(H, E)) {
+        route_small_kernel<<<dim3((unsigned)T), dim3(1024), 0, stream>>>(p);
+        FP8Q_CHECK_LAUNCH();
+        return FP8Q_OK;
+    }
     route_logits_kernel<<<dim3((unsigned)((E + 15) / 16), (unsigned)p.splits, (unsigned)((T + 15) / 16)), dim3(256), 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     const dim3 grid((unsigned)T), block(64);
-    if (E <= 64) route_select_kernel<1><<<grid, block, 0, stream>>>(p);
-    else if (E <= 256) route_select_kernel<4><<<grid, block, 0, stream>>>(p);
+    if (E <= 256) route_choose_kernel<<<grid, dim3(256), 0, stream>>>(p);
     else route_select_kernel<16><<<grid, block, 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
@@ -565,7 +670,8 @@ extern "C" fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_
     if (T == 0) return FP8Q_OK;
     if (!x || !ids || !weights || !w13 || !s13 || !w2 || !s2 || !y) return FP8Q_ERR_INVALID_ARG;
     if (T > MOE_MAX_T || E > MOE_MAX_E || top_k > MOE_MAX_K || H % 16 || I % 16 || H > 0x3FFFFFFF || I > 0x3FFFFFFF || ld13 >= (1 << 26) ||
-        ld2 >= (1 << 26) || ld_x % 8 || ld13 % 16 || ld2 % 16 || w13_group_stride % 16 || w2_group_stride % 16 || !fp8q_aligned(x, 16) ||
+        ld2 >= (1 << 26) || ld_x >= (1 << 23) ||
+        T * top_k * I >= (1 << 29) || ld_x % 8 || ld13 % 16 || ld2 % 16 || w13_group_stride % 16 || w2_group_stride % 16 || !fp8q_aligned(x, 16) ||
         !fp8q_aligned(w13, 16) || !fp8q_aligned(w2, 16))
         return FP8Q_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < fp8_moe_few_tokens_workspace_size(T, H, I, top_k)) return FP8Q_ERR_WORKSPACE;
@@ -573,9 +679,11 @@ extern "C" fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_
     MoeArgs p{};
     p.x = x; p.ld_x = ld_x; p.ids = ids; p.weights = weights; p.w13 = w13; p.w2 = w2; p.ld13 = ld13; p.gs13 = w13_group_stride;
     p.ld2 = ld2; p.gs2 = w2_group_stride; p.s13 = s13; p.s2 = s2; p.s13_n = s13_n; p.s13_k = s13_k; p.s13_g = s13_group_stride;
-    p.s2_n = s2_n; p.s2_k = s2_k; p.s2_g = s2_group_stride; p.h = reinterpret_cast<float*>(workspace);
-    p.o = p.h + T * top_k * I; p.y = y; p.ld_y = ld_y;
+    p.s2_n = s2_n; p.s2_k = s2_k; p.s2_g = s2_group_stride; p.h = reinterpret_cast<uint16_t*>(workspace);
+    p.o = reinterpret_cast<float*>(workspace) + T * top_k * I; p.y = y; p.ld_y = ld_y;
     p.T = (int)T; p.H = (int)H; p.I = (int)I; p.E = (int)E; p.top_k = top_k;
     p.by_choice = T * top_k < E;
-    return T <= 16 ? launch_moe<1>(p, stream) : launch_moe<2>(p, stream);
+    p.pass = 1;
+    while (p.pass < T && p.pass < 64) p.pass *= 2;
+    return T <= 16 ? launch_moe<1>(p, stream) : T <= 32 ? launch_moe<2>(p, stream) : launch_moe<4>(p, stream);
 }

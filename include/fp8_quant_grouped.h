@@ -427,7 +427,7 @@ fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, c
  *   y[t] = sum_j weights[t,j] * W2_e (silu(G_e x_t) * (U_e x_t)),  e = ids[t,j]
  * with e4m3fn weights in blocks of 128 x 128 (fp8_block_quant_weights): [G_e; U_e] = w13[e] is
  * 2I x H (gate rows first), W2_e = w2[e] is H x I.  Nothing is quantized: x stays bf16, and what lies
- * between the two products and all sums are fp32 (or two bf16 halves of it).  An id
+ * between the two products has 16 significant bits and fp32 range, sums are fp32.  An id
  * outside [0, E) adds nothing (an expert that lives elsewhere); a token with none gives zeros.
  *   x bf16 [T][ld_x >= H]; ids int32, weights fp32 [T][top_k]
  *   w13 rows at stride ld13 >= H, experts at w13_group_stride; w2 rows at ld2 >= I
