@@ -1,0 +1,486 @@
+// Block-scaled FP8 grouped GEMM on gfx950 matrix cores: e4m3fn operands with one fp32 factor per
+// 128 elements of the contraction (1 x 128 blocks of activations and gradients, 128 x 128 blocks of
+// weights).
+//
+//   forward, M-grouped:  c[m,n]   = sum_kb sa[kb,m] sb[g,n/128,kb] sum_{k in kb} A[m,k] B_g[n,k]
+//   wgrad, K-grouped:    c[g,k,n] = sum_tb sa[tb,k] sb[tb,n] sum_{m in tb, g} A[k,m] B[n,m]
+//
+// One contraction step is one block, so v_mfma_f32_16x16x128_f8f6f4 makes a block's whole sum from
+// zero, and each of its results is added to an accumulator times its factors by one fused
+// multiply-add (the weight gradient: a product more).  Those run on the vector units while the
+// matrix cores work on the next row of results: the sums of row i are added while row i + 1 is
+// multiplied, 16 lanes' worth of work per 32-cycle matrix instruction.
+//
+// Tiles: T x T outputs (T = 256 or 128) by 8 waves, 128-byte steps, operands straight from memory
+// into two LDS stages (layout and swizzles: gemm_tile.hpp), the next step's loads in flight during
+// this one's arithmetic, one barrier per step.  A step's load offsets are the tile's plus the
+// step's position: they are held in registers, and only steps that end or begin inside a block
+// form masked ones.
+//   T = 256: one block per CU.  T = 128: two blocks per CU, for problems whose 256-tiles would
+//   leave CUs without work (see launch).
+//
+// Schedule (persistent blocks, no cross-block waits): as the other grouped GEMM.  Forward tiles go
+// by group, in bands of 8 row tiles, an XCD's share in one piece; weight-gradient tiles by group
+// size, largest first, in rounds.  Offsets are clamped into [0, M] before use, so any offsets
+// content keeps every access in range.
+#include <type_traits>
+
+#include "common.hpp"
+#include "gemm_tile.hpp"
+#include "lds_dma.hpp"
+
+namespace fp8q {
+
+struct BlockGemmArgs {
+    const uint8_t* a;
+    int64_t lda;
+    const float* sa;
+    int64_t ld_sa;
+    const uint8_t* b;
+    int64_t ldb, bgs;
+    const float* sb;
+    int64_t sb_n, sb_k, sb_g;  // strides by column block (forward), contraction block and group
+    const int32_t* offsets;    // null: one group
+    int G;
+    int M, N, K;
+    uint8_t* c;
+    int64_t ldc;
+    int32_t* status;           // null: not reported
+    int nt_n, nt_k;            // column tiles; weight gradient: row tiles
+    bool out_f32, vec_store;
+};
+
+__device__ __forceinline__ v8i_t two_chunks(const uint8_t* lo, const uint8_t* hi) {
+    const uint4 a = *reinterpret_cast<const uint4*>(lo), b = *reinterpret_cast<const uint4*>(hi);
+    return v8i_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+template <int MODE, int T>
+__global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const BlockGemmArgs p) {
+    constexpr bool FWD = MODE == MODE_FWD;
+    constexpr int STAGE = T * GK, NP = T / 64;     // bytes of one operand tile; its loads per wave
+    constexpr int WM = T / 2, WN = T / 4;          // a wave's rows and columns
+    constexpr int MI = WM / 16, NJ = WN / 16;
+    constexpr int NT = 512;
+    __shared__ __align__(16) uint8_t smem[2][2][STAGE];
+    __shared__ __align__(16) float sscale[2][2][T];  // by stage: factors of the tile's rows, columns
+    __shared__ int s_pref[FWD ? GMAX + 1 : 1];       // forward: row tiles before each group
+    __shared__ unsigned short s_perm[FWD ? 1 : GMAX];  // weight gradient: groups, most steps first
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int lr = lane & 15, lq = lane >> 4;
+
+    auto end_of = [&](int g) -> int { return p.offsets ? p.offsets[g] : p.M; };
+    // group g's rows, clamped so that any offsets content stays in range
+    auto rows_of = [&](int lo, int hi, int& l, int& h) {
+        l = lo < 0 ? 0 : lo > p.M ? p.M : lo;
+        h = hi < l ? l : hi > p.M ? p.M : hi;
+    };
+    auto group_rows = [&](int g, int& l, int& h) { rows_of(g == 0 ? 0 : end_of(g - 1), end_of(g), l, h); };
+
+    // --- the offsets check (block 0's last wave) and the schedule's table
+    if (p.status != nullptr && blockIdx.x == 0 && wave == 7) {
+        int bad = 0x7FFFFFFF;
+        for (int i = lane; i < p.G; i += 64) {
+            const int64_t lo = i == 0 ? 0 : end_of(i - 1), hi = end_of(i);
+            if ((hi < lo || hi > p.M || (i == p.G - 1 && hi != p.M)) && i < bad) bad = i;
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            const int o = __shfl_xor(bad, off, 64);
+            bad = o < bad ? o : bad;
+        }
+        if (lane == 0) {
+            p.status[0] = bad == 0x7FFFFFFF ? (int32_t)FP8Q_OK : (int32_t)FP8Q_ERR_INVALID_ARG;
+            p.status[1] = bad == 0x7FFFFFFF ? -1 : bad;
+        }
+    }
+    if (FWD) {
+        if (wave == 0) {
+            int base = 0;
+            for (int g0 = 0; g0 < p.G; g0 += 64) {
+                int l = 0, h = 0;
+                if (g0 + lane < p.G) group_rows(g0 + lane, l, h);
+                int n = (h - l + T - 1) / T;
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const int o = __shfl_up(n, off, 64);
+                    if (lane >= off) n += o;
+                }
+                if (g0 + lane < p.G) s_pref[g0 + lane + 1] = base + n;
+                base += __shfl(n, 63, 64);
+            }
+            if (lane == 0) s_pref[0] = 0;
+        }
+    } else {
+        // a group's place is the number of groups with more steps, or as many and a lower index
+        int* steps = reinterpret_cast<int*>(&smem[0][0][0]);
+        for (int g = t; g < p.G; g += NT) {
+            int l, h;
+            group_rows(g, l, h);
+            l &= ~(GK - 1);
+            steps[g] = h > l ? (h - l + GK - 1) / GK : 0;
+        }
+        __syncthreads();
+        for (int g = t; g < p.G; g += NT) {
+            const int mine = steps[g];
+            int place = 0;
+            for (int o = 0; o < p.G; o++) place += steps[o] > mine || (steps[o] == mine && o < g);
+            s_perm[place] = (unsigned short)g;
+        }
+    }
+    __syncthreads();
+
+    const int nb = gridDim.x, nx = nb % 8 == 0 ? 8 : 1;  // blocks are dealt to the 8 XCDs round-robin
+    const int xcd = (int)blockIdx.x % nx, lb = (int)blockIdx.x / nx, bpx = nb / nx;
+    int ti = 0, t_end = 0, round = 0;
+    if (FWD) {
+        const long long total = (long long)s_pref[p.G] * p.nt_n;  // < 2^31 (host check)
+        ti = __builtin_amdgcn_readfirstlane((int)(total * xcd / nx) + lb);
+        t_end = __builtin_amdgcn_readfirstlane((int)(total * (xcd + 1) / nx));
+    }
+    const int tpg = p.nt_k * p.nt_n, w_tiles = FWD ? 0 : p.G * tpg;
+
+    struct Tile {
+        int g, raw_lo, raw_hi;
+        int row, n0, rows, cols;       // first output row and column, rows and columns inside
+        int k_lo, k_hi, k0, steps;     // contraction range, its first step's position, steps
+    };
+    auto tile_start = [&](Tile& x) -> bool {
+        if (FWD) {
+            if (ti >= t_end) return false;
+            int lo = 0, hi = p.G - 1;  // last group whose tiles start at or before ti
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s_pref[mid] * p.nt_n <= ti) lo = mid; else hi = mid - 1;
+            }
+            x.g = lo;
+            const int rt = s_pref[lo + 1] - s_pref[lo], l = ti - s_pref[lo] * p.nt_n;
+            constexpr int BAND = 8;
+            const int bt = BAND * p.nt_n, b = l / bt, r = l - b * bt;
+            const int in_band = rt - b * BAND < BAND ? rt - b * BAND : BAND;
+            x.n0 = (r / in_band) * T;
+            x.row = (b * BAND + r % in_band) * T;  // relative to the group's start
+            ti += bpx;
+        } else {
+            int idx;
+            if (nx == 8) {
+                const int chunk = (round & 1) ? 7 - xcd : xcd;
+                idx = round * nb + chunk * bpx + ((round & 1) ? bpx - 1 - lb : lb);
+            } else {
+                idx = round * nb + ((round & 1) ? nb - 1 - (int)blockIdx.x : (int)blockIdx.x);
+            }
+            if (idx >= w_tiles) return false;
+            round++;
+            x.g = s_perm[idx / tpg];
+            const int l = idx % tpg;
+            x.row = (l / p.nt_n) * T;
+            x.n0 = (l % p.nt_n) * T;
+        }
+        // uniform, though read from LDS: keep the tile in scalar registers
+        x.g = __builtin_amdgcn_readfirstlane(x.g);
+        x.row = __builtin_amdgcn_readfirstlane(x.row);
+        x.n0 = __builtin_amdgcn_readfirstlane(x.n0);
+        x.raw_lo = x.g == 0 ? 0 : end_of(x.g - 1);
+        x.raw_hi = end_of(x.g);
+        return true;
+    };
+    auto tile_finish = [&](Tile& x) {
+        int l, h;
+        rows_of(x.raw_lo, x.raw_hi, l, h);
+        if (FWD) {
+            x.row += l;
+            x.rows = h - x.row < T ? h - x.row : T;
+            x.k_lo = 0;
+            x.k_hi = p.K;
+        } else {
+            x.rows = p.K - x.row < T ? p.K - x.row : T;
+            x.k_lo = l;
+            x.k_hi = h;
+        }
+        x.k0 = x.k_lo & ~(GK - 1);
+        x.steps = x.k_hi > x.k0 ? (x.k_hi - x.k0 + GK - 1) / GK : 0;
+        x.cols = p.N - x.n0 < T ? p.N - x.n0 : T;
+    };
+
+    // Loads of the tile whose steps are being issued: descriptors at its first rows, and this lane's
+    // offset in each of the wave's NP parts (8 rows x 128 bytes) of either operand.
+    i32x4_t ra, rb;
+    uint32_t oa[NP], ob[NP];
+    Tile src;
+    const int part_row = wave * (8 * NP) + (lane >> 3);
+    auto aim = [&](const Tile& x) {
+        src = x;
+        ra = make_rsrc4(p.a + (int64_t)x.row * p.lda, (uint32_t)(x.rows * p.lda));
+        rb = make_rsrc4(p.b + (FWD ? (int64_t)x.g * p.bgs : 0) + (int64_t)x.n0 * p.ldb, (uint32_t)(x.cols * p.ldb));
+#pragma unroll
+        for (int i = 0; i < NP; i++) {
+            const int row = part_row + 8 * i, ch = lane & 7;
+            oa[i] = row < x.rows ? (uint32_t)row * (uint32_t)p.lda + 16 * (ch ^ swz(row)) : OOB;
+            ob[i] = row < x.cols ? (uint32_t)row * (uint32_t)p.ldb + 16 * (ch ^ swzB(row)) : OOB;
+        }
+    };
+    auto issue = [&](int kpos, int stage) {
+        const uint32_t at_a = lds_addr(smem[stage][0]) + wave * (NP * 1024), at_b = lds_addr(smem[stage][1]) + wave * (NP * 1024);
+        if (t < T) {  // wave-uniform: the factors of row t of both tiles
+            const int64_t kb = kpos / GK;
+            const i32x4_t rsa = make_rsrc4(p.sa + kb * p.ld_sa + src.row, (uint32_t)src.rows * 4u);
+            const i32x4_t rsb = make_rsrc4(FWD ? p.sb + (int64_t)src.g * p.sb_g + kb * p.sb_k : p.sb + kb * p.sb_k + src.n0, 0x7FFFFFFFu);
+            const uint32_t o = FWD ? (uint32_t)((src.n0 + t) / GK) * (uint32_t)p.sb_n * 4u : (uint32_t)t * 4u;
+            dma4(rsa, (uint32_t)t * 4u, lds_addr(&sscale[stage][0][0]) + wave * 256);
+            dma4(rsb, t < src.cols ? o : OOB, lds_addr(&sscale[stage][1][0]) + wave * 256);
+        }
+        if (kpos >= src.k_lo && kpos + GK <= src.k_hi) {
+#pragma unroll
+            for (int i = 0; i < NP; i++) {
+                // parts past the tile's rows stay as they are: their results are not stored
+                if (!FWD || wave * (8 * NP) + 8 * i < src.rows) dma16_at(ra, oa[i], kpos, at_a + i * 1024);
+                dma16_at(rb, ob[i], kpos, at_b + i * 1024);
+            }
+        } else {  // chunks outside the range read as zeros
+#pragma unroll
+            for (int i = 0; i < NP; i++) {
+                const int row = part_row + 8 * i, ch = lane & 7;
+                const int pa = kpos + 16 * (ch ^ swz(row)), pb = kpos + 16 * (ch ^ swzB(row));
+                const uint32_t xa = pa < src.k_hi && pa + 16 > src.k_lo ? oa[i] + kpos : OOB;
+                const uint32_t xb = pb < src.k_hi && pb + 16 > src.k_lo ? ob[i] + kpos : OOB;
+                dma16(ra, xa, at_a + i * 1024);
+                dma16(rb, xb, at_b + i * 1024);
+            }
+        }
+    };
+
+    Tile cur, nxt;
+    bool have = tile_start(cur);
+    int st = 0;  // stage of the current step
+    if (have) {
+        tile_finish(cur);
+        if (cur.steps > 0) {
+            aim(cur);
+            issue(cur.k0, 0);
+        }
+    }
+    // this lane's fragments: A row wm * WM + lr (+ 16 i), B row brow(j, lr) of its columns
+    const int fa0 = lds_off(wm * WM + lr, lq), fa1 = lds_off(wm * WM + lr, 4 + lq);
+    const int fb0 = lds_offB(wn * WN + brow(0, lr), lq), fb1 = lds_offB(wn * WN + brow(0, lr), 4 + lq);
+
+    while (have) {
+        v4f_t acc[MI][NJ];
+#pragma unroll
+        for (int i = 0; i < MI; i++)
+#pragma unroll
+            for (int j = 0; j < NJ; j++) acc[i][j] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+        bool have_next = false;
+        for (int s = 0; s < cur.steps; s++, st ^= 1) {
+            const int kpos = cur.k0 + s * GK;
+            wait_vm0();
+            if (!FWD && (kpos < cur.k_lo || kpos + GK > cur.k_hi)) {
+                // zero the bytes of other groups' tokens (or of the padding past M) in the chunks that
+                // the range cuts, in both operands: such a byte may be a NaN code
+                __syncthreads();
+                const int lo = cur.k_lo - kpos, hi = cur.k_hi - kpos;
+                if (t < 2 * T) {
+                    const int row = t & (T - 1);
+                    uint8_t* side = smem[st][t / T];
+#pragma unroll
+                    for (int ch = 0; ch < 8; ch++) {
+                        const int b0 = 16 * ch;
+                        if ((lo > b0 && lo < b0 + 16) || (hi > b0 && hi < b0 + 16)) {
+                            uint4* q = reinterpret_cast<uint4*>(side + (t < T ? lds_off(row, ch) : lds_offB(row, ch)));
+                            uint4 w = *q;
+                            w.x &= keep_mask4(lo, hi, b0);
+                            w.y &= keep_mask4(lo, hi, b0 + 4);
+                            w.z &= keep_mask4(lo, hi, b0 + 8);
+                            w.w &= keep_mask4(lo, hi, b0 + 12);
+                            *q = w;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            if (s == 0) have_next = tile_start(nxt);
+            if (s + 1 < cur.steps) {
+                issue(kpos + GK, st ^ 1);
+            } else if (have_next) {
+                tile_finish(nxt);
+                if (nxt.steps > 0) {
+                    aim(nxt);
+                    issue(nxt.k0, st ^ 1);
+                }
+            }
+            const uint8_t* As = smem[st][0];
+            const uint8_t* Bs = smem[st][1];
+            const float* sa = &sscale[st][0][wm * WM + lr];
+            const float* sb = &sscale[st][1][wn * WN];
+            v8i_t bf[NJ];
+            v4f_t sbv[FWD ? 1 : NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; j++) {
+                const int o = 32 * GK * (j >> 1) + 4 * GK * (j & 1);
+                bf[j] = two_chunks(Bs + fb0 + o, Bs + fb1 + o);
+                if (!FWD) sbv[FWD ? 0 : j] = *reinterpret_cast<const v4f_t*>(sb + 32 * (j >> 1) + 8 * lq + 4 * (j & 1));
+            }
+            const float sbu = FWD ? sb[0] : 1.0f;  // a wave's columns lie in one weight block
+            v4f_t sum[2][NJ];
+            float f[2];
+#pragma unroll
+            for (int i = 0; i <= MI; i++) {
+                if (i < MI) {
+                    const v8i_t af = two_chunks(As + fa0 + 16 * GK * i, As + fa1 + 16 * GK * i);
+                    f[i & 1] = sa[16 * i] * sbu;
+#pragma unroll
+                    for (int j = 0; j < NJ; j++)
+                        sum[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            bf[j], af, v4f_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+                }
+                if (i > 0) {
+#pragma unroll
+                    for (int j = 0; j < NJ; j++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const float v = sum[(i - 1) & 1][j][e];
+                            acc[i - 1][j][e] = fmaf(FWD ? v : v * sbv[FWD ? 0 : j][e], f[(i - 1) & 1], acc[i - 1][j][e]);
+                        }
+                }
+            }
+        }
+        if (cur.steps == 0) {
+            have_next = tile_start(nxt);
+            if (have_next) {
+                tile_finish(nxt);
+                if (nxt.steps > 0) {
+                    __syncthreads();  // the other waves may still read the stage
+                    aim(nxt);
+                    issue(nxt.k0, st);
+                }
+            }
+        }
+
+        // Epilogue: lane rows wm * WM + 16 i + lr, and per pair of column blocks 8 consecutive
+        // columns.  A row or column past the tile's last gets an offset past the buffer.
+        const int64_t row0 = FWD ? (int64_t)cur.row : (int64_t)cur.g * p.K + cur.row;
+        auto epilogue = [&](auto f32) {
+            constexpr bool F32 = decltype(f32)::value;
+            constexpr uint32_t ESZ = F32 ? 4 : 2;
+            const uint32_t ldc = (uint32_t)p.ldc * ESZ;
+            const __amdgpu_buffer_rsrc_t rc =
+                make_rsrc(p.c + (row0 * p.ldc + cur.n0) * ESZ, (uint32_t)(cur.rows - 1) * ldc + (uint32_t)cur.cols * ESZ);
+            int el = lane;
+            asm volatile("" : "+v"(el));  // the addresses are formed here, not held through the steps
+            const int elr = el & 15, elq = el >> 4;
+            if (p.vec_store) {
+                const uint32_t at = (wm * WM + elr) * ldc + (wn * WN + 8 * elq) * ESZ;
+#pragma unroll
+                for (int jp = 0; jp < NJ / 2; jp++) {
+                    const bool col_ok = wn * WN + 32 * jp + 8 * elq < cur.cols;
+#pragma unroll
+                    for (int i = 0; i < MI; i++) {
+                        const uint32_t off = col_ok && wm * WM + 16 * i + elr < cur.rows ? at + 16 * i * ldc + 32 * jp * ESZ : OOB;
+                        const v4f_t v = acc[i][2 * jp], w = acc[i][2 * jp + 1];
+                        if (F32) {
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, v), rc, off, 0, 0);
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, w), rc, off + 16u, 0, 0);
+                        } else {
+                            __builtin_amdgcn_raw_buffer_store_b128(
+                                i32x4_t{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3]), (int)pack_bf16x2(w[0], w[1]), (int)pack_bf16x2(w[2], w[3])},
+                                rc, off, 0, 0);
+                        }
+                    }
+                }
+            } else {
+                // any N, ldc and alignment: 16 rows at a time through LDS (the wave's own piece of
+                // the stage that no load goes to), so that a store's lanes write neighbouring columns
+                __syncthreads();
+                float* own = reinterpret_cast<float*>(&smem[st ^ 1][0][0] + wave * (16 * WN * 4));
+#pragma unroll
+                for (int i = 0; i < MI; i++) {
+#pragma unroll
+                    for (int j = 0; j < NJ; j++)
+                        *reinterpret_cast<v4f_t*>(own + elr * WN + 32 * (j >> 1) + 8 * elq + 4 * (j & 1)) = acc[i][j];
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 4
+                    for (int q = 0; q < 16 * WN / 64; q++) {
+                        const int idx = q * 64 + el, row = wm * WM + 16 * i + idx / WN, col = wn * WN + idx % WN;
+                        const uint32_t off = row < cur.rows && col < cur.cols ? row * ldc + col * ESZ : OOB;
+                        const float v = own[idx];
+                        if (F32)
+                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), rc, off, 0, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b16((short)(pack_bf16x2(v, 0.0f) & 0xFFFFu), rc, off, 0, 0);
+                    }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                }
+            }
+        };
+        if (p.out_f32) epilogue(std::true_type{});
+        else epilogue(std::false_type{});
+        have = have_next;
+        cur = nxt;
+    }
+}
+
+template <int MODE, int T>
+static fp8q_status_t launch_block_gemm(BlockGemmArgs p, hipStream_t stream) {
+    p.nt_n = (p.N + T - 1) / T;
+    p.nt_k = MODE == MODE_FWD ? 1 : (p.K + T - 1) / T;
+    const int64_t tiles = MODE == MODE_FWD ? ((int64_t)(p.M + T - 1) / T + p.G) * p.nt_n : (int64_t)p.G * p.nt_k * p.nt_n;
+    if (tiles >= 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
+    int64_t grid = (int64_t)num_cus() * (T == 256 ? 1 : 2);
+    if (tiles < grid) grid = tiles;
+    block_gemm_kernel<MODE, T><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(p);
+    FP8Q_CHECK_LAUNCH();
+    return FP8Q_OK;
+}
+
+template <int MODE>
+static fp8q_status_t pick_block_gemm(const BlockGemmArgs& p, hipStream_t stream) {
+    const int64_t rows = MODE == MODE_FWD ? p.M : (int64_t)p.G * p.K;
+    const int64_t tiles = (rows + 255) / 256 * ((p.N + 255) / 256);
+#ifdef FORCE_T
+    return launch_block_gemm<MODE, FORCE_T>(p, stream);
+#endif
+    return tiles < 256 ? launch_block_gemm<MODE, 128>(p, stream) : launch_block_gemm<MODE, 256>(p, stream);
+}
+
+}  // namespace fp8q
+
+extern "C" fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uint8_t* a, int64_t lda,
+                                                const float* a_scales, int64_t ld_sa, const uint8_t* b,
+                                                int64_t ldb, int64_t b_group_stride, const float* b_scales,
+                                                int64_t sb_n, int64_t sb_k, int64_t sb_group_stride,
+                                                const int32_t* offsets, int32_t groups, int64_t M, int64_t N,
+                                                int64_t K, void* c, int64_t ldc, fp8q_out_t out_dtype,
+                                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    using namespace fp8q;
+    const bool fwd = mode == FP8Q_GEMM_FWD_MGROUPED;
+    if (!fwd && mode != FP8Q_GEMM_WGRAD_KGROUPED) return FP8Q_ERR_INVALID_ARG;
+    if (groups < 1 || M < 0 || N < 0 || K < 0 || ldc < N || (!offsets && groups != 1) || sb_n < 0 || sb_k < 0 ||
+        sb_group_stride < 0 || b_group_stride < 0)
+        return FP8Q_ERR_INVALID_ARG;
+    if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_FP32) return FP8Q_ERR_INVALID_ARG;
+    const int64_t esz = out_dtype == FP8Q_OUT_FP32 ? 4 : 2;
+    if (workspace && workspace_bytes < 256) return FP8Q_ERR_WORKSPACE;
+    if (!fp8q_aligned(workspace, 4) || !fp8q_aligned(a_scales, 4) || !fp8q_aligned(b_scales, 4) || !fp8q_aligned(c, (uintptr_t)esz))
+        return FP8Q_ERR_INVALID_ARG;
+    const int64_t inner = fwd ? K : M, rows = fwd ? M : K;
+    if (lda < inner || ldb < inner || ld_sa < rows) return FP8Q_ERR_INVALID_ARG;
+    if (!fwd && (b_group_stride != 0 || sb_group_stride != 0 || sb_n != 1 || sb_k < N)) return FP8Q_ERR_INVALID_ARG;
+    if (N == 0 || rows == 0) return FP8Q_OK;
+    if (!c || (inner > 0 && (!a || !b || !a_scales || !b_scales))) return FP8Q_ERR_INVALID_ARG;
+    if (lda % 16 || ldb % 16 || !fp8q_aligned(a, 16) || !fp8q_aligned(b, 16)) return FP8Q_ERR_UNSUPPORTED;
+    if (fwd && (K % 16 || b_group_stride % 16)) return FP8Q_ERR_UNSUPPORTED;
+    // 32-bit tile indices, contraction positions and offsets within 256 rows; a column block's
+    // factor is reached with a 32-bit byte offset
+    constexpr int64_t most = 0x7FFFFF00LL;
+    if (groups > GMAX || M > most || N > most || K > most || 256 * lda > most || 256 * ldb > most || 256 * ldc * esz > most ||
+        (fwd && (N / GK + 1) * sb_n > (1LL << 29)))
+        return FP8Q_ERR_UNSUPPORTED;
+    BlockGemmArgs p{};
+    p.a = a; p.lda = lda; p.sa = a_scales; p.ld_sa = ld_sa; p.b = b; p.ldb = ldb; p.bgs = b_group_stride;
+    p.sb = b_scales; p.sb_n = sb_n; p.sb_k = sb_k; p.sb_g = sb_group_stride; p.offsets = offsets; p.G = groups;
+    p.M = (int)M; p.N = (int)N; p.K = (int)K; p.c = reinterpret_cast<uint8_t*>(c); p.ldc = ldc;
+    p.status = reinterpret_cast<int32_t*>(workspace); p.out_f32 = out_dtype == FP8Q_OUT_FP32;
+    p.vec_store = N % 8 == 0 && ldc % 8 == 0 && fp8q_aligned(c, 16);
+    return fwd ? pick_block_gemm<MODE_FWD>(p, stream) : pick_block_gemm<MODE_WGRAD>(p, stream);
+}

@@ -55,35 +55,14 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "gemm_tile.hpp"
 #include "lds_dma.hpp"
 
 namespace fp8q {
 
-typedef int v8i_t __attribute__((ext_vector_type(8)));
-typedef float v4f_t __attribute__((ext_vector_type(4)));
-
 constexpr int GT = 256;         // output tile edge (rows and columns)
 
-constexpr int GK = 128;         // contraction bytes per step
 constexpr int STAGE = GT * GK;  // bytes of one operand tile in LDS
-constexpr uint32_t OOB = 0x80000000u;
-constexpr int MODE_FWD = 0, MODE_WGRAD = 1;
-
-// 16-byte slot of chunk c in row r: c ^ (2*((r >> 2) & 3) + ((r >> 1) & 1)).  A fragment read
-// is served as two 32-lane halves, each touching 16 consecutive rows at chunks kg ^ s and
-// (kg+1) ^ s; the rows that share a 512-byte LDS window (same r & 3) get distinct
-// 2*((r >> 2) & 3), so all 32 16-byte slots of a half are distinct (no bank conflicts).
-__device__ __forceinline__ int swz(int r) { return (((r >> 2) & 3) << 1) | ((r >> 1) & 1); }
-__device__ __forceinline__ int lds_off(int r, int ch) { return r * GK + ((ch ^ swz(r)) << 4); }
-// N-side tile: its fragments take rows 32j' + 8q + 4h + e (q = lane%16 / 4, e = lane%4) so that
-// each lane's results are 8 consecutive output columns; slot c ^ (2*((r>>3)&3) + ((r>>1)&1))
-// puts those 16 rows in 16 distinct 16-byte bank slots.
-__device__ __forceinline__ int swzB(int r) { return (((r >> 3) & 3) << 1) | ((r >> 1) & 1); }
-__device__ __forceinline__ int lds_offB(int r, int ch) { return r * GK + ((ch ^ swzB(r)) << 4); }
-// Row of the N-side tile that feeds MFMA row lr of column block j (see swzB).
-__device__ __forceinline__ int brow(int j, int lr) {
-    return 32 * (j >> 1) + 8 * (lr >> 2) + 4 * (j & 1) + (lr & 3);
-}
 
 // e4m3fnuz byte -> e4m3fn byte of the same value (four bytes at a time).
 __device__ __forceinline__ uint32_t fnuz_to_fn4(uint32_t w) {
@@ -96,23 +75,6 @@ __device__ __forceinline__ uint32_t fnuz_to_fn4(uint32_t w) {
     const uint32_t rnd = v & (v >> 1) & 0x01010101u;     // odd v with odd v>>1: round up to even
     const uint32_t small = (half + rnd) | sign;
     return (normal & m8) | (small & ~m8);
-}
-
-// Bytes at positions base..base+3 of a chunk kept where lo <= pos < hi.
-__device__ __forceinline__ uint32_t keep_mask4(int lo, int hi, int base) {
-    int a = lo - base, b = hi - base;
-    a = a < 0 ? 0 : (a > 4 ? 4 : a);
-    b = b < 0 ? 0 : (b > 4 ? 4 : b);
-    const uint32_t below_b = b >= 4 ? 0xFFFFFFFFu : ((1u << (8 * b)) - 1u);
-    const uint32_t from_a = a >= 4 ? 0u : (0xFFFFFFFFu << (8 * a));
-    return below_b & from_a;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
-    a += 0x7FFFu + ((a >> 16) & 1u);
-    b += 0x7FFFu + ((b >> 16) & 1u);
-    return (a >> 16) | (b & 0xFFFF0000u);
 }
 
 template <bool NSIDE>
@@ -142,7 +104,6 @@ struct GemmArgs {
     const uint8_t* b_e8;
     int64_t ld_sb;
     int64_t sbgs;
-    int64_t sb_n, sb_k;  // BLK: strides of b's factors by column block and contraction block
     const int32_t* offsets;
     int G;
     int64_t M, N, K;
@@ -155,7 +116,6 @@ struct GemmArgs {
     bool vec_store;   // N, ldc multiples of 8 and c 16-byte aligned: whole 16-byte stores
 };
 
-constexpr int GMAX = 2048;  // groups whose schedule prefix fits in LDS
 
 struct Tile {  // all extents < 2^31 (checked on the host)
     int g, par;  // group; parity of the tile in the block's sequence (scale buffer)
@@ -172,11 +132,7 @@ struct Tile {  // all extents < 2^31 (checked on the host)
 // forward); or one dword DMA per row and side per step (MX_DW: 4-byte aligned scale rows, the
 // weight gradient, whose tiles then start on 128-token boundaries so that a step's 4 scale
 // bytes are one aligned dword).
-//
-// BLK is no MX form but shares their per-step scales: one fp32 factor per row and 128-element
-// contraction block (forward: per 128 x 128 block on the weight side).  A step is one block, so a
-// step's products are summed from zero and added to the accumulators times the two factors.
-constexpr int MX_NONE = 0, MX_BYTES = 1, MX_DMA = 2, MX_DW = 3, BLK = 4;
+constexpr int MX_NONE = 0, MX_BYTES = 1, MX_DMA = 2, MX_DW = 3;
 
 template <int FMT, int MODE, int MXV, int NW>
 __global__ __launch_bounds__(64 * NW, 1) void gemm256_kernel(const GemmArgs p) {
@@ -214,12 +170,10 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm256_kernel(const GemmArgs p) {
     // weight gradient: a tile's contraction starts at its group's first token rounded down to
     // 16 (one LDS chunk), or to 32 for MX so that the steps' 32-token blocks are the scale blocks
     // (128 with dword scale DMA: a step's four scale bytes are then one aligned dword)
-    constexpr int64_t KALIGN = MXV == MX_DW || MXV == BLK ? 127 : MX ? 31 : 15;
+    constexpr int64_t KALIGN = MXV == MX_DW ? 127 : MX ? 31 : 15;
 
     if (OFF_LDS) {
-        // BLK: no offsets means one group of all rows
-        for (int i = t; i < p.G; i += NT)
-            s_off[i] = MXV == BLK && p.offsets == nullptr ? (int)p.M : p.offsets[i];
+        for (int i = t; i < p.G; i += NT) s_off[i] = p.offsets[i];
         __syncthreads();
     }
     auto off_at = [&](int g) -> int { return OFF_LDS ? s_off[g] : p.offsets[g]; };
@@ -498,20 +452,6 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm256_kernel(const GemmArgs p) {
             dma4(rsa, oa, lds_addr(&sscale[stage][0][(wave & 3) * 64]));
             dma4(rsb, ob, lds_addr(&sscale[stage][1][(wave & 3) * 64]));
         }
-        if (MXV == BLK && row_thread) {
-            // rows t of both tiles: the factors of this step's contraction block
-            const int64_t kb = kpos / GK;
-            const i32x4_t rsa = make_rsrc4(p.a_scales + kb * p.ld_sa + T.row_lo, (uint32_t)T.a_rows * 4u);
-            const int n = T.n0 + t;
-            uint32_t ob;
-            if (MODE == MODE_FWD) ob = (uint32_t)(n / GK) * (uint32_t)p.sb_n * 4u;
-            else ob = (uint32_t)t * 4u;
-            const i32x4_t rsb = make_rsrc4(
-                MODE == MODE_FWD ? p.b_scales + (int64_t)T.g * p.sbgs + kb * p.sb_k
-                                 : p.b_scales + kb * p.sb_k + T.n0, 0x7FFFFFFFu);
-            dma4(rsa, (uint32_t)t * 4u, lds_addr(&sscale[stage][0][(wave & 3) * 64]));
-            dma4(rsb, t < T.b_rows ? ob : OOB, lds_addr(&sscale[stage][1][(wave & 3) * 64]));
-        }
         if (MXV == MX_BYTES && row_thread) {
             // rows t of both tiles: the 4 E8M0 bytes of this 128-byte step, packed into one
             // dword per row (blocks past K get 127 = 2^0: their data bytes are zero)
@@ -705,19 +645,6 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm256_kernel(const GemmArgs p) {
             }
             // 16 waves: a wave issuing its matrix instructions goes ahead of the other waves'
             // memory instructions (weight gradient 517 -> 510 us; forward unchanged)
-            v4f_t sbv[MXV == BLK && MODE == MODE_WGRAD ? NJ : 1];
-            float sbu = 0.0f;
-            if (MXV == BLK) {
-                const float* sbp = reinterpret_cast<const float*>(&sscale[cur_st][1][wn * WNC]);
-                if (MODE == MODE_FWD) {
-                    sbu = sbp[0];  // a wave's columns lie in one 128-column block
-                } else {
-#pragma unroll
-                    for (int j = 0; j < NJ; j++)
-                        sbv[MODE == MODE_WGRAD ? j : 0] = *reinterpret_cast<const v4f_t*>(
-                            sbp + 32 * (j >> 1) + 8 * lq + 4 * (j & 1));
-                }
-            }
             if (NW == 16) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
@@ -741,21 +668,9 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm256_kernel(const GemmArgs p) {
                     const int e = (int)smx[ma_dma + 256 * i];
                     sa_ = kb_in ? e : 127;
                 }
-                float fa = 0.0f;
-                if (MXV == BLK) fa = __uint_as_float(sscale[cur_st][0][ma_byt + 16 * i]);
-                if (MXV == BLK && MODE == MODE_FWD) fa *= sbu;
 #pragma unroll
                 for (int j = 0; j < NJ; j++) {
-                    if (MXV == BLK) {
-                        const v4f_t part_sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            bf[j], af, v4f_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const float v = MODE == MODE_FWD ? part_sum[e]
-                                                             : part_sum[e] * sbv[MODE == MODE_WGRAD ? j : 0][e];
-                            acc[i][j][e] = fmaf(v, fa, acc[i][j][e]);
-                        }
-                    } else if (MX)
+                    if (MX)
                         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                             bf[j], af, acc[i][j], 0, 0, 0, sb_[j], 0, sa_);
                     else
@@ -882,20 +797,6 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm256_kernel(const GemmArgs p) {
     }
 }
 
-static int num_cus() {
-    static int cached[64] = {0};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    if (!cached[dev]) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-            n <= 0)
-            n = 256;
-        cached[dev] = n;
-    }
-    return cached[dev];
-}
-
 template <int FMT, int MODE, int MXV>
 static fp8q_status_t launch_gemm(GemmArgs p, hipStream_t stream) {
     p.nt_n = (int)((p.N + GT - 1) / GT);
@@ -921,7 +822,7 @@ static fp8q_status_t launch_gemm(GemmArgs p, hipStream_t stream) {
     // (127 registers, no spills): MX forward 455 / 406 / 392 us at 4 / 8 / 16 waves.  MX with
     // byte-loaded scales (the MX weight gradient): 8 waves (256 registers): 801 -> 713 us
     // against 4 waves; at 16 waves its registers spill inside the loop (1267 us).
-    constexpr int NW = MXV == MX_BYTES || MXV == BLK ? 8 : 16;
+    constexpr int NW = MXV == MX_BYTES ? 8 : 16;
     gemm256_kernel<FMT, MODE, MXV, NW><<<dim3((unsigned)grid), dim3(64 * NW), 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
@@ -1057,45 +958,4 @@ extern "C" fp8q_status_t fp8_mx_grouped_gemm(const uint8_t* a, int64_t lda, cons
                      fp8q_aligned(a_e8m0, 16) && fp8q_aligned(b_e8m0, 16);
     if (dma) return launch_gemm<FP8Q_E4M3FN, MODE_FWD, MX_DMA>(p, stream);
     return launch_gemm<FP8Q_E4M3FN, MODE_FWD, MX_BYTES>(p, stream);
-}
-
-extern "C" fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uint8_t* a, int64_t lda,
-                                                const float* a_scales, int64_t ld_sa, const uint8_t* b,
-                                                int64_t ldb, int64_t b_group_stride,
-                                                const float* b_scales, int64_t sb_n, int64_t sb_k,
-                                                int64_t sb_group_stride, const int32_t* offsets,
-                                                int32_t groups, int64_t M, int64_t N, int64_t K,
-                                                void* c, int64_t ldc, fp8q_out_t out_dtype,
-                                                void* workspace, size_t workspace_bytes,
-                                                hipStream_t stream) {
-    using namespace fp8q;
-    const bool fwd = mode == FP8Q_GEMM_FWD_MGROUPED;
-    if (!fwd && mode != FP8Q_GEMM_WGRAD_KGROUPED) return FP8Q_ERR_INVALID_ARG;
-    if (groups < 1 || M < 0 || N < 0 || K < 0 || ldc < N || (!offsets && groups != 1) || sb_n < 0 ||
-        sb_k < 0 || sb_group_stride < 0 || b_group_stride < 0)
-        return FP8Q_ERR_INVALID_ARG;
-    if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_FP32) return FP8Q_ERR_INVALID_ARG;
-    if (workspace && workspace_bytes < kGemmWorkspace) return FP8Q_ERR_WORKSPACE;
-    if (!fp8q_aligned(workspace, 4) || !fp8q_aligned(a_scales, 4) || !fp8q_aligned(b_scales, 4))
-        return FP8Q_ERR_INVALID_ARG;
-    if (lda < (fwd ? K : M) || ldb < (fwd ? K : M) || ld_sa < (fwd ? M : K)) return FP8Q_ERR_INVALID_ARG;
-    if (!fwd && (b_group_stride != 0 || sb_group_stride != 0 || sb_n != 1 || sb_k < N))
-        return FP8Q_ERR_INVALID_ARG;
-    GemmArgs p{};
-    p.out_f32 = out_dtype == FP8Q_OUT_FP32;
-    p.status = reinterpret_cast<int32_t*>(workspace);
-    if (N == 0 || (fwd ? M : K) == 0) return FP8Q_OK;
-    const bool read = (fwd ? K : M) > 0;
-    if (!c || (read && (!a || !b || !a_scales || !b_scales))) return FP8Q_ERR_INVALID_ARG;
-    if (lda % 16 || ldb % 16 || !fp8q_aligned(a, 16) || !fp8q_aligned(b, 16) || !offsets_fit(lda, ldb))
-        return FP8Q_ERR_UNSUPPORTED;
-    if (fwd && (K % 16 || b_group_stride % 16)) return FP8Q_ERR_UNSUPPORTED;
-    // a column block's factor is reached with a 32-bit byte offset
-    if (fwd && (N / GK + 1) > 0x1FFFFFFFLL / (sb_n > 0 ? sb_n : 1)) return FP8Q_ERR_UNSUPPORTED;
-    p.a = a; p.lda = lda; p.a_scales = a_scales; p.ld_sa = ld_sa; p.b = b; p.ldb = ldb;
-    p.bgs = b_group_stride; p.b_scales = b_scales; p.sb_n = sb_n; p.sb_k = sb_k;
-    p.sbgs = sb_group_stride; p.offsets = offsets; p.G = groups; p.M = M; p.N = N; p.K = K;
-    p.c = reinterpret_cast<uint8_t*>(c); p.ldc = ldc;
-    if (fwd) return launch_gemm<FP8Q_E4M3FN, MODE_FWD, BLK>(p, stream);
-    return launch_gemm<FP8Q_E4M3FN, MODE_WGRAD, BLK>(p, stream);
 }

@@ -6,6 +6,7 @@
 namespace fp8q {
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
+constexpr uint32_t OOB = 0x80000000u;  // an offset past any buffer: loads give zeros, stores are dropped
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ i32x4_t make_rsrc4(const void* base, uint32_t bytes) {
     const uint64_t a = (uint64_t)base;  // block-uniform: keep the descriptor in SGPRs
@@ -24,13 +25,20 @@ __device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t voff, uint32_t lds_
                  : "s"(lds_base), "v"(voff), "s"(rsrc)
                  : "memory", "m0");
 }
-#pragma clang diagnostic pop
+// The same with a wave-uniform offset on top of the lanes'.
+__device__ __forceinline__ void dma16_at(i32x4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds_base), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
+}
 __device__ __forceinline__ void dma4(i32x4_t rsrc, uint32_t voff, uint32_t lds_base) {
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(lds_base), "v"(voff), "s"(rsrc)
                  : "memory", "m0");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ void wait_vm0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {

@@ -30,7 +30,6 @@ typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 constexpr int MB = 128;           // weight factor block
 constexpr int MOE_MAX_T = 128;    // tokens of one call
 constexpr int MOE_MAX_E = 1024;   // experts
-constexpr uint32_t OOB = 0x80000000u;  // past any buffer: the load gives zeros
 constexpr int MOE_MAX_K = 32;     // experts of one token
 
 // 8 e4m3fn bytes as bf16 (exact: 4 significant bits, exponents -9 .. 8).
