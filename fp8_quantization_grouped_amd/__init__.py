@@ -417,17 +417,22 @@ def _rows_of(t: torch.Tensor, what: str, dtypes, shape, dev) -> None:
     raise ValueError(f"{what} must have unit stride in its last dimension")
 
 
-def _matrix(t: torch.Tensor, what: str, dtypes) -> torch.Size:
-    """Checks the first operand of a call, a matrix of any size; returns its shape."""
-    _want(t.dim() == 2, f"{what} must be a matrix")
-    shape = t.shape
-    _rows_of(t, what, dtypes, shape, t.device)
-    return shape
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Leading dimension of a matrix; the stride of a single or an empty row says nothing."""
+def _matrix(t: torch.Tensor, what: str, dtypes):
+    """Checks the first operand of a call, a matrix of any size; returns its rows, columns and
+    device."""
+    dev = t.device
+    if t.dtype not in dtypes or t.dim() != 2 or dev.type != "cuda":
+        _want(t.dim() == 2, f"{what} must be a matrix")
+        _rows_of(t, what, dtypes, t.shape, dev)
     rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    return rows, cols, dev
+
+
+def _ld(t: torch.Tensor, rows: int, cols: int) -> int:
+    """Leading dimension of a rows x cols matrix; the stride of a single or an empty row says
+    nothing."""
     return t.stride(0) if rows > 1 and cols > 0 else 0 if cols == 0 else max(t.stride(0), cols)
 
 
@@ -454,6 +459,8 @@ def _blocks(n: int) -> int:
 
 def _padded_bytes(rows: int, cols: int, dev) -> torch.Tensor:
     """[rows, cols] bytes whose rows start on 16 bytes, as the GEMMs take them."""
+    if cols % 16 == 0:
+        return torch.empty((rows, cols), dtype=torch.uint8, device=dev)
     return torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)[:, :cols]
 
 
@@ -471,18 +478,20 @@ def fp8_block_quant_rowwise(x: torch.Tensor, q: torch.Tensor | None = None,
     """x: bf16 [rows, cols] in blocks of 1 x 128.  Returns (q [rows, cols] e4m3fn bytes, scales
     float32 [ceil(cols/128), rows], the factors d with x ~ q * d).  Rows of a new q start on 16
     bytes."""
-    rows, cols = _matrix(x, "x", _BF16)
-    dev = x.device
+    rows, cols, dev = _matrix(x, "x", _BF16)
     if q is None:
         q = _padded_bytes(rows, cols, dev)
     else:
         _rows_of(q, "q", _BYTES, x.shape, dev)
+    blocks = -(-cols // BLOCK)
     if scales is None:
-        scales = torch.empty((_blocks(cols), rows), dtype=torch.float32, device=dev)
+        scales = torch.empty((blocks, rows), dtype=torch.float32, device=dev)
+        ld_s = rows
     else:
-        _rows_of(scales, "scales", _F32, (_blocks(cols), rows), dev)
-    _call("fp8_block_quant_rowwise", dev, x.data_ptr(), rows, cols, _ld(x), q.data_ptr(), _ld(q),
-          scales.data_ptr(), _ld(scales) if cols else rows)
+        _rows_of(scales, "scales", _F32, (blocks, rows), dev)
+        ld_s = _ld(scales, blocks, rows)
+    _call("fp8_block_quant_rowwise", dev, x.data_ptr(), rows, cols, _ld(x, rows, cols),
+          q.data_ptr(), _ld(q, rows, cols), scales.data_ptr(), ld_s)
     return q, scales
 
 
@@ -493,8 +502,7 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
     [ceil(cols/128), rows]) as fp8_block_quant_rowwise would, (q_t [cols, rows], s_cols float32
     [ceil(rows/128), cols]) in blocks of 128 rows of a column).  transposed_only: the second pair
     alone is made, and the first is (None, None)."""
-    rows, cols = _matrix(x, "x", _BF16)
-    dev = x.device
+    rows, cols, dev = _matrix(x, "x", _BF16)
     f32 = torch.float32
     if transposed_only:
         _want(q is None and s_rows is None, "transposed_only takes no q and s_rows")
@@ -508,7 +516,8 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
             s_rows = torch.empty((_blocks(cols), rows), dtype=f32, device=dev)
         else:
             _rows_of(s_rows, "s_rows", _F32, (_blocks(cols), rows), dev)
-        row_args = (q.data_ptr(), _ld(q), s_rows.data_ptr(), _ld(s_rows) if cols else rows)
+        row_args = (q.data_ptr(), _ld(q, rows, cols), s_rows.data_ptr(),
+                    max(_ld(s_rows, _blocks(cols), rows), rows))
     if q_t is None:
         q_t = _padded_bytes(cols, rows, dev)
     else:
@@ -517,8 +526,9 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
         s_cols = torch.empty((_blocks(rows), cols), dtype=f32, device=dev)
     else:
         _rows_of(s_cols, "s_cols", _F32, (_blocks(rows), cols), dev)
-    _call("fp8_block_quant_dual", dev, x.data_ptr(), rows, cols, _ld(x), *row_args, q_t.data_ptr(),
-          _ld(q_t) if cols else rows, s_cols.data_ptr(), _ld(s_cols) if rows else cols)
+    _call("fp8_block_quant_dual", dev, x.data_ptr(), rows, cols, _ld(x, rows, cols), *row_args,
+          q_t.data_ptr(), max(_ld(q_t, cols, rows), rows), s_cols.data_ptr(),
+          max(_ld(s_cols, _blocks(rows), cols), cols))
     return (q, s_rows), (q_t, s_cols)
 
 
@@ -527,26 +537,26 @@ def fp8_block_quant_weights(w: torch.Tensor, experts: int, q: torch.Tensor | Non
     """w: bf16 [experts * rows, cols], each expert's matrix in blocks of 128 x 128.  Returns (q
     [experts * rows, cols], q_t [cols, experts * rows] with the experts' transposes side by side,
     scales float32 [experts, ceil(rows/128), ceil(cols/128)], which serve both)."""
-    _matrix(w, "w", _BF16)
-    _want(experts > 0 and w.shape[0] % experts == 0, "w must hold experts matrices of equal size")
-    rows, cols = w.shape[0] // experts, w.shape[1]
-    dev = w.device
+    total, cols, dev = _matrix(w, "w", _BF16)
+    _want(experts > 0 and total % experts == 0, "w must hold experts matrices of equal size")
+    rows = total // experts
     if q is None:
-        q = _padded_bytes(*w.shape, dev)
+        q = _padded_bytes(total, cols, dev)
     else:
         _rows_of(q, "q", _BYTES, w.shape, dev)
     if q_t is None:
-        q_t = _padded_bytes(cols, w.shape[0], dev)
+        q_t = _padded_bytes(cols, total, dev)
     else:
-        _rows_of(q_t, "q_t", _BYTES, (cols, w.shape[0]), dev)
+        _rows_of(q_t, "q_t", _BYTES, (cols, total), dev)
     shape = (experts, _blocks(rows), _blocks(cols))
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         _rows_of(scales, "scales", _F32, shape, dev)
         _want(scales.is_contiguous(), "scales must be contiguous")
-    _call("fp8_block_quant_weights", dev, w.data_ptr(), experts, rows, cols, _ld(w), q.data_ptr(),
-          _ld(q), q_t.data_ptr(), _ld(q_t) if cols else w.shape[0], scales.data_ptr())
+    _call("fp8_block_quant_weights", dev, w.data_ptr(), experts, rows, cols, _ld(w, total, cols),
+          q.data_ptr(), _ld(q, total, cols), q_t.data_ptr(), max(_ld(q_t, cols, total), total),
+          scales.data_ptr())
     return q, q_t, scales
 
 
@@ -565,41 +575,51 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
     from a given workspace."""
     _want(mode in (GEMM_FWD_MGROUPED, GEMM_WGRAD_KGROUPED), "unknown mode")
     fwd = mode == GEMM_FWD_MGROUPED
-    rows, inner = _matrix(a, "a", _BYTES)  # forward M, K; weight gradient K, M
-    dev = a.device
-    groups = 1
+    rows, inner, dev = _matrix(a, "a", _BYTES)  # forward M, K; weight gradient K, M
+    groups, off = 1, None
     if offsets is not None:
         _want(offsets.dim() == 1, "offsets must have one dimension")
         groups = offsets.shape[0]
         _rows_of(offsets, "offsets", _I32T, (groups,), dev)
+        off = offsets.data_ptr()
     _want(b.dim() == (3 if fwd else 2), "b must be [groups, N, K] in the forward, [N, M] else")
     N = b.shape[-2]
     _rows_of(b, "b", _BYTES, (groups, N, inner) if fwd else (N, inner), dev)
-    kb = _blocks(inner)
+    kb = -(-inner // BLOCK)
     _rows_of(a_scales, "a_scales", _F32, (kb, rows), dev)
-    lda, ld_sa = _ld(a), max(_ld(a_scales), rows) if kb else rows
+    ld_sa = max(a_scales.stride(0), rows) if kb > 1 else rows
     if fwd:
-        _factors(b_scales, "b_scales", (groups, _blocks(N), kb), dev)
+        nb = -(-N // BLOCK)
+        _factors(b_scales, "b_scales", (groups, nb, kb), dev)
         # a dimension of one entry has no stride that means anything
-        bgs = b.stride(0) if groups > 1 else 0
-        ldb = b.stride(1) if N > 1 else max(b.stride(1), inner)
-        sbg, sbn, sbk = (d if n > 1 else 0 for d, n in zip(b_scales.stride(), b_scales.shape))
+        sbg, sbn, sbk = b_scales.stride()
+        bgs, ldb, _ = b.stride()
+        if groups == 1:
+            bgs = sbg = 0
+        if nb <= 1:
+            sbn = 0
+        if kb <= 1:
+            sbk = 0
+        if N <= 1:
+            ldb = max(ldb, inner)
         M, K, shape = rows, inner, (rows, N)
     else:
         _rows_of(b_scales, "b_scales", _F32, (kb, N), dev)
-        bgs, ldb, sbg, sbn, sbk = 0, _ld(b), 0, 1, max(_ld(b_scales), N) if kb else N
+        bgs, ldb, sbg, sbn = 0, _ld(b, N, inner), 0, 1
+        sbk = max(b_scales.stride(0), N) if kb > 1 else N
         M, K, shape = inner, rows, (groups, rows, N)
     if c is None:
         _want(out_dtype in _OUT, "the output must be bfloat16 or float32")
         c = torch.empty(shape, dtype=out_dtype, device=dev)
+        ldc = N
     else:
         c = _gemm_out(c, shape, out_dtype, dev)
         _want(c.device == dev, "c must be on the operands' GPU")
+        ldc = c.stride(-2) if c.shape[-2] > 1 else max(c.stride(-2), N)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    _call("fp8_block_grouped_gemm", dev, mode, a.data_ptr(), lda, a_scales.data_ptr(), ld_sa,
-          b.data_ptr(), ldb, bgs, b_scales.data_ptr(), sbn, sbk, sbg,
-          None if offsets is None else offsets.data_ptr(), groups, M, N, K, c.data_ptr(),
-          c.stride(-2) if c.shape[-2] > 1 else max(c.stride(-2), N), _OUT[c.dtype], ws, ws_bytes)
+    _call("fp8_block_grouped_gemm", dev, mode, a.data_ptr(), _ld(a, rows, inner),
+          a_scales.data_ptr(), ld_sa, b.data_ptr(), ldb, bgs, b_scales.data_ptr(), sbn, sbk, sbg,
+          off, groups, M, N, K, c.data_ptr(), ldc, _OUT[c.dtype], ws, ws_bytes)
     return c
 
 
@@ -621,8 +641,7 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     """The experts of each token: x bf16 [T, H], router bf16 [E, H], bias float32 [E] (added to the
     scores for the choice alone).  scoring: "softmax" or "sigmoid".  Returns (ids int32 [T, top_k],
     weights float32 [T, top_k]) in descending order; ties go to the lowest index."""
-    T, H = _matrix(x, "x", _BF16)
-    dev = x.device
+    T, H, dev = _matrix(x, "x", _BF16)
     E = router.shape[0]
     _rows_of(router, "router", _BF16, (E, H), dev)
     _want(scoring in _SCORING, "scoring must be softmax or sigmoid")
@@ -640,8 +659,10 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
         _rows_of(weights, "weights", _F32, (T, top_k), dev)
         _want(weights.is_contiguous(), "weights must be contiguous")
     if workspace is None:
-        workspace = torch.empty((moe_route_workspace_size(T, H, E),), dtype=torch.uint8, device=dev)
-    _call("moe_route", dev, x.data_ptr(), T, H, _ld(x), router.data_ptr(), E, _ld(router),
+        workspace = torch.empty((lib().moe_route_workspace_size(T, H, E),), dtype=torch.uint8,
+                                device=dev)
+    _call("moe_route", dev, x.data_ptr(), T, H, _ld(x, T, H), router.data_ptr(), E,
+          _ld(router, E, H),
           None if bias is None else bias.data_ptr(), _SCORING[scoring], top_k, int(renormalize),
           scale, ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return ids, weights
@@ -656,9 +677,17 @@ def _expert_weights(w, s, what, shape, dev):
     _rows_of(w, what, _BYTES, shape, dev)
     E, n, k = shape
     _factors(s, f"the factors of {what}", (E, _blocks(n), _blocks(k)), dev)
-    sg, sn, sk = (d if m > 1 else 0 for d, m in zip(s.stride(), s.shape))
-    return (w.data_ptr(), w.stride(1) if n > 1 else max(w.stride(1), k), w.stride(0) if E > 1 else 0,
-            s.data_ptr(), sn, sk, sg)
+    sg, sn, sk = s.stride()
+    gs, ld, _ = w.stride()
+    if E == 1:
+        gs = sg = 0
+    if n <= BLOCK:
+        sn = 0
+        if n <= 1:
+            ld = max(ld, k)
+    if k <= BLOCK:
+        sk = 0
+    return w.data_ptr(), ld, gs, s.data_ptr(), sn, sk, sg
 
 
 def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
@@ -668,8 +697,7 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     weights float32 [T, top_k] (moe_route's); w13 [E, 2I, H] and w2 [E, H, I] e4m3fn bytes with
     scales [E, ceil(2I/128), ceil(H/128)] and [E, ceil(H/128), ceil(I/128)]
     (fp8_block_quant_weights').  Returns y bf16 [T, H].  An id outside [0, E) adds nothing."""
-    T, H = _matrix(x, "x", _BF16)
-    dev = x.device
+    T, H, dev = _matrix(x, "x", _BF16)
     _want(ids.dim() == 2, "ids must be a matrix")
     top_k = ids.shape[1]
     _rows_of(ids, "ids", _I32T, (T, top_k), dev)
@@ -686,7 +714,7 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     if workspace is None:
         need = fp8_moe_few_tokens_workspace_size(T, H, I, top_k)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    _call("fp8_moe_few_tokens", dev, x.data_ptr(), T, H, _ld(x), ids.data_ptr(),
-          weights.data_ptr(), top_k, *args13, *args2, E, I, y.data_ptr(), _ld(y),
+    _call("fp8_moe_few_tokens", dev, x.data_ptr(), T, H, _ld(x, T, H), ids.data_ptr(),
+          weights.data_ptr(), top_k, *args13, *args2, E, I, y.data_ptr(), _ld(y, T, H),
           workspace.data_ptr(), workspace.nbytes)
     return y

@@ -209,14 +209,15 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
     i32x4_t ra, rb;
     uint32_t oa[NP], ob[NP];
     Tile src;
-    const int part_row = wave * (8 * NP) + (lane >> 3);
     auto aim = [&](const Tile& x) {
         src = x;
         ra = make_rsrc4(p.a + (int64_t)x.row * p.lda, (uint32_t)(x.rows * p.lda));
         rb = make_rsrc4(p.b + (FWD ? (int64_t)x.g * p.bgs : 0) + (int64_t)x.n0 * p.ldb, (uint32_t)(x.cols * p.ldb));
+        int l = lane;
+        asm volatile("" : "+v"(l));
 #pragma unroll
         for (int i = 0; i < NP; i++) {
-            const int row = part_row + 8 * i, ch = lane & 7;
+            const int row = wave * (8 * NP) + 8 * i + (l >> 3), ch = l & 7;
             oa[i] = row < x.rows ? (uint32_t)row * (uint32_t)p.lda + 16 * (ch ^ swz(row)) : OOB;
             ob[i] = row < x.cols ? (uint32_t)row * (uint32_t)p.ldb + 16 * (ch ^ swzB(row)) : OOB;
         }
@@ -239,9 +240,11 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
                 dma16_at(rb, ob[i], kpos, at_b + i * 1024);
             }
         } else {  // chunks outside the range read as zeros
+            int l = lane;  // rare: what follows is formed here, not held through the steps
+            asm volatile("" : "+v"(l));
 #pragma unroll
             for (int i = 0; i < NP; i++) {
-                const int row = part_row + 8 * i, ch = lane & 7;
+                const int row = wave * (8 * NP) + 8 * i + (l >> 3), ch = l & 7;
                 const int pa = kpos + 16 * (ch ^ swz(row)), pb = kpos + 16 * (ch ^ swzB(row));
                 const uint32_t xa = pa < src.k_hi && pa + 16 > src.k_lo ? oa[i] + kpos : OOB;
                 const uint32_t xb = pb < src.k_hi && pb + 16 > src.k_lo ? ob[i] + kpos : OOB;
@@ -271,6 +274,15 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
         for (int i = 0; i < MI; i++)
 #pragma unroll
             for (int j = 0; j < NJ; j++) acc[i][j] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+        // sums of the row multiplied last, waiting to be added times f (forward: across steps too)
+        v4f_t sum[NJ];
+        float f = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; j++) sum[j] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+        auto add_sums = [&](int i, int j, const v4f_t* sbv) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[i][j][e] = fmaf(FWD ? sum[j][e] : sum[j][e] * sbv[FWD ? 0 : j][e], f, acc[i][j][e]);
+        };
         bool have_next = false;
         for (int s = 0; s < cur.steps; s++, st ^= 1) {
             const int kpos = cur.k0 + s * GK;
@@ -280,14 +292,16 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
                 // the range cuts, in both operands: such a byte may be a NaN code
                 __syncthreads();
                 const int lo = cur.k_lo - kpos, hi = cur.k_hi - kpos;
-                if (t < 2 * T) {
-                    const int row = t & (T - 1);
-                    uint8_t* side = smem[st][t / T];
+                int tt = t;
+                asm volatile("" : "+v"(tt));
+                if (tt < 2 * T) {
+                    const int row = tt & (T - 1);
+                    uint8_t* side = smem[st][tt / T];
 #pragma unroll
                     for (int ch = 0; ch < 8; ch++) {
                         const int b0 = 16 * ch;
                         if ((lo > b0 && lo < b0 + 16) || (hi > b0 && hi < b0 + 16)) {
-                            uint4* q = reinterpret_cast<uint4*>(side + (t < T ? lds_off(row, ch) : lds_offB(row, ch)));
+                            uint4* q = reinterpret_cast<uint4*>(side + (tt < T ? lds_off(row, ch) : lds_offB(row, ch)));
                             uint4 w = *q;
                             w.x &= keep_mask4(lo, hi, b0);
                             w.y &= keep_mask4(lo, hi, b0 + 4);
@@ -300,49 +314,72 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
             }
             __syncthreads();
             if (s == 0) have_next = tile_start(nxt);
-            if (s + 1 < cur.steps) {
-                issue(kpos + GK, st ^ 1);
-            } else if (have_next) {
-                tile_finish(nxt);
-                if (nxt.steps > 0) {
-                    aim(nxt);
-                    issue(nxt.k0, st ^ 1);
+            int to_issue = kpos + GK;
+            if (s + 1 == cur.steps) {
+                to_issue = -1;
+                if (have_next) {
+                    tile_finish(nxt);
+                    if (nxt.steps > 0) {
+                        aim(nxt);
+                        to_issue = nxt.k0;
+                    }
                 }
             }
+            if (to_issue >= 0) issue(to_issue, st ^ 1);
             const uint8_t* As = smem[st][0];
             const uint8_t* Bs = smem[st][1];
             const float* sa = &sscale[st][0][wm * WM + lr];
             const float* sb = &sscale[st][1][wn * WN];
-            v8i_t bf[NJ];
-            v4f_t sbv[FWD ? 1 : NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; j++) {
+            // The order below is the order of issue (no scheduling across the barriers): while a
+            // matrix instruction runs, the vector unit adds the sums that the same column block gave
+            // for the row before, and the next row's fragment is read.
+            v8i_t bf[NJ], af[3];
+            float fa[MI];
+            auto load_b = [&](int j) {
                 const int o = 32 * GK * (j >> 1) + 4 * GK * (j & 1);
                 bf[j] = two_chunks(Bs + fb0 + o, Bs + fb1 + o);
-                if (!FWD) sbv[FWD ? 0 : j] = *reinterpret_cast<const v4f_t*>(sb + 32 * (j >> 1) + 8 * lq + 4 * (j & 1));
-            }
+            };
+            auto load_a = [&](int i) {
+                af[i % 3] = two_chunks(As + fa0 + 16 * GK * i, As + fa1 + 16 * GK * i);
+            };
+            load_b(0);
+            load_a(0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 1; j < NJ; j++) load_b(j);
+            load_a(1);
+#pragma unroll
+            for (int i = 0; i < MI; i++) fa[i] = sa[16 * i];
             const float sbu = FWD ? sb[0] : 1.0f;  // a wave's columns lie in one weight block
-            v4f_t sum[2][NJ];
-            float f[2];
+            v4f_t sbv[FWD ? 1 : NJ];
+            if (!FWD) {
 #pragma unroll
-            for (int i = 0; i <= MI; i++) {
-                if (i < MI) {
-                    const v8i_t af = two_chunks(As + fa0 + 16 * GK * i, As + fa1 + 16 * GK * i);
-                    f[i & 1] = sa[16 * i] * sbu;
+                for (int j = 0; j < NJ; j++) sbv[FWD ? 0 : j] = *reinterpret_cast<const v4f_t*>(sb + 32 * (j >> 1) + 8 * lq + 4 * (j & 1));
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int j = 0; j < NJ; j++)
-                        sum[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            bf[j], af, v4f_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+            for (int i = 0; i < MI; i++) {
+                if (i + 2 < MI) load_a(i + 2);
+                const float f_new = FWD ? fa[i] * sbu : fa[i];
+#pragma unroll
+                for (int j = 0; j < NJ; j++) {
+                    if (FWD || i > 0) add_sums(i > 0 ? i - 1 : MI - 1, j, sbv);
+                    sum[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        bf[j], af[i % 3], v4f_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if (i > 0) {
+                f = f_new;
+            }
+            if (!FWD) {
 #pragma unroll
-                    for (int j = 0; j < NJ; j++)
+                for (int j = 0; j < NJ; j++) add_sums(MI - 1, j, sbv);
+            }
+        }
+        if (FWD && cur.steps > 0) {
 #pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const float v = sum[(i - 1) & 1][j][e];
-                            acc[i - 1][j][e] = fmaf(FWD ? v : v * sbv[FWD ? 0 : j][e], f[(i - 1) & 1], acc[i - 1][j][e]);
-                        }
-                }
+            for (int j = 0; j < NJ; j++) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[MI - 1][j][e] = fmaf(sum[j][e], f, acc[MI - 1][j][e]);
             }
         }
         if (cur.steps == 0) {
@@ -437,9 +474,6 @@ template <int MODE>
 static fp8q_status_t pick_block_gemm(const BlockGemmArgs& p, hipStream_t stream) {
     const int64_t rows = MODE == MODE_FWD ? p.M : (int64_t)p.G * p.K;
     const int64_t tiles = (rows + 255) / 256 * ((p.N + 255) / 256);
-#ifdef FORCE_T
-    return launch_block_gemm<MODE, FORCE_T>(p, stream);
-#endif
     return tiles < 256 ? launch_block_gemm<MODE, 128>(p, stream) : launch_block_gemm<MODE, 256>(p, stream);
 }
 
