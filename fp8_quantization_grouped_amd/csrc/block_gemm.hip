@@ -492,7 +492,9 @@ static fp8q_status_t launch_block_gemm(BlockGemmArgs p, hipStream_t stream) {
         return FP8Q_OK;
     }
     const int64_t tiles = MODE == MODE_FWD ? ((int64_t)(p.M + T - 1) / T + p.G) * p.nt_n : (int64_t)p.G * p.nt_k * p.nt_n;
-    if (tiles >= 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
+    // offsets that go up and down can make every group as long as M
+    const int64_t most = MODE == MODE_FWD ? (int64_t)p.G * ((p.M + T - 1) / T) * p.nt_n : tiles;
+    if (tiles >= 0x7FFFFFFFLL || most >= 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
     int64_t grid = (int64_t)num_cus() * (T == 256 ? 1 : 2);
     if (tiles < grid) grid = tiles;
     block_gemm_kernel<MODE, T><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(p);

@@ -392,7 +392,8 @@ fp8q_status_t fp8_block_quant_weights(const uint16_t* w, int64_t experts, int64_
  * offsets check is then not reported (the kernel uses clamped offsets either way); otherwise
  * fp8_grouped_gemm_workspace_size bytes.  Sums: each block's products on the matrix cores (see
  * Accuracy at fp8_grouped_gemm) from zero, times the factors into an fp32 accumulator.
- * Limits (FP8Q_ERR_UNSUPPORTED): as for fp8_grouped_gemm, and (N/128 + 1) * sb_n < 2^29. */
+ * Limits (FP8Q_ERR_UNSUPPORTED): as for fp8_grouped_gemm (M, N, K up to 2^31 - 256), (N/128 + 1) *
+ * sb_n <= 2^29, and in the forward groups * ceil(M/128) * ceil(N/128) < 2^31. */
 fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uint8_t* a, int64_t lda,
                                      const float* a_scales, int64_t ld_sa, const uint8_t* b,
                                      int64_t ldb, int64_t b_group_stride, const float* b_scales,
@@ -437,7 +438,8 @@ fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, c
  *   16-byte aligned.
  * Three kernels; every sum has a fixed order.  Limits (FP8Q_ERR_UNSUPPORTED): T <= 128 (the grouped
  * product takes more), E <= 1024, top_k <= 32, H and I multiples of 16, ld_x a multiple of 8, the
- * weights' strides multiples of 16, x, w13 and w2 16-byte aligned.  T == 0 is a no-op. */
+ * weights' strides multiples of 16, x, w13 and w2 16-byte aligned, ld13 and ld2 < 2^26, T * ld_x <
+ * 2^30, T * top_k * I < 2^29.  T == 0 is a no-op. */
 size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t H, int64_t I, int32_t top_k);
 fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x,
                                  const int32_t* ids, const float* weights, int32_t top_k,
