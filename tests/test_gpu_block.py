@@ -343,3 +343,27 @@ def test_other_stream_and_graph(fq):
         torch.cuda.synchronize()
         assert torch.equal(y, want[i])
         assert torch.equal(step(xs[(i + 1) % 4]), want[(i + 1) % 4])
+
+
+def test_sizes_past_32_bits(fq):
+    """Element offsets past 2^31 and byte offsets past 2^32: the last rows and columns of a long
+    activation, and the last group's weights, against their own small calls."""
+    rows, cols = 270000, 8192  # 2.2e9 elements
+    x = torch.randn(rows // 1000, cols, device=DEV).to(torch.bfloat16).repeat(1000, 1)
+    x[-300:] *= 3
+    (q, d), (q_t, d_t) = fq.fp8_block_quant_dual(x)
+    at = (rows - 300) // 128 * 128
+    (q2, d2), (q_t2, d_t2) = fq.fp8_block_quant_dual(x[at:])
+    assert torch.equal(q[at:], q2) and torch.equal(d[:, at:], d2)
+    assert torch.equal(q_t[:, at:], q_t2) and torch.equal(d_t[at // 128:], d_t2)
+    qr, dr = fq.fp8_block_quant_rowwise(x)
+    assert torch.equal(qr[at:], q2) and torch.equal(dr, d)
+    del x, qr, dr, q_t, d_t
+    # the long operand's last rows, times the last of groups that lie past 4 GiB
+    G, N = 70, 8192
+    w = torch.randint(0, 120, (G, N, cols), dtype=torch.uint8, device=DEV)
+    wd = torch.rand(G, N // 128, cols // 128, device=DEV)
+    off = torch.full((G,), 0, dtype=torch.int32, device=DEV)
+    off[-1] = rows - at
+    y = fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, q[at:], d[:, at:], w, wd, off)
+    assert torch.equal(y, fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, q2, d2, w[-1:].clone(), wd[-1:].clone()))

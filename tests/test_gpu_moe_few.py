@@ -286,3 +286,18 @@ def test_no_tokens(fq):
     ids, weights = fq.moe_route(x, normal(2, E, H), 2)
     assert ids.shape == (0, 2)
     assert fq.fp8_moe_few_tokens(x, ids, weights, *layer(fq, 3, E, H, I)).shape == (0, H)
+
+
+def test_experts_past_32_bits(fq):
+    """The last experts' weights start past 4 GiB."""
+    T, H, I, E = 3, 4096, 2048, 300  # w13: 300 x 16 MiB
+    w13 = torch.randint(0, 120, (E, 2 * I, H), dtype=torch.uint8, device=DEV)
+    s13 = torch.rand(E, 2 * I // 128, H // 128, device=DEV) * 1e-4
+    w2 = torch.randint(0, 120, (E, H, I), dtype=torch.uint8, device=DEV)
+    s2 = torch.rand(E, H // 128, I // 128, device=DEV) * 1e-3
+    x = normal(1, T, H)
+    ids = torch.tensor([[E - 1, E - 2]] * T, dtype=torch.int32, device=DEV)
+    weights = torch.full((T, 2), 0.5, device=DEV)
+    y = fq.fp8_moe_few_tokens(x, ids, weights, w13, s13, w2, s2)
+    want = fq.fp8_moe_few_tokens(x, ids - (E - 2), weights, w13[-2:].clone(), s13[-2:].clone(), w2[-2:].clone(), s2[-2:].clone())
+    assert torch.equal(y, want) and bool(y.isfinite().all()) and bool(y.any())
