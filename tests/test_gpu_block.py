@@ -367,3 +367,29 @@ def test_sizes_past_32_bits(fq):
     off[-1] = rows - at
     y = fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, q[at:], d[:, at:], w, wd, off)
     assert torch.equal(y, fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, q2, d2, w[-1:].clone(), wd[-1:].clone()))
+
+
+def test_outputs_past_the_last_level_cache(fq):
+    """Outputs of more than 128 MiB, which are stored past the cache, hold the bits that the same rows and
+    groups have in small calls; ragged in both directions."""
+    M, N, K = 8195, 8200, 272
+    q, d = fq.fp8_block_quant_rowwise(values(5, M, K))
+    wq, _, wd = fq.fp8_block_quant_weights(values(6, N, K, 0.05), 1)
+    b = wq.unflatten(0, (1, N))
+    y = fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, q, d, b, wd)
+    for at in (0, 4096, 8192):
+        rows = slice(at, min(at + 259, M))
+        part = fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, q[rows], d[:, rows].contiguous(), b, wd)
+        assert torch.equal(y[rows], part)
+    # weight gradient: 9 groups of 2808 x 2816, one without rows
+    G, KK, NN, T = 9, 2808, 2816, 1100
+    _, (a_t, a_s) = fq.fp8_block_quant_dual(values(7, T, KK))
+    _, (g_t, g_s) = fq.fp8_block_quant_dual(values(8, T, NN))
+    ends = [130, 256, 256, 300, 511, 700, 800, 1000, 1100]
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    dw = fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, g_t, g_s, a_t, a_s, off)
+    assert dw.shape[0] == G and dw.numel() * 2 > 128 << 20 and not bool(dw[2].any())
+    for g in (0, 1, 3, 8):
+        one = torch.tensor([ends[g - 1] if g else 0, ends[g]], dtype=torch.int32, device=DEV)
+        part = fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, g_t, g_s, a_t, a_s, one)
+        assert torch.equal(dw[g], part[1])
