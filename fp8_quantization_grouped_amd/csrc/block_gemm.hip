@@ -313,19 +313,21 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
             wait_vm0();
             if (!FWD && (kpos < cur.k_lo || kpos + GK > cur.k_hi)) {
                 // zero the bytes of other groups' tokens (or of the padding past M) in the chunks that
-                // the range cuts, in both operands: such a byte may be a NaN code
-                barrier();
+                // the range cuts, in both operands: such a byte may be a NaN code.  Each wave does the
+                // rows that it loaded, so its own wait suffices.
                 const int lo = cur.k_lo - kpos, hi = cur.k_hi - kpos;
-                int tt = t;
-                asm volatile("" : "+v"(tt));
-                if (tt < 2 * T) {
-                    const int row = tt & (T - 1);
-                    uint8_t* side = smem[st][tt / T];
+                int l = lane;
+                asm volatile("" : "+v"(l));
+                constexpr int OWN = 8 * NP;
+                if (l < 2 * OWN) {
+                    const int row = wave * OWN + (l & (OWN - 1));
+                    const bool in_a = l < OWN;
+                    uint8_t* side = smem[st][in_a ? 0 : 1];
 #pragma unroll
                     for (int ch = 0; ch < 8; ch++) {
                         const int b0 = 16 * ch;
                         if ((lo > b0 && lo < b0 + 16) || (hi > b0 && hi < b0 + 16)) {
-                            uint4* q = reinterpret_cast<uint4*>(side + (tt < T ? lds_off(row, ch) : lds_offB(row, ch)));
+                            uint4* q = reinterpret_cast<uint4*>(side + (in_a ? lds_off(row, ch) : lds_offB(row, ch)));
                             uint4 w = *q;
                             w.x &= keep_mask4(lo, hi, b0);
                             w.y &= keep_mask4(lo, hi, b0 + 4);
@@ -534,7 +536,7 @@ static fp8q_status_t pick_block_gemm(const BlockGemmArgs& p, hipStream_t stream)
     // 2048 47 against 53 us, weight gradient of 8 groups of 1024 x 2048 28 against 31 us
     const int64_t rows = MODE == MODE_FWD ? p.M : (int64_t)p.G * p.K;
     const int64_t tiles = (rows + 255) / 256 * ((p.N + 255) / 256);
-        return tiles < 256 ? launch_block_gemm<MODE, 128>(p, stream) : launch_block_gemm<MODE, 256>(p, stream);
+    return tiles < 256 ? launch_block_gemm<MODE, 128>(p, stream) : launch_block_gemm<MODE, 256>(p, stream);
 }
 
 }  // namespace fp8q
