@@ -523,7 +523,7 @@ static fp8q_status_t launch_block_gemm(BlockGemmArgs p, hipStream_t stream) {
     const int64_t most = MODE == MODE_FWD ? (int64_t)p.G * ((p.M + T - 1) / T) * p.nt_n : tiles;
     if (tiles >= 0x7FFFFFFFLL || most >= 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
     int64_t grid = (int64_t)num_cus() * (T == 256 ? 1 : 2);
-    if (tiles < grid) grid = tiles;
+    if (tiles < grid) grid = (tiles + 7) / 8 * 8;  // whole rounds of the XCDs
     block_gemm_kernel<MODE, T><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
