@@ -453,28 +453,38 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
                     }
                 }
             } else {
-                // any N, ldc and alignment: 16 rows at a time through LDS (the wave's own piece of
-                // the last step's stage, which the loads reach after the next barrier), so that a
-                // store's lanes write neighbouring columns
-                barrier();
-                float* own = reinterpret_cast<float*>(&smem[st ^ 1][0][0] + wave * (16 * WN * 4));
+                // any N, ldc and alignment: the same 8 columns of a lane in stores that need no alignment
+                // but the element's, one by one where the tile's last columns cut them
+                typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+                typedef __attribute__((address_space(1))) uint8_t* gptr;
+                const gptr base = (gptr)(uintptr_t)(p.c + (row0 * p.ldc + cur.n0) * ESZ);
 #pragma unroll
                 for (int i = 0; i < MI; i++) {
+                    const int row = wm * WM + 16 * i + elr;
+                    if (row >= cur.rows) continue;
 #pragma unroll
-                    for (int j = 0; j < NJ; j++)
-                        *reinterpret_cast<v4f_t*>(own + elr * WN + 32 * (j >> 1) + 8 * elq + 4 * (j & 1)) = acc[i][j];
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll 4
-                    for (int q = 0; q < 16 * WN / 64; q++) {
-                        const int idx = q * 64 + el, row = wm * WM + 16 * i + idx / WN, col = wn * WN + idx % WN;
-                        const uint32_t off = row < cur.rows && col < cur.cols ? row * ldc + col * ESZ : OOB;
-                        const float v = own[idx];
-                        if (F32)
-                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), rc, off, 0, 0);
-                        else
-                            __builtin_amdgcn_raw_buffer_store_b16((short)(pack_bf16x2(v, 0.0f) & 0xFFFFu), rc, off, 0, 0);
+                    for (int jp = 0; jp < NJ / 2; jp++) {
+                        const int col = wn * WN + 32 * jp + 8 * elq;
+                        const gptr at = base + (uint32_t)row * ldc + (uint32_t)col * ESZ;
+                        const v4f_t v = acc[i][2 * jp], w = acc[i][2 * jp + 1];
+                        if (col + 8 <= cur.cols) {
+                            if (F32) {
+                                *(__attribute__((address_space(1))) i32x4_any*)at = __builtin_bit_cast(i32x4_t, v);
+                                *(__attribute__((address_space(1))) i32x4_any*)(at + 16) = __builtin_bit_cast(i32x4_t, w);
+                            } else {
+                                *(__attribute__((address_space(1))) i32x4_any*)at =
+                                    i32x4_t{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3]), (int)pack_bf16x2(w[0], w[1]), (int)pack_bf16x2(w[2], w[3])};
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; e++) {
+                                const float x = e < 4 ? v[e & 3] : w[e & 3];
+                                if (col + e >= cur.cols) continue;
+                                if (F32) ((__attribute__((address_space(1))) float*)at)[e] = x;
+                                else ((__attribute__((address_space(1))) uint16_t*)at)[e] = (uint16_t)pack_bf16x2(x, 0.0f);
+                            }
+                        }
                     }
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 }
             }
         };
