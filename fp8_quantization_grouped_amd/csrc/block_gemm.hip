@@ -55,21 +55,23 @@ __device__ __forceinline__ v8i_t two_chunks(const uint8_t* lo, const uint8_t* hi
     return v8i_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
-template <int MODE, int T>
-__global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const BlockGemmArgs p) {
+template <int MODE, int TM, int TN, int NS>
+__global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(const BlockGemmArgs p) {
     constexpr bool FWD = MODE == MODE_FWD;
-    constexpr int STAGE = T * GK, NP = T / 64;     // bytes of one operand tile; its loads per wave
-    constexpr int WM = T / 2, WN = T / 4;          // a wave's rows and columns
+    constexpr int STAGE_A = TM * GK, STAGE_B = TN * GK, STAGE = STAGE_A + STAGE_B;  // bytes of a step's operands
+    constexpr int NA = TM / 64, NB = TN / 64;      // each wave's loads of either
+    constexpr int WC = TN > 64 ? 4 : 2;            // waves side by side
+    constexpr int WM = TM * WC / 8, WN = TN / WC;  // a wave's rows and columns
     constexpr int MI = WM / 16, NJ = WN / 16;
     constexpr int NT = 512;
-    __shared__ __align__(16) uint8_t smem[2][2][STAGE];
-    __shared__ __align__(16) float sscale[2][2][T];  // by stage: factors of the tile's rows, columns
-    __shared__ int s_pref[FWD ? GMAX + 1 : 1];       // forward: row tiles before each group
-    __shared__ unsigned short s_perm[FWD ? 1 : GMAX];  // weight gradient: groups, most steps first
-    __shared__ int s_busy;                             // and how many have any
+    __shared__ __align__(16) uint8_t smem[NS][STAGE];
+    __shared__ __align__(16) float sscale[NS][TM + TN];  // by stage: factors of the tile's rows, columns
+    __shared__ int s_pref[FWD ? GMAX + 1 : 1];           // forward: row tiles before each group
+    __shared__ unsigned short s_perm[FWD ? 1 : GMAX];    // weight gradient: groups, most steps first
+    __shared__ int s_busy;                               // and how many have any
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / WC, wn = wave % WC;
     const int lr = lane & 15, lq = lane >> 4;
 
     // the offsets as constant memory: a uniform group's come by scalar loads, which the waits on the
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
             for (int g0 = 0; g0 < p.G; g0 += 64) {
                 int l = 0, h = 0;
                 if (g0 + lane < p.G) group_rows(g0 + lane, l, h);
-                int n = (h - l + T - 1) / T;
+                int n = (h - l + TM - 1) / TM;
 #pragma unroll
                 for (int off = 1; off < 64; off <<= 1) {
                     const int o = __shfl_up(n, off, 64);
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
         }
     } else {
         // a group's place is the number of groups with more steps, or as many and a lower index
-        int* steps = reinterpret_cast<int*>(&smem[0][0][0]);
+        int* steps = reinterpret_cast<int*>(&smem[0][0]);
         if (t == 0) s_busy = 0;
         for (int g = t; g < p.G; g += NT) {
             int l, h;
@@ -173,8 +175,8 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
             constexpr int BAND = 8;
             const int bt = BAND * p.nt_n, b = l / bt, r = l - b * bt;
             const int in_band = rt - b * BAND < BAND ? rt - b * BAND : BAND;
-            x.n0 = (r / in_band) * T;
-            x.row = (b * BAND + r % in_band) * T;  // relative to the group's start
+            x.n0 = (r / in_band) * TN;
+            x.row = (b * BAND + r % in_band) * TM;  // relative to the group's start
             w.next += bpx;
         } else {
             const int round = w.next;
@@ -189,8 +191,8 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
             w.next++;
             x.g = s_perm[idx / tpg];
             const int l = idx % tpg;
-            x.row = (l / p.nt_n) * T;
-            x.n0 = (l % p.nt_n) * T;
+            x.row = (l / p.nt_n) * TM;
+            x.n0 = (l % p.nt_n) * TN;
         }
         // uniform, though read from LDS: keep the tile in scalar registers
         x.g = __builtin_amdgcn_readfirstlane(x.g);
@@ -200,29 +202,29 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
         rows_of(x.g == 0 ? 0 : end_of(x.g - 1), end_of(x.g), l, h);
         if (FWD) {
             x.row += l;
-            x.rows = h - x.row < T ? h - x.row : T;
+            x.rows = h - x.row < TM ? h - x.row : TM;
             x.k_lo = 0;
             x.k_hi = p.K;
         } else {
-            x.rows = p.K - x.row < T ? p.K - x.row : T;
+            x.rows = p.K - x.row < TM ? p.K - x.row : TM;
             x.k_lo = l;
             x.k_hi = h;
         }
         x.k0 = x.k_lo & ~(GK - 1);
         x.steps = x.k_hi > x.k0 ? (x.k_hi - x.k0 + GK - 1) / GK : 0;
-        x.cols = p.N - x.n0 < T ? p.N - x.n0 : T;
+        x.cols = p.N - x.n0 < TN ? p.N - x.n0 : TN;
         return true;
     };
 
-    // The loads run one step ahead of the arithmetic, across tiles.  What they are at: a tile, the
+    // The loads run NS - 1 steps ahead of the arithmetic, across tiles.  What they are at: a tile, the
     // step's position, descriptors at the tile's first rows, and this lane's offset in each of the
-    // wave's NP parts (8 rows x 128 bytes) of either operand.
+    // wave's parts (8 rows x 128 bytes) of either operand.
     Tile src;
     int src_k = 0;
     bool src_ok;
     i32x4_t ra, rb;
-    uint32_t oa[NP], ob[NP];
-    const uint32_t smem_at = lds_addr(&smem[0][0][0]) + wave * (NP * 1024), scale_at = lds_addr(&sscale[0][0][0]);
+    uint32_t oa[NA], ob[NB];
+    const uint32_t smem_at = lds_addr(&smem[0][0]), scale_at = lds_addr(&sscale[0][0]);
     auto aim = [&]() {  // at the next tile
         src_ok = next_tile(lead, src);
         if (!src_ok) return;
@@ -231,40 +233,50 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
         rb = make_rsrc4(p.b + (FWD ? (int64_t)src.g * p.bgs : 0) + (int64_t)src.n0 * p.ldb, (uint32_t)(src.cols * p.ldb));
         int l = lane;
         asm volatile("" : "+v"(l));  // formed here, not held through the steps
+        const int ch = l & 7;
 #pragma unroll
-        for (int i = 0; i < NP; i++) {
-            const int row = wave * (8 * NP) + 8 * i + (l >> 3), ch = l & 7;
+        for (int i = 0; i < NA; i++) {
+            const int row = wave * (8 * NA) + 8 * i + (l >> 3);
             oa[i] = row < src.rows ? (uint32_t)row * (uint32_t)p.lda + 16 * (ch ^ swz(row)) : OOB;
+        }
+#pragma unroll
+        for (int i = 0; i < NB; i++) {
+            const int row = wave * (8 * NB) + 8 * i + (l >> 3);
             ob[i] = row < src.cols ? (uint32_t)row * (uint32_t)p.ldb + 16 * (ch ^ swzB(row)) : OOB;
         }
     };
-    // The loads of one step into a stage; each of the first T / 32 waves also brings 64 factors.
+    // The loads of one step into a stage; each of the first waves also brings 64 factors.
+    constexpr int FW = (TM + TN) / 64;
     auto issue = [&](int stage) {
-        const uint32_t at_a = smem_at + stage * (2 * STAGE), at_b = at_a + STAGE;
+        const uint32_t at_a = smem_at + stage * STAGE + wave * (NA * 1024), at_b = smem_at + stage * STAGE + STAGE_A + wave * (NB * 1024);
         const int kpos = __builtin_amdgcn_readfirstlane(src_k);
         if (kpos >= src.k_lo && kpos + GK <= src.k_hi) {
 #pragma unroll
-            for (int i = 0; i < NP; i++) {
-                dma16_at(ra, oa[i], kpos, at_a + i * 1024);
-                dma16_at(rb, ob[i], kpos, at_b + i * 1024);
+            for (int i = 0; i < (NA > NB ? NA : NB); i++) {
+                if (i < NA) dma16_at(ra, oa[i < NA ? i : 0], kpos, at_a + i * 1024);
+                if (i < NB) dma16_at(rb, ob[i < NB ? i : 0], kpos, at_b + i * 1024);
             }
         } else {  // chunks outside the range read as zeros
             int l = lane;
             asm volatile("" : "+v"(l));
+            const int ch = l & 7;
 #pragma unroll
-            for (int i = 0; i < NP; i++) {
-                const int row = wave * (8 * NP) + 8 * i + (l >> 3), ch = l & 7;
-                const int pa = kpos + 16 * (ch ^ swz(row)), pb = kpos + 16 * (ch ^ swzB(row));
+            for (int i = 0; i < NA; i++) {
+                const int pa = kpos + 16 * (ch ^ swz(wave * (8 * NA) + 8 * i + (l >> 3)));
                 dma16(ra, pa < src.k_hi && pa + 16 > src.k_lo ? oa[i] + kpos : OOB, at_a + i * 1024);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; i++) {
+                const int pb = kpos + 16 * (ch ^ swzB(wave * (8 * NB) + 8 * i + (l >> 3)));
                 dma16(rb, pb < src.k_hi && pb + 16 > src.k_lo ? ob[i] + kpos : OOB, at_b + i * 1024);
             }
         }
-        if (wave < T / 32) {
-            const int side = wave / (T / 64), row = (wave & (T / 64 - 1)) * 64 + lane;
+        if (wave < FW) {
+            const int row = (wave < NA ? wave : wave - NA) * 64 + lane;
             const int64_t kb = kpos / GK;
             const float* f;
             uint32_t o = (uint32_t)row * 4u;
-            if (side == 0) {
+            if (wave < NA) {
                 f = p.sa + kb * p.ld_sa + src.row;
             } else if (FWD) {
                 f = p.sb + (int64_t)src.g * p.sb_g + kb * p.sb_k;
@@ -272,7 +284,7 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
             } else {
                 f = p.sb + kb * p.sb_k + src.n0;
             }
-            dma4(make_rsrc4(f, 0x7FFFFFFFu), row < (side == 0 ? src.rows : src.cols) ? o : OOB, scale_at + stage * (8 * T) + wave * 256);
+            dma4(make_rsrc4(f, 0x7FFFFFFFu), row < (wave < NA ? src.rows : src.cols) ? o : OOB, scale_at + stage * (4 * (TM + TN)) + wave * 256);
         }
         src_k += GK;
         if (src_k >= src.k_hi) aim();
@@ -282,8 +294,14 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
     aim();
     Tile cur;
     bool have = next_tile(follow, cur);
-    int st = 0;  // stage of the current step
-    if (src_ok) issue(0);
+    int st = 0, ahead = 0;  // stage of the current step; steps whose loads are on their way
+#pragma unroll
+    for (int d = 0; d < NS - 1; d++) {
+        if (src_ok) {
+            issue(d);
+            ahead++;
+        }
+    }
     auto barrier = [&]() {  // LDS reads and writes done; loads from memory keep flying
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
@@ -308,9 +326,15 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
 #pragma unroll
             for (int e = 0; e < 4; e++) acc[i][j][e] = fmaf(FWD ? sum[j][e] : sum[j][e] * sbv[FWD ? 0 : j][e], f, acc[i][j][e]);
         };
-        for (int s = 0; s < cur.steps; s++, st ^= 1) {
+        for (int s = 0; s < cur.steps; s++, st = st + 1 < NS ? st + 1 : 0) {
             const int kpos = cur.k0 + s * GK;
-            wait_vm0();
+            // this step's loads have landed; NS - 2 steps' are younger
+            if (NS > 2 && ahead == NS - 1) {
+                if (wave < FW) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (NA + NB + 1)) : "memory");
+                else asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (NA + NB)) : "memory");
+            } else {
+                wait_vm0();
+            }
             if (!FWD && (kpos < cur.k_lo || kpos + GK > cur.k_hi)) {
                 // zero the bytes of other groups' tokens (or of the padding past M) in the chunks that
                 // the range cuts, in both operands: such a byte may be a NaN code.  Each wave does the
@@ -318,11 +342,12 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
                 const int lo = cur.k_lo - kpos, hi = cur.k_hi - kpos;
                 int l = lane;
                 asm volatile("" : "+v"(l));
-                constexpr int OWN = 8 * NP;
+                static_assert(FWD || TM == TN, "one count of rows");
+                constexpr int OWN = 8 * NA;
                 if (l < 2 * OWN) {
                     const int row = wave * OWN + (l & (OWN - 1));
                     const bool in_a = l < OWN;
-                    uint8_t* side = smem[st][in_a ? 0 : 1];
+                    uint8_t* side = smem[st] + (in_a ? 0 : STAGE_A);
 #pragma unroll
                     for (int ch = 0; ch < 8; ch++) {
                         const int b0 = 16 * ch;
@@ -339,11 +364,15 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
                 }
             }
             barrier();
-            if (src_ok) issue(st ^ 1);  // into the stage that every wave has left
-            const uint8_t* As = smem[st][0];
-            const uint8_t* Bs = smem[st][1];
-            const float* sa = &sscale[st][0][wm * WM + lr];
-            const float* sb = &sscale[st][1][wn * WN];
+            ahead--;
+            if (src_ok) {  // into the stage of the step before, which every wave has left
+                issue(st > 0 ? st - 1 : NS - 1);
+                ahead++;
+            }
+            const uint8_t* As = smem[st];
+            const uint8_t* Bs = As + STAGE_A;
+            const float* sa = &sscale[st][wm * WM + lr];
+            const float* sb = &sscale[st][TM + wn * WN];
             // The order below is the order of issue (no scheduling across the barriers): while a
             // matrix instruction runs, the vector unit adds the sums that the same column block gave
             // for the row before, and the next row's fragment is read.
@@ -361,7 +390,7 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 1; j < NJ; j++) load_b(j);
-            load_a(1);
+            if (MI > 1) load_a(1);
 #pragma unroll
             for (int i = 0; i < MI; i++) fa[i] = sa[16 * i];
             const float sbu = FWD ? sb[0] : 1.0f;  // a wave's columns lie in one weight block
@@ -497,9 +526,9 @@ __global__ __launch_bounds__(512, T == 256 ? 2 : 4) void block_gemm_kernel(const
     if (!FWD) {
         const int esz = p.out_f32 ? 4 : 2;
         for (int idx = w_tiles + (int)blockIdx.x; idx < p.G * tpg; idx += nb) {
-            const int g = s_perm[idx / tpg], l = idx % tpg, r0 = l / p.nt_n * T, c0 = l % p.nt_n * T;
-            for (int i = t; i < T * T; i += NT) {
-                const int row = r0 + i / T, col = c0 + i % T;
+            const int g = s_perm[idx / tpg], l = idx % tpg, r0 = l / p.nt_n * TM, c0 = l % p.nt_n * TN;
+            for (int i = t; i < TM * TN; i += NT) {
+                const int row = r0 + i / TN, col = c0 + i % TN;
                 if (row < p.K && col < p.N) {
                     uint8_t* dst = p.c + (((int64_t)g * p.K + row) * p.ldc + col) * esz;
                     if (p.out_f32) *reinterpret_cast<float*>(dst) = 0.0f;
@@ -519,34 +548,46 @@ __global__ __launch_bounds__(256) void block_zero_kernel(const BlockGemmArgs p) 
     }
 }
 
-template <int MODE, int T>
+template <int MODE, int TM, int TN, int NS>
 static fp8q_status_t launch_block_gemm(BlockGemmArgs p, hipStream_t stream) {
-    p.nt_n = (p.N + T - 1) / T;
-    p.nt_k = MODE == MODE_FWD ? 1 : (p.K + T - 1) / T;
+    p.nt_n = (p.N + TN - 1) / TN;
+    p.nt_k = MODE == MODE_FWD ? 1 : (p.K + TM - 1) / TM;
     if (MODE == MODE_FWD && p.K == 0) {
         block_zero_kernel<<<dim3(1024), dim3(256), 0, stream>>>(p);
         FP8Q_CHECK_LAUNCH();
         return FP8Q_OK;
     }
-    const int64_t tiles = MODE == MODE_FWD ? ((int64_t)(p.M + T - 1) / T + p.G) * p.nt_n : (int64_t)p.G * p.nt_k * p.nt_n;
+    const int64_t tiles = MODE == MODE_FWD ? ((int64_t)(p.M + TM - 1) / TM + p.G) * p.nt_n : (int64_t)p.G * p.nt_k * p.nt_n;
     // offsets that go up and down can make every group as long as M
-    const int64_t most = MODE == MODE_FWD ? (int64_t)p.G * ((p.M + T - 1) / T) * p.nt_n : tiles;
+    const int64_t most = MODE == MODE_FWD ? (int64_t)p.G * ((p.M + TM - 1) / TM) * p.nt_n : tiles;
     if (tiles >= 0x7FFFFFFFLL || most >= 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
-    int64_t grid = (int64_t)num_cus() * (T == 256 ? 1 : 2);
+    int64_t grid = (int64_t)num_cus() * (TM == 256 || NS > 2 ? 1 : 2);
     if (tiles < grid) grid = (tiles + 7) / 8 * 8;  // whole rounds of the XCDs
-    block_gemm_kernel<MODE, T><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(p);
+    block_gemm_kernel<MODE, TM, TN, NS><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
 
 template <int MODE>
 static fp8q_status_t pick_block_gemm(const BlockGemmArgs& p, hipStream_t stream) {
+    // Where CUs would be left over, smaller tiles and loads 2 or 3 steps ahead, one block per CU (1 group,
+    // 7168 long): 512 x 2048 in 64-tiles 24 us, in 128 x 64-tiles 31, in 128-tiles 42; 960 x 2048 in
+    // 128 x 64-tiles 32 us, in 128-tiles 42, in 64-tiles, two for some CUs, 34.  Every group but one
+    // ends inside a tile, on average half way.
+    const int64_t ends = (p.G - 1) / 2, cus = num_cus();
+    auto up = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+    if (MODE == MODE_FWD) {
+        if ((up(p.M, 64) + ends) * up(p.N, 64) <= cus) return launch_block_gemm<MODE, 64, 64, 4>(p, stream);
+        if ((up(p.M, 128) + ends) * up(p.N, 64) <= cus) return launch_block_gemm<MODE_FWD, 128, 64, 3>(p, stream);
+    } else if (p.G * up(p.K, 64) * up(p.N, 64) <= cus) {
+        return launch_block_gemm<MODE, 64, 64, 4>(p, stream);
+    }
     // 128-tiles where 256-tiles would not give every CU one: 2048 x 2048 x 2048 in one group 26 against
     // 40 us, 4096 x 2048 x 2048 34 against 43 us; with a tile for each, 256 is faster: 4096 x 4096 x
     // 2048 47 against 53 us, weight gradient of 8 groups of 1024 x 2048 28 against 31 us
     const int64_t rows = MODE == MODE_FWD ? p.M : (int64_t)p.G * p.K;
     const int64_t tiles = (rows + 255) / 256 * ((p.N + 255) / 256);
-    return tiles < 256 ? launch_block_gemm<MODE, 128>(p, stream) : launch_block_gemm<MODE, 256>(p, stream);
+    return tiles < 256 ? launch_block_gemm<MODE, 128, 128, 2>(p, stream) : launch_block_gemm<MODE, 256, 256, 2>(p, stream);
 }
 
 }  // namespace fp8q

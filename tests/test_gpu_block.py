@@ -393,3 +393,21 @@ def test_outputs_past_the_last_level_cache(fq):
         one = torch.tensor([ends[g - 1] if g else 0, ends[g]], dtype=torch.int32, device=DEV)
         part = fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, g_t, g_s, a_t, a_s, one)
         assert torch.equal(dw[g], part[1])
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K,G,kind", [
+    (200, 1000, 1040, 2, "cuts"), (1000, 1500, 400, 3, "cuts"), (130, 4100, 656, 1, "even"), (900, 1408, 2064, 4, "empties"),
+    (1900, 1511, 272, 5, "cuts"), (700, 2048, 1168, 20, "empties"), (5000, 3500, 144, 6, "cuts"), (4700, 3600, 400, 5, "empties")])
+def test_forward_by_tile(fq, M, N, K, G, kind, out):
+    """Two sizes for each tile: 64 x 64, 128 x 64, 128 x 128 and 256 x 256."""
+    test_forward(fq, M, N, K, G, kind, out)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K,G,kind", [
+    (1000, 500, 700, 1, "even"), (1333, 300, 260, 9, "empties"), (900, 700, 1030, 3, "cuts"), (700, 1500, 1300, 9, "cuts"),
+    (400, 1530, 1290, 12, "empties")])
+def test_weight_gradient_by_tile(fq, M, N, K, G, kind, out):
+    """64-tiles (several steps ahead of the arithmetic, over groups' ends), 128- and 256-tiles."""
+    test_weight_gradient(fq, M, N, K, G, kind, out)
