@@ -409,7 +409,7 @@ def _rows_of(t: torch.Tensor, what: str, dtypes, shape, dev) -> None:
     """Checks that t is a tensor on device dev of one of dtypes and of the given shape, with unit
     stride in its last dimension."""
     if (t.dtype in dtypes and t.device == dev and t.shape == shape
-            and (t.stride(-1) == 1 or t.shape[-1] <= 1) and dev.type == "cuda"):
+            and (t.stride()[-1] == 1 or shape[-1] <= 1) and t.is_cuda):
         return
     _want(t.is_cuda and t.device == dev, f"{what} must be on the operands' GPU")
     _want(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
@@ -421,11 +421,11 @@ def _matrix(t: torch.Tensor, what: str, dtypes):
     """Checks the first operand of a call, a matrix of any size; returns its rows, columns and
     device."""
     dev = t.device
-    if t.dtype not in dtypes or t.dim() != 2 or dev.type != "cuda":
+    if t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda:
         _want(t.dim() == 2, f"{what} must be a matrix")
         _rows_of(t, what, dtypes, t.shape, dev)
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if cols > 1 and t.stride()[1] != 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
     return rows, cols, dev
 
@@ -433,18 +433,21 @@ def _matrix(t: torch.Tensor, what: str, dtypes):
 def _ld(t: torch.Tensor, rows: int, cols: int) -> int:
     """Leading dimension of a rows x cols matrix; the stride of a single or an empty row says
     nothing."""
-    return t.stride(0) if rows > 1 and cols > 0 else 0 if cols == 0 else max(t.stride(0), cols)
+    ld = t.stride()[0]
+    return ld if rows > 1 and cols > 0 else 0 if cols == 0 else max(ld, cols)
 
 
 # the current stream's handle without a Stream object made for it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+# the current device, for callers that hold a tensor of a GPU already
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name: str, dev: torch.device, *args) -> None:
     """The C entry point on the current stream of dev, with dev the current device."""
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == _device_now():
         status = getattr(_lib or lib(), name)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
@@ -460,8 +463,8 @@ def _blocks(n: int) -> int:
 def _padded_bytes(rows: int, cols: int, dev) -> torch.Tensor:
     """[rows, cols] bytes whose rows start on 16 bytes, as the GEMMs take them."""
     if cols % 16 == 0:
-        return torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    return torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)[:, :cols]
+        return torch.empty(rows, cols, dtype=torch.uint8, device=dev)
+    return torch.empty(rows, -(-cols // 16) * 16, dtype=torch.uint8, device=dev)[:, :cols]
 
 
 _BF16, _F32, _I32T = (torch.bfloat16,), (torch.float32,), (torch.int32,)
@@ -485,7 +488,7 @@ def fp8_block_quant_rowwise(x: torch.Tensor, q: torch.Tensor | None = None,
         _rows_of(q, "q", _BYTES, x.shape, dev)
     blocks = -(-cols // BLOCK)
     if scales is None:
-        scales = torch.empty((blocks, rows), dtype=torch.float32, device=dev)
+        scales = torch.empty(blocks, rows, dtype=torch.float32, device=dev)
         ld_s = rows
     else:
         _rows_of(scales, "scales", _F32, (blocks, rows), dev)
@@ -513,7 +516,7 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
         else:
             _rows_of(q, "q", _BYTES, x.shape, dev)
         if s_rows is None:
-            s_rows = torch.empty((_blocks(cols), rows), dtype=f32, device=dev)
+            s_rows = torch.empty(_blocks(cols), rows, dtype=f32, device=dev)
         else:
             _rows_of(s_rows, "s_rows", _F32, (_blocks(cols), rows), dev)
         row_args = (q.data_ptr(), _ld(q, rows, cols), s_rows.data_ptr(),
@@ -523,7 +526,7 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
     else:
         _rows_of(q_t, "q_t", _BYTES, (cols, rows), dev)
     if s_cols is None:
-        s_cols = torch.empty((_blocks(rows), cols), dtype=f32, device=dev)
+        s_cols = torch.empty(_blocks(rows), cols, dtype=f32, device=dev)
     else:
         _rows_of(s_cols, "s_cols", _F32, (_blocks(rows), cols), dev)
     _call("fp8_block_quant_dual", dev, x.data_ptr(), rows, cols, _ld(x, rows, cols), *row_args,
@@ -610,7 +613,7 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
         M, K, shape = inner, rows, (groups, rows, N)
     if c is None:
         _want(out_dtype in _OUT, "the output must be bfloat16 or float32")
-        c = torch.empty(shape, dtype=out_dtype, device=dev)
+        c = torch.empty(*shape, dtype=out_dtype, device=dev)
         ldc = N
     else:
         c = _gemm_out(c, shape, out_dtype, dev)
@@ -649,17 +652,17 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     if bias is not None:
         _rows_of(bias, "bias", _F32, (E,), dev)
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
     else:
         _rows_of(ids, "ids", _I32T, (T, top_k), dev)
         _want(ids.is_contiguous(), "ids must be contiguous")
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        weights = torch.empty(T, top_k, dtype=torch.float32, device=dev)
     else:
         _rows_of(weights, "weights", _F32, (T, top_k), dev)
         _want(weights.is_contiguous(), "weights must be contiguous")
     if workspace is None:
-        workspace = torch.empty((lib().moe_route_workspace_size(T, H, E),), dtype=torch.uint8,
+        workspace = torch.empty(lib().moe_route_workspace_size(T, H, E), dtype=torch.uint8,
                                 device=dev)
     _call("moe_route", dev, x.data_ptr(), T, H, _ld(x, T, H), router.data_ptr(), E,
           _ld(router, E, H),
@@ -708,12 +711,12 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     args13 = _expert_weights(w13, s13, "w13", (E, 2 * I, H), dev)
     args2 = _expert_weights(w2, s2, "w2", (E, H, I), dev)
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
     else:
         _rows_of(y, "y", _BF16, (T, H), dev)
     if workspace is None:
         need = fp8_moe_few_tokens_workspace_size(T, H, I, top_k)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _call("fp8_moe_few_tokens", dev, x.data_ptr(), T, H, _ld(x, T, H), ids.data_ptr(),
           weights.data_ptr(), top_k, *args13, *args2, E, I, y.data_ptr(), _ld(y, T, H),
           workspace.data_ptr(), workspace.nbytes)
