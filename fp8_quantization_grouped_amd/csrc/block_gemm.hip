@@ -11,13 +11,29 @@
 // matrix cores work on the next row of results: the sums of row i are added while row i + 1 is
 // multiplied, 16 lanes' worth of work per 32-cycle matrix instruction.
 //
-// Tiles: T x T outputs (T = 256 or 128) by 8 waves, 128-byte steps, operands straight from memory
-// into two LDS stages (layout and swizzles: gemm_tile.hpp), the next step's loads in flight during
-// this one's arithmetic, one barrier per step.  A step's load offsets are the tile's plus the
-// step's position: they are held in registers, and only steps that end or begin inside a block
-// form masked ones.
-//   T = 256: one block per CU.  T = 128: two blocks per CU, for problems whose 256-tiles would
-//   leave CUs without work (see launch).
+// Tiles: TM x TN outputs by 8 waves, 128-byte steps, operands straight from memory into NS LDS
+// stages (layout and swizzles: gemm_tile.hpp), the loads NS - 1 steps ahead of the arithmetic, one
+// barrier per step.  A step's load offsets are the tile's plus the step's position: they are held in
+// registers, and only steps that end or begin inside a block form masked ones.
+//   256 x 256, 2 stages, one block per CU: a wave's 128 x 64 results fill its registers, and
+//     with them the waves read 192 KB of LDS a step, the least that eight of them can.
+//   128 x 128, 2 stages, two blocks per CU; 128 x 64, 3 stages, and 64 x 64, 4 stages, one block per
+//     CU: for problems whose larger tiles would leave CUs without work (see pick_block_gemm).
+//
+// Bound: the matrix cores and LDS.  At 256 x 256 a step's matrix instructions take 2048 cycles of a
+// SIMD, and so do LDS's 128 bytes a cycle for what the waves read and the loads bring; they overlap
+// in part.  Measured: 8192 x 14336 x 4096 in one group 435 us, 2.2 PFLOP/s (415 us with the loads
+// taken away after the first step, so that LDS and the matrix cores alone remain, 219 us without the
+// reads of A's fragments); 49152 rows in 64 groups, 1408 x 2048, 204 us (1.4 PFLOP/s of the products
+// asked for: groups and columns that end inside a tile add a third); data gradient of 16384 rows in
+// 32 groups, 2048 x 7168, 332 us, their weight gradient 499 us, of which 40 are stores, 56 the
+// columns' factors and a quarter of the rest the groups' ends inside blocks.  Small: 512 x 2048 x
+// 7168 24 us, bound by the chain of 56 steps of 0.35 us.
+//
+// Measured and not kept: 16 waves per block, fragments of A read two rows ahead, wave priorities, the
+// loads issued later in a step and B two steps ahead of the arithmetic (all within 1%); leaving out
+// the multiplications of waves without rows or columns of the tile (64 experts 1% faster, dense 1%
+// slower: the loads take as long); long and short tiles of the weight gradient in turn (same).
 //
 // Schedule (persistent blocks, no cross-block waits): as the other grouped GEMM.  Forward tiles go
 // by group, in bands of 8 row tiles, an XCD's share in one piece; weight-gradient tiles by group

@@ -18,6 +18,17 @@
 //
 // Every sum has a fixed order: a contraction's parts are added in wave order, a token's experts in
 // the order of its choices.
+//
+// Measured (32 experts of 2048 x 7168, 8 of them a token): 1 token's gate and up products 46 us (5.1
+// TB/s of weights) and down product 26 us (4.5 TB/s), 64 tokens' 193 and 117 us (4.9 and 4.0 TB/s),
+// where a copy of large buffers reaches 4.9 TB/s and a kernel that only reads as these do 5.4 at 240
+// MB and 6.2 at 960 MB.  64 experts of 1408 x 2048, 6 of them, 5 tokens: 37 and 19 us (3.8 TB/s: each
+// wave has 16 and 11 blocks to stream, so starting and ending count).  Routing and the join take 2
+// to 6 us each, a launch's time.
+//
+// Measured and not kept: 4 blocks ahead instead of 2 (spills: 340 against 242 us for 64 tokens), 8
+// waves a CU with twice the registers (242 to 265 us), non-temporal weight loads, a second pass over
+// the weights for more than 32 tokens (65 us), h in one bf16 (its rounding shows in the result).
 #include "common.hpp"
 #include "lds_dma.hpp"
 
@@ -327,7 +338,7 @@ constexpr int moe_lds(int nw) { return 8192 * nw; }  // staged activations of a 
 
 // One expert's product with its chosen tokens.  DOWN = false: h[a] = silu(G x) * (U x), a wave's two
 // weight tiles being 16 gate rows and the same 16 up rows; DOWN = true: o[a] = W2 h[a], two
-// neighbouring tiles of 16 rows.  A block's 8 waves are 8 / S such pairs times S parts of the
+// neighbouring tiles of 16 rows.  A block's NW waves are NW / S such pairs times S parts of the
 // contraction, whose sums meet in LDS.
 //
 // A wave streams its 32 weight rows through registers, D contraction blocks (4 KB each) ahead of the
@@ -371,12 +382,18 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_stream_kernel(const MoeArgs p)
     const float* srow[2] = {s + (row0 / MB) * s_n_, s + (row1 / MB) * s_n_};
     const int kbs = (K + MB - 1) / MB, kb0 = kbs * part / S, len = kbs * (part + 1) / S - kb0;
     const int most = (kbs + S - 1) / S;  // the longest part's blocks
+    // A block begins at its own place of the contraction and goes round: rows often lie a power of two
+    // apart, and waves at one place of all of them ask few of the memory's channels at a time (16 tokens
+    // of 8 experts of 14336 x 4096 312 -> 284 us, 128 tokens 528 -> 492; 32 of 2048 x 7168 288 -> 290 and
+    // 357 -> 352).
+    const int turn = (int)(blockIdx.x * 5u % (unsigned)most);
+    auto place = [&](int i) { return i + turn < most ? i + turn : i + turn - most; };
 
     for (int first = 0;; first += p.pass) {
         uint4 wv[D][2][2];
         auto load = [&](int d, int hf, int i) {  // half of block i of the part into register set d
-            const int k = (kb0 + i) * MB + 64 * hf;
-            const uint32_t off = k + 16 * g < K && i < len ? lane_off + k : OOB;
+            const int j = place(i), k = (kb0 + j) * MB + 64 * hf;
+            const uint32_t off = k + 16 * g < K && i < most && j < len ? lane_off + k : OOB;
 #pragma unroll
             for (int c = 0; c < 2; c++)
                 wv[d][c][hf] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf[c], off, 0, 0));
@@ -410,7 +427,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_stream_kernel(const MoeArgs p)
         // each other, of the chunk that starts at block i0 of every part; q counts them.
         auto bring = [&](int i0, int q, uint32_t to) {
             const int unit = 4 * q + g, row = unit & ((1 << lr) - 1), rest = unit >> lr, bl = rest / PL;
-            const int kb = kbs * (bl >> lc) / S + i0 + (bl & ((1 << lc) - 1));
+            const int kb = kbs * (bl >> lc) / S + place(i0 + (bl & ((1 << lc) - 1)));
             const int k = kb * MB + 8 * (r ^ (row & 15));
             uint32_t off = OOB;
             if (row < toks && k < K) off = at_byte[row] + 2 * k + (PL == 2 && (rest & 1) ? plane : 0);
@@ -433,7 +450,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_stream_kernel(const MoeArgs p)
             if ((i0 & 63) == 0) {
 #pragma unroll
                 for (int c = 0; c < 2; c++)
-                    sv[c] = on[c] && i0 + lane < len ? srow[c][(kb0 + i0 + lane) * s_k] : 0.0f;
+                    sv[c] = on[c] && i0 + lane < most && place(i0 + lane) < len ? srow[c][(kb0 + place(i0 + lane)) * s_k] : 0.0f;
             }
 #pragma unroll
             for (int d = 0; d < D; d++) {
@@ -470,7 +487,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_stream_kernel(const MoeArgs p)
                     load(d, hf, i + D);
 #pragma unroll
                     for (int m = 0; m < MT; m++) {
-                        if (m < mt && i < len) {
+                        if (m < mt && place(i) < len) {
                             const int row = (16 * m + r) & ((1 << lr) - 1);
                             f4_t sum0 = {0.0f, 0.0f, 0.0f, 0.0f}, sum1 = sum0;
 #pragma unroll
@@ -572,12 +589,16 @@ template <int MT, bool DOWN>
 static void launch_stream(const MoeArgs& p, hipStream_t stream) {
     const int n = p.T * p.top_k, experts = n < p.E ? n : p.E;
     const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
-    // parts of the contraction: 16 waves for every CU, each with 4 blocks or more; one block of every
-    // part has to fit half the staging buffer (2^8 bytes a row and plane)
-    constexpr int NW = MT == 1 ? 4 : 8, PL = DOWN ? 2 : 1, SMAX = MT == 1 ? NW : 8 / (MT * PL);
+    // Parts of the contraction: two unless there are waves for the chip twice over (4096 run at a time),
+    // four below half of it, each with 4 blocks or more (layers of 32 experts of 2048 x 7168, 8 of them a
+    // token: 1 token 78 us in four parts, 79 in two, 88 in one; 5 tokens 231, 230 and 252; 24 tokens of 64
+    // experts of 1408 x 2048 120 us in two, 129 in one).  In passes of 64 tokens one part stages them best
+    // (64 tokens 315 us, in two parts 326).  One block of every part has to fit half the staging buffer
+    // (2^8 bytes a row and plane).
+    constexpr int NW = MT == 1 ? 4 : 8, PL = DOWN ? 2 : 1, SMAX = MT == 1 ? 4 : MT == 2 ? 4 / PL : 1;
     static_assert(moe_lds(NW) / 2 >= SMAX * PL * (MT == 1 ? 1 : 16 * MT) * 256, "a block of every part fits");
     int S = 1;
-    while (2 * S <= SMAX && 2 * S * PL * p.pass * 256 <= moe_lds(NW) / 2 && experts * pairs * S < 4096 && kbs >= 8 * S) S *= 2;
+    while (2 * S <= SMAX && 2 * S * PL * p.pass * 256 <= moe_lds(NW) / 2 && experts * pairs * S < (S == 1 ? 8192 : 4096) && kbs >= 8 * S) S *= 2;
     const dim3 grid((unsigned)((pairs * S + NW - 1) / NW), (unsigned)(p.by_choice ? n : p.E)), block(64 * NW);
     if (S == 1) moe_stream_kernel<MT, 1, DOWN, NW><<<grid, block, 0, stream>>>(p);
     else if (S == 2) moe_stream_kernel<MT, SMAX < 2 ? 1 : 2, DOWN, NW><<<grid, block, 0, stream>>>(p);
