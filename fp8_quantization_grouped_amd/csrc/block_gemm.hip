@@ -603,7 +603,14 @@ static fp8q_status_t pick_block_gemm(const BlockGemmArgs& p, hipStream_t stream)
     // 2048 47 against 53 us, weight gradient of 8 groups of 1024 x 2048 28 against 31 us
     const int64_t rows = MODE == MODE_FWD ? p.M : (int64_t)p.G * p.K;
     const int64_t tiles = (rows + 255) / 256 * ((p.N + 255) / 256);
-    return tiles < 256 ? launch_block_gemm<MODE, 128, 128, 2>(p, stream) : launch_block_gemm<MODE, 256, 256, 2>(p, stream);
+    // Forward tiles are of one length, so a launch takes whole rounds of them: a round of 512 128-tiles
+    // takes 0.65 as long as one of 256 256-tiles, and few rounds of cut tiles can come out shorter (16384
+    // rows in 64 groups, 1408 x 2048: 76 against 92 us; 4096 rows in 8 groups, 4096 x 4096: 91 against
+    // 110).  Past three rounds the larger tile's fewer loads count (49152 rows in 64 groups: 235 against
+    // 207 us, though the rounds are even).
+    const int64_t r256 = up((up(p.M, 256) + ends) * up(p.N, 256), cus), r128 = up((up(p.M, 128) + ends) * up(p.N, 128), 2 * cus);
+    const bool small = tiles < 256 || (MODE == MODE_FWD && r256 <= 3 && 65 * r128 < 100 * r256);
+    return small ? launch_block_gemm<MODE, 128, 128, 2>(p, stream) : launch_block_gemm<MODE, 256, 256, 2>(p, stream);
 }
 
 }  // namespace fp8q
