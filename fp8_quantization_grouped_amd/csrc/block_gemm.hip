@@ -12,28 +12,30 @@
 // multiplied, 16 lanes' worth of work per 32-cycle matrix instruction.
 //
 // Tiles: TM x TN outputs by 8 waves, 128-byte steps, operands straight from memory into NS LDS
-// stages (layout and swizzles: gemm_tile.hpp), the loads NS - 1 steps ahead of the arithmetic, one
-// barrier per step.  A step's load offsets are the tile's plus the step's position: they are held in
-// registers, and only steps that end or begin inside a block form masked ones.
-//   256 x 256, 2 stages, one block per CU: a wave's 128 x 64 results fill its registers, and
-//     with them the waves read 192 KB of LDS a step, the least that eight of them can.
+// stages (layout and swizzles: gemm_tile.hpp), one barrier per step, before its last row of results:
+// by then every fragment of the step is in registers, so its stage takes the loads of the step NS
+// later, and the next step's first fragments come during that row.  A step's load offsets are the
+// tile's plus the step's position: they are held in registers (formed anew at each step, they delay
+// the last row: 7% slower), and only steps that end or begin inside a block form masked ones.
+//   256 x 256, 2 stages, one block per CU: a wave's 128 x 64 results fill its registers, and with
+//     them the waves read 192 KB of LDS a step, the least that eight of them can.
 //   128 x 128, 2 stages, two blocks per CU; 128 x 64, 3 stages, and 64 x 64, 4 stages, one block per
 //     CU: for problems whose larger tiles would leave CUs without work (see pick_block_gemm).
 //
-// Bound: the matrix cores and LDS.  At 256 x 256 a step's matrix instructions take 2048 cycles of a
-// SIMD, and so do LDS's 128 bytes a cycle for what the waves read and the loads bring; they overlap
-// in part.  Measured: 8192 x 14336 x 4096 in one group 435 us, 2.2 PFLOP/s (415 us with the loads
-// taken away after the first step, so that LDS and the matrix cores alone remain, 219 us without the
-// reads of A's fragments); 49152 rows in 64 groups, 1408 x 2048, 204 us (1.4 PFLOP/s of the products
-// asked for: groups and columns that end inside a tile add a third); data gradient of 16384 rows in
-// 32 groups, 2048 x 7168, 332 us, their weight gradient 499 us, of which 40 are stores, 56 the
-// columns' factors and a quarter of the rest the groups' ends inside blocks.  Small: 512 x 2048 x
-// 7168 24 us, bound by the chain of 56 steps of 0.35 us.
+// Bound: delivery of the operands to the matrix cores, which are busy half of the time (48% by
+// counters); at 256 x 256 a step's matrix instructions take 2048 cycles of a SIMD, and the step 3700.
+// Measured: 8192 x 14336 x 4096 in one group 430 us, 2.2 PFLOP/s (20 us less with the loads taken away
+// after the first step, half without the reads of A's fragments, 6% less without the factors); 49152
+// rows in 64 groups, 1408 x 2048, 202 us (1.4 PFLOP/s of the products asked for: groups and columns
+// that end inside a tile add a third); data gradient of 16384 rows in 32 groups, 2048 x 7168, 325 us,
+// their weight gradient 497 us, of which 40 are stores, 56 the columns' factors and a quarter of the
+// rest the groups' ends inside blocks.  Small: 512 x 2048 x 7168 24 us, a chain of 56 steps of 0.35 us.
 //
 // Measured and not kept: 16 waves per block, fragments of A read two rows ahead, wave priorities, the
 // loads issued later in a step and B two steps ahead of the arithmetic (all within 1%); leaving out
 // the multiplications of waves without rows or columns of the tile (64 experts 1% faster, dense 1%
-// slower: the loads take as long); long and short tiles of the weight gradient in turn (same).
+// slower: the loads take as long), and the loads with them (2 to 4% slower); long and short tiles of
+// the weight gradient in turn (same).
 //
 // Schedule (persistent blocks, no cross-block waits): as the other grouped GEMM.  Forward tiles go
 // by group, in bands of 8 row tiles, an XCD's share in one piece; weight-gradient tiles by group
@@ -263,6 +265,8 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
     };
     // The loads of one step into a stage; each of the first waves also brings 64 factors.
     constexpr int FW = (TM + TN) / 64;
+    int ahead = 0;                        // steps whose loads are on their way
+    int cut_lo[NS - 1], cut_hi[NS - 1];  // weight gradient: the tokens of each that count
     auto issue = [&](int stage) {
         const uint32_t at_a = smem_at + stage * STAGE + wave * (NA * 1024), at_b = smem_at + stage * STAGE + STAGE_A + wave * (NB * 1024);
         const int kpos = __builtin_amdgcn_readfirstlane(src_k);
@@ -302,6 +306,16 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
             }
             dma4(make_rsrc4(f, 0x7FFFFFFFu), row < (wave < NA ? src.rows : src.cols) ? o : OOB, scale_at + stage * (4 * (TM + TN)) + wave * 256);
         }
+        if (!FWD) {
+#pragma unroll
+            for (int d = 0; d < NS - 1; d++) {
+                if (d == ahead) {
+                    cut_lo[d] = src.k_lo - kpos;
+                    cut_hi[d] = src.k_hi - kpos;
+                }
+            }
+        }
+        ahead++;
         src_k += GK;
         if (src_k >= src.k_hi) aim();
     };
@@ -310,22 +324,75 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
     aim();
     Tile cur;
     bool have = next_tile(follow, cur);
-    int st = 0, ahead = 0;  // stage of the current step; steps whose loads are on their way
+    int st = 0;  // stage of the current step
 #pragma unroll
-    for (int d = 0; d < NS - 1; d++) {
-        if (src_ok) {
-            issue(d);
-            ahead++;
+    for (int d = 0; d < NS - 1; d++)
+        if (src_ok) issue(d);
+    // The oldest step's loads, to a stage, have landed in every wave (NS - 2 steps' are younger), and
+    // every wave has read what it takes from the stage before.
+    auto arrive = [&](int stage) {
+        if (NS > 2 && ahead == NS - 1) {
+            if (wave < FW) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (NA + NB + 1)) : "memory");
+            else asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (NA + NB)) : "memory");
+        } else {
+            wait_vm0();
         }
-    }
-    auto barrier = [&]() {  // LDS reads and writes done; loads from memory keep flying
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (!FWD) {
+            const int lo = cut_lo[0], hi = cut_hi[0];
+#pragma unroll
+            for (int d = 0; d + 1 < NS - 1; d++) {
+                cut_lo[d] = cut_lo[d + 1];
+                cut_hi[d] = cut_hi[d + 1];
+            }
+            if (lo > 0 || hi < GK) {
+                // zero the bytes of other groups' tokens (or of the padding past M) in the chunks that
+                // the range cuts, in both operands: such a byte may be a NaN code.  Each wave does the
+                // rows that it loaded, so its own wait suffices.
+                int l = lane;
+                asm volatile("" : "+v"(l));
+                static_assert(FWD || TM == TN, "one count of rows");
+                constexpr int OWN = 8 * NA;
+                if (l < 2 * OWN) {
+                    const int row = wave * OWN + (l & (OWN - 1));
+                    const bool in_a = l < OWN;
+                    uint8_t* side = smem[stage] + (in_a ? 0 : STAGE_A);
+#pragma unroll
+                    for (int ch = 0; ch < 8; ch++) {
+                        const int b0 = 16 * ch;
+                        if ((lo > b0 && lo < b0 + 16) || (hi > b0 && hi < b0 + 16)) {
+                            uint4* q = reinterpret_cast<uint4*>(side + (in_a ? lds_off(row, ch) : lds_offB(row, ch)));
+                            uint4 w = *q;
+                            w.x &= keep_mask4(lo, hi, b0);
+                            w.y &= keep_mask4(lo, hi, b0 + 4);
+                            w.z &= keep_mask4(lo, hi, b0 + 8);
+                            w.w &= keep_mask4(lo, hi, b0 + 12);
+                            *q = w;
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // LDS reads and writes done
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        ahead--;
     };
     // this lane's fragments: A row wm * WM + lr (+ 16 i), B row brow(j, lr) of its columns
     const int fa0 = lds_off(wm * WM + lr, lq), fa1 = lds_off(wm * WM + lr, 4 + lq);
-    const int fb0 = lds_offB(wn * WN + brow(0, lr), lq), fb1 = lds_offB(wn * WN + brow(0, lr), 4 + lq);
+    const int fb0 = STAGE_A + lds_offB(wn * WN + brow(0, lr), lq), fb1 = STAGE_A + lds_offB(wn * WN + brow(0, lr), 4 + lq);
+    v8i_t bf[NJ], af[2];  // rows of A in turn
+    auto load_b = [&](const uint8_t* at, int j) {
+        const int o = 32 * GK * (j >> 1) + 4 * GK * (j & 1);
+        bf[j] = two_chunks(at + fb0 + o, at + fb1 + o);
+    };
+    auto load_a = [&](const uint8_t* at, int i) { af[i & 1] = two_chunks(at + fa0 + 16 * GK * i, at + fa1 + 16 * GK * i); };
+    if (have) {
+        arrive(0);
+        if (src_ok) issue(NS - 1);
+        load_a(smem[0], 0);
+#pragma unroll
+        for (int j = 0; j < NJ; j++) load_b(smem[0], j);
+    }
 
     while (have) {
         v4f_t acc[MI][NJ];
@@ -342,97 +409,63 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
 #pragma unroll
             for (int e = 0; e < 4; e++) acc[i][j][e] = fmaf(FWD ? sum[j][e] : sum[j][e] * sbv[FWD ? 0 : j][e], f, acc[i][j][e]);
         };
-        for (int s = 0; s < cur.steps; s++, st = st + 1 < NS ? st + 1 : 0) {
-            const int kpos = cur.k0 + s * GK;
-            // this step's loads have landed; NS - 2 steps' are younger
-            if (NS > 2 && ahead == NS - 1) {
-                if (wave < FW) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (NA + NB + 1)) : "memory");
-                else asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (NA + NB)) : "memory");
-            } else {
-                wait_vm0();
-            }
-            if (!FWD && (kpos < cur.k_lo || kpos + GK > cur.k_hi)) {
-                // zero the bytes of other groups' tokens (or of the padding past M) in the chunks that
-                // the range cuts, in both operands: such a byte may be a NaN code.  Each wave does the
-                // rows that it loaded, so its own wait suffices.
-                const int lo = cur.k_lo - kpos, hi = cur.k_hi - kpos;
-                int l = lane;
-                asm volatile("" : "+v"(l));
-                static_assert(FWD || TM == TN, "one count of rows");
-                constexpr int OWN = 8 * NA;
-                if (l < 2 * OWN) {
-                    const int row = wave * OWN + (l & (OWN - 1));
-                    const bool in_a = l < OWN;
-                    uint8_t* side = smem[st] + (in_a ? 0 : STAGE_A);
+        float fa[MI], sbu = 1.0f;
+        v4f_t sbv[FWD ? 1 : NJ];
+        // The order below is the order of issue (no scheduling across the barriers): while a matrix
+        // instruction runs, the vector unit adds the sums that the same column block gave for the row
+        // before, and the next row's fragment is read; in the last row the next step's first ones.
+        auto row = [&](int i, const uint8_t* now, const uint8_t* next) {
+            if (i + 1 < MI) load_a(now, i + 1);
+            else if (MI > 1) load_a(next, 0);  // (MI even)
+            const float f_new = FWD ? fa[i] * sbu : fa[i];
 #pragma unroll
-                    for (int ch = 0; ch < 8; ch++) {
-                        const int b0 = 16 * ch;
-                        if ((lo > b0 && lo < b0 + 16) || (hi > b0 && hi < b0 + 16)) {
-                            uint4* q = reinterpret_cast<uint4*>(side + (in_a ? lds_off(row, ch) : lds_offB(row, ch)));
-                            uint4 w = *q;
-                            w.x &= keep_mask4(lo, hi, b0);
-                            w.y &= keep_mask4(lo, hi, b0 + 4);
-                            w.z &= keep_mask4(lo, hi, b0 + 8);
-                            w.w &= keep_mask4(lo, hi, b0 + 12);
-                            *q = w;
-                        }
-                    }
+            for (int j = 0; j < NJ; j++) {
+                if (FWD || i > 0) add_sums(i > 0 ? i - 1 : MI - 1, j, sbv);
+                sum[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    bf[j], af[i & 1], v4f_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+                if (i == MI - 1) load_b(next, j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            f = f_new;
+            if (i == MI - 1) {
+                if (MI == 1) load_a(next, 0);
+                if (!FWD) {
+#pragma unroll
+                    for (int j = 0; j < NJ; j++) add_sums(MI - 1, j, sbv);
                 }
             }
-            barrier();
-            ahead--;
-            if (src_ok) {  // into the stage of the step before, which every wave has left
-                issue(st > 0 ? st - 1 : NS - 1);
-                ahead++;
-            }
-            const uint8_t* As = smem[st];
-            const uint8_t* Bs = As + STAGE_A;
+        };
+        auto first_rows = [&]() {  // factors, and all rows but the last
             const float* sa = &sscale[st][wm * WM + lr];
             const float* sb = &sscale[st][TM + wn * WN];
-            // The order below is the order of issue (no scheduling across the barriers): while a
-            // matrix instruction runs, the vector unit adds the sums that the same column block gave
-            // for the row before, and the next row's fragment is read.
-            v8i_t bf[NJ], af[3];
-            float fa[MI];
-            auto load_b = [&](int j) {
-                const int o = 32 * GK * (j >> 1) + 4 * GK * (j & 1);
-                bf[j] = two_chunks(Bs + fb0 + o, Bs + fb1 + o);
-            };
-            auto load_a = [&](int i) {
-                af[i % 3] = two_chunks(As + fa0 + 16 * GK * i, As + fa1 + 16 * GK * i);
-            };
-            load_b(0);
-            load_a(0);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 1; j < NJ; j++) load_b(j);
-            if (MI > 1) load_a(1);
 #pragma unroll
             for (int i = 0; i < MI; i++) fa[i] = sa[16 * i];
-            const float sbu = FWD ? sb[0] : 1.0f;  // a wave's columns lie in one weight block
-            v4f_t sbv[FWD ? 1 : NJ];
-            if (!FWD) {
+            if (FWD) sbu = sb[0];  // a wave's columns lie in one weight block
+            else
 #pragma unroll
                 for (int j = 0; j < NJ; j++) sbv[FWD ? 0 : j] = *reinterpret_cast<const v4f_t*>(sb + 32 * (j >> 1) + 8 * lq + 4 * (j & 1));
-            }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < MI; i++) {
-                if (i + 2 < MI) load_a(i + 2);
-                const float f_new = FWD ? fa[i] * sbu : fa[i];
-#pragma unroll
-                for (int j = 0; j < NJ; j++) {
-                    if (FWD || i > 0) add_sums(i > 0 ? i - 1 : MI - 1, j, sbv);
-                    sum[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        bf[j], af[i % 3], v4f_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                f = f_new;
+            for (int i = 0; i + 1 < MI; i++) row(i, smem[st], smem[st]);
+        };
+        first_rows();
+        for (int s = 1; s < cur.steps; s++) {
+            const int st_next = st + 1 < NS ? st + 1 : 0;
+            arrive(st_next);
+            if (src_ok) issue(st);
+            __builtin_amdgcn_sched_barrier(0);
+            row(MI - 1, smem[st], smem[st_next]);
+            st = st_next;
+            first_rows();
+        }
+        {
+            const int st_next = st + 1 < NS ? st + 1 : 0;
+            if (ahead > 0) {
+                arrive(st_next);
+                if (src_ok) issue(st);
             }
-            if (!FWD) {
-#pragma unroll
-                for (int j = 0; j < NJ; j++) add_sums(MI - 1, j, sbv);
-            }
+            row(MI - 1, smem[st], smem[st_next]);
+            st = st_next;
         }
         if (FWD) {
 #pragma unroll
@@ -586,10 +619,10 @@ static fp8q_status_t launch_block_gemm(BlockGemmArgs p, hipStream_t stream) {
 
 template <int MODE>
 static fp8q_status_t pick_block_gemm(const BlockGemmArgs& p, hipStream_t stream) {
-    // Where CUs would be left over, smaller tiles and loads 2 or 3 steps ahead, one block per CU (1 group,
-    // 7168 long): 512 x 2048 in 64-tiles 24 us, in 128 x 64-tiles 31, in 128-tiles 42; 960 x 2048 in
-    // 128 x 64-tiles 32 us, in 128-tiles 42, in 64-tiles, two for some CUs, 34.  Every group but one
-    // ends inside a tile, on average half way.
+    // Where CUs would be left over, smaller tiles and loads further ahead, one block per CU (1 group, 7168
+    // long): 512 x 2048 in 64-tiles 24 us, in 128 x 64-tiles 27, in 128-tiles 42; 1024 x 2048 in 128 x
+    // 64-tiles 28 us, in 128-tiles 42, in 64-tiles, two for every CU, 34.  Every group but one ends inside
+    // a tile, on average half way.
     const int64_t ends = (p.G - 1) / 2, cus = num_cus();
     auto up = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
     if (MODE == MODE_FWD) {
