@@ -586,11 +586,13 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const MoeArgs p) {
 }
 
 template <int MT, bool DOWN>
-static void launch_stream(const MoeArgs& p, hipStream_t stream) {
+static void launch_stream(MoeArgs p, hipStream_t stream) {
     const int n = p.T * p.top_k, experts = n < p.E ? n : p.E;
+    p.pass = 1;
+    while (p.pass < p.T && p.pass < 16 * MT) p.pass *= 2;
     const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
     // Parts of the contraction: two unless there are waves for the chip twice over (4096 run at a time),
-    // four below half of it, each with 4 blocks or more (layers of 32 experts of 2048 x 7168, 8 of them a
+    // four below half of it, each with 4 blocks or more, or 2 where most of the chip is idle (layers of 32 experts of 2048 x 7168, 8 of them a
     // token: 1 token 78 us in four parts, 79 in two, 88 in one; 5 tokens 231, 230 and 252; 24 tokens of 64
     // experts of 1408 x 2048 120 us in two, 129 in one).  In passes of 64 tokens one part stages them best
     // (64 tokens 315 us, in two parts 326).  One block of every part has to fit half the staging buffer
@@ -598,18 +600,33 @@ static void launch_stream(const MoeArgs& p, hipStream_t stream) {
     constexpr int NW = MT == 1 ? 4 : 8, PL = DOWN ? 2 : 1, SMAX = MT == 1 ? 4 : MT == 2 ? 4 / PL : 1;
     static_assert(moe_lds(NW) / 2 >= SMAX * PL * (MT == 1 ? 1 : 16 * MT) * 256, "a block of every part fits");
     int S = 1;
-    while (2 * S <= SMAX && 2 * S * PL * p.pass * 256 <= moe_lds(NW) / 2 && experts * pairs * S < (S == 1 ? 8192 : 4096) && kbs >= 8 * S) S *= 2;
+    while (2 * S <= SMAX && 2 * S * PL * p.pass * 256 <= moe_lds(NW) / 2 && experts * pairs * S < (S == 1 ? 8192 : 4096) && kbs >= (experts * pairs * S < 2048 ? 3 : 8) * S) S *= 2;
     const dim3 grid((unsigned)((pairs * S + NW - 1) / NW), (unsigned)(p.by_choice ? n : p.E)), block(64 * NW);
     if (S == 1) moe_stream_kernel<MT, 1, DOWN, NW><<<grid, block, 0, stream>>>(p);
     else if (S == 2) moe_stream_kernel<MT, SMAX < 2 ? 1 : 2, DOWN, NW><<<grid, block, 0, stream>>>(p);
     else moe_stream_kernel<MT, SMAX, DOWN, NW><<<grid, block, 0, stream>>>(p);
 }
 
-template <int MT>
+// The tokens of an expert that one pass takes: as many as may come, since a second pass reads the
+// weights again (65 us for 64 tokens of 32 experts of 2048 x 7168 in passes of 32).  Where the waves
+// leave half of the chip idle, the chain of one wave's blocks counts instead, and passes of 32 leave
+// room for two parts of it: 34 tokens of 4 experts of 4096 x 1024, 2 a token, 78 -> 52 us, 128 tokens
+// 165 -> 125; 64 tokens of 4 experts of 816 x 1920, all four of them, 63 -> 52 us.  Passes of 16 were
+// slower than those of 32 from 17 tokens on (1024 x 4096, 28 tokens: 52 against 45 us).
+template <bool DOWN>
+static void pick_stream(const MoeArgs& p, hipStream_t stream) {
+    const int n = p.T * p.top_k, experts = n < p.E ? n : p.E;
+    const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
+    const bool idle = experts * pairs < 2048 && kbs >= 3;
+    if (p.T <= 16) launch_stream<1, DOWN>(p, stream);
+    else if (p.T <= 32 || idle) launch_stream<2, DOWN>(p, stream);
+    else launch_stream<4, DOWN>(p, stream);
+}
+
 static fp8q_status_t launch_moe(const MoeArgs& p, hipStream_t stream) {
-    launch_stream<MT, false>(p, stream);
+    pick_stream<false>(p, stream);
     FP8Q_CHECK_LAUNCH();
-    launch_stream<MT, true>(p, stream);
+    pick_stream<true>(p, stream);
     FP8Q_CHECK_LAUNCH();
     moe_join_kernel<<<dim3((unsigned)(((int64_t)p.T * p.H / 4 + 255) / 256)), dim3(256), 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
@@ -703,7 +720,5 @@ extern "C" fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_
     p.o = reinterpret_cast<float*>(workspace) + T * top_k * I; p.y = y; p.ld_y = ld_y;
     p.T = (int)T; p.H = (int)H; p.I = (int)I; p.E = (int)E; p.top_k = top_k;
     p.by_choice = T * top_k < E;
-    p.pass = 1;
-    while (p.pass < T && p.pass < 64) p.pass *= 2;
-    return T <= 16 ? launch_moe<1>(p, stream) : T <= 32 ? launch_moe<2>(p, stream) : launch_moe<4>(p, stream);
+    return launch_moe(p, stream);
 }

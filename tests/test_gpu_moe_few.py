@@ -301,3 +301,19 @@ def test_experts_past_32_bits(fq):
     y = fq.fp8_moe_few_tokens(x, ids, weights, w13, s13, w2, s2)
     want = fq.fp8_moe_few_tokens(x, ids - (E - 2), weights, w13[-2:].clone(), s13[-2:].clone(), w2[-2:].clone(), s2[-2:].clone())
     assert torch.equal(y, want) and bool(y.isfinite().all()) and bool(y.any())
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(34, 400, 1040, 6, 2), (100, 512, 528, 3, 2), (128, 1040, 400, 4, 4), (70, 2048, 272, 2, 1)])
+def test_many_tokens_of_few_experts(fq, T, H, I, E, k):
+    """Several passes of 32 tokens over an expert's weights, the contraction in parts."""
+    x = normal(T + 1, T, H)
+    w = layer(fq, H + I, E, H, I)
+    g = torch.Generator().manual_seed(T)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32).to(DEV)
+    ids[: T // 2, 0] = E - 1  # the last expert takes more than half of the tokens
+    weights = torch.rand(T, k, generator=g).to(DEV)
+    y = fq.fp8_moe_few_tokens(x, ids, weights, *w)
+    check_layer(y, x, ids, weights, *w)
+    for t in (0, T - 1):  # and tokens by themselves
+        one = fq.fp8_moe_few_tokens(x[t:t + 1], ids[t:t + 1], weights[t:t + 1], *w)
+        check_layer(one, x[t:t + 1], ids[t:t + 1], weights[t:t + 1], *w)
