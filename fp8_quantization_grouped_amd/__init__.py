@@ -661,13 +661,18 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     else:
         _rows_of(weights, "weights", _F32, (T, top_k), dev)
         _want(weights.is_contiguous(), "weights must be contiguous")
+    need = 0
     if workspace is None:
-        workspace = torch.empty(lib().moe_route_workspace_size(T, H, E), dtype=torch.uint8,
-                                device=dev)
+        need = lib().moe_route_workspace_size(T, H, E)
+        if need:  # a small router takes none
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        need = workspace.nbytes
     _call("moe_route", dev, x.data_ptr(), T, H, _ld(x, T, H), router.data_ptr(), E,
           _ld(router, E, H),
           None if bias is None else bias.data_ptr(), _SCORING[scoring], top_k, int(renormalize),
-          scale, ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.nbytes)
+          scale, ids.data_ptr(), weights.data_ptr(),
+          None if workspace is None else workspace.data_ptr(), need)
     return ids, weights
 
 

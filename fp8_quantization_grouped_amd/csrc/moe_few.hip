@@ -649,7 +649,8 @@ static int route_splits(int64_t T, int64_t H, int64_t E) {
 }  // namespace fp8q
 
 extern "C" size_t moe_route_workspace_size(int64_t T, int64_t H, int64_t E) {
-    if (T <= 0 || H <= 0 || E <= 0 || fp8q::route_is_small(H, E)) return 256;
+    if (T <= 0 || H <= 0 || E <= 0) return 256;
+    if (fp8q::route_is_small(H, E)) return 0;
     return (size_t)fp8q::route_splits(T, H, E) * (size_t)T * (size_t)E * 4;
 }
 

@@ -414,7 +414,7 @@ fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uint8_t* a, in
  *   weights     the chosen scores (without the bias), divided by their sum if renormalize, times
  *               scale
  *   ids int32 [T][top_k], weights fp32 [T][top_k]; workspace moe_route_workspace_size bytes, any
- *   content, 4-byte aligned.
+ *   content, 4-byte aligned; it may be null where that is 0 (small routers).
  * Limits (FP8Q_ERR_UNSUPPORTED): E <= 1024, top_k <= 32, H, ld_x and ld_r multiples of 8, x and
  * router 16-byte aligned, T <= 1048560.  T == 0 is a no-op. */
 typedef enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 } fp8q_scoring_t;

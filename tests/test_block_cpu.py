@@ -168,3 +168,10 @@ def test_binding_refuses_host_tensors():
                 lambda: fq.fp8_moe_few_tokens(x, d.int(), d, q[None], d, q[None], d)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_small_router_takes_no_workspace(fn):
+    f, ws = fn("moe_route"), fn("moe_route_workspace_size")
+    assert ws(4, 256, 4) == 0 and ws(4, 2048, 64) > 0
+    #       0  1  2    3    4  5  6    7     8  9  10 11   12 13 14    15 16
+    refuse(f, [P, 4, 2048, 2048, P, 64, 2048, None, 0, 2, 1, 1.0, P, P, None, 0, None], [({1: 0}, OK), ({}, WORKSPACE)])
