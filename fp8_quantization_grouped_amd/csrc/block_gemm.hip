@@ -567,7 +567,7 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
             }
         };
         if (p.out_f32) epilogue(std::true_type{}, std::false_type{});
-        else if (p.stream_out) epilogue(std::false_type{}, std::true_type{});
+        else if (NJ == 4 && p.stream_out) epilogue(std::false_type{}, std::true_type{});
         else epilogue(std::false_type{}, std::false_type{});
         have = next_tile(follow, cur);
     }
@@ -576,12 +576,19 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
         const int esz = p.out_f32 ? 4 : 2;
         for (int idx = w_tiles + (int)blockIdx.x; idx < p.G * tpg; idx += nb) {
             const int g = s_perm[idx / tpg], l = idx % tpg, r0 = l / p.nt_n * TM, c0 = l % p.nt_n * TN;
-            for (int i = t; i < TM * TN; i += NT) {
-                const int row = r0 + i / TN, col = c0 + i % TN;
+            const int width = p.vec_store ? 8 : 1;  // columns of a thread
+            for (int i = t; i < TM * TN / width; i += NT) {
+                const int row = r0 + i * width / TN, col = c0 + i * width % TN;
                 if (row < p.K && col < p.N) {
                     uint8_t* dst = p.c + (((int64_t)g * p.K + row) * p.ldc + col) * esz;
-                    if (p.out_f32) *reinterpret_cast<float*>(dst) = 0.0f;
-                    else *reinterpret_cast<uint16_t*>(dst) = 0;
+                    if (p.vec_store) {
+                        reinterpret_cast<uint4*>(dst)[0] = make_uint4(0, 0, 0, 0);
+                        if (p.out_f32) reinterpret_cast<uint4*>(dst)[1] = make_uint4(0, 0, 0, 0);
+                    } else if (p.out_f32) {
+                        *reinterpret_cast<float*>(dst) = 0.0f;
+                    } else {
+                        *reinterpret_cast<uint16_t*>(dst) = 0;
+                    }
                 }
             }
         }
@@ -609,7 +616,7 @@ static fp8q_status_t launch_block_gemm(BlockGemmArgs p, hipStream_t stream) {
     const int64_t tiles = MODE == MODE_FWD ? ((int64_t)(p.M + TM - 1) / TM + p.G) * p.nt_n : (int64_t)p.G * p.nt_k * p.nt_n;
     // offsets that go up and down can make every group as long as M
     const int64_t most = MODE == MODE_FWD ? (int64_t)p.G * ((p.M + TM - 1) / TM) * p.nt_n : tiles;
-    if (tiles >= 0x7FFFFFFFLL || most >= 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
+    if (tiles >= 0x7FFF0000LL || most >= 0x7FFF0000LL) return FP8Q_ERR_UNSUPPORTED;
     int64_t grid = (int64_t)num_cus() * (TM == 256 || NS > 2 ? 1 : 2);
     if (tiles < grid) grid = (tiles + 7) / 8 * 8;  // whole rounds of the XCDs
     block_gemm_kernel<MODE, TM, TN, NS><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(p);

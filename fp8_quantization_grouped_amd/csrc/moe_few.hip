@@ -587,7 +587,8 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const MoeArgs p) {
 
 template <int MT, bool DOWN>
 static void launch_stream(MoeArgs p, hipStream_t stream) {
-    const int n = p.T * p.top_k, experts = n < p.E ? n : p.E;
+    const int n = p.T * p.top_k;
+    const int64_t experts = n < p.E ? n : p.E;
     p.pass = 1;
     while (p.pass < p.T && p.pass < 16 * MT) p.pass *= 2;
     const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
@@ -615,7 +616,8 @@ static void launch_stream(MoeArgs p, hipStream_t stream) {
 // slower than those of 32 from 17 tokens on (1024 x 4096, 28 tokens: 52 against 45 us).
 template <bool DOWN>
 static void pick_stream(const MoeArgs& p, hipStream_t stream) {
-    const int n = p.T * p.top_k, experts = n < p.E ? n : p.E;
+    const int n = p.T * p.top_k;
+    const int64_t experts = n < p.E ? n : p.E;
     const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
     const bool idle = experts * pairs < 2048 && kbs >= 3;
     if (p.T <= 16) launch_stream<1, DOWN>(p, stream);
