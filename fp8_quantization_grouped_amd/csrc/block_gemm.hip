@@ -9,7 +9,7 @@
 // zero, and each of its results is added to an accumulator times its factors by one fused
 // multiply-add (the weight gradient: a product more).  Those run on the vector units while the
 // matrix cores work on the next row of results: the sums of row i are added while row i + 1 is
-// multiplied, 16 lanes' worth of work per 32-cycle matrix instruction.
+// multiplied, four multiply-adds per 32-cycle matrix instruction.
 //
 // Tiles: TM x TN outputs by 8 waves, 128-byte steps, operands straight from memory into NS LDS
 // stages (layout and swizzles: gemm_tile.hpp), one barrier per step, before its last row of results:
