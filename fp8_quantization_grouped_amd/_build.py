@@ -7,7 +7,8 @@ The device assembly of each file is kept beside its object and checked: no kerne
 generic (flat) memory instruction.  A flat access is routed to LDS or to global memory by the
 aperture its base address register falls in, so an address the compiler forms as "base below
 the LDS aperture + immediate offset" faults with an aperture violation; every access here is
-written against LDS or global memory explicitly.
+written against LDS or global memory explicitly.  And a memory instruction inside inline assembly,
+where the compiler inserts no waits for hazards, must follow enough of them in its own block.
 """
 from __future__ import annotations
 
@@ -53,6 +54,35 @@ def device_asm(src_name: str) -> str:
     return os.path.join(BUILD_DIR, f"{src_name}-hip-amdgcn-amd-amdhsa-{ARCH}.s")
 
 
+ASM_BLOCK = re.compile(r"^\s*;+#ASMSTART\s*\n(.*?)^\s*;+#ASMEND", re.M | re.S)
+MEMORY_INSN = re.compile(r"(buffer|global|scratch)_(load|store|atomic)")
+# Wait states between a vector instruction that writes a scalar register and a memory instruction
+# that reads it, and between a scalar write of M0 and a load to LDS (gfx9; not made by the hardware).
+SGPR_WAIT, M0_WAIT = 5, 1
+
+
+def unguarded_asm(text: str) -> list[str]:
+    """Memory instructions of device assembly's inline blocks that come too soon after the block's
+    start (what ran before it may have written their scalar registers) or after a write of M0."""
+    bad = []
+    for block in ASM_BLOCK.findall(text):
+        since_start = since_m0 = 0
+        for line in block.splitlines():
+            insn = line.split(";")[0].split("//")[0].strip()
+            if not insn:
+                continue
+            name, _, args = insn.partition(" ")
+            if MEMORY_INSN.match(name) and (
+                    since_start < SGPR_WAIT or (re.search(r"\blds\b", args) and since_m0 < M0_WAIT)):
+                bad.append(insn)
+            states = int(args.strip(), 0) + 1 if name == "s_nop" else 1
+            since_start += states
+            since_m0 += states
+            if name.startswith("s_") and re.match(r"\s*m0\b", args):
+                since_m0 = 0
+    return bad
+
+
 def check_device_asm(srcs: list[str]) -> None:
     for s in srcs:
         name = os.path.basename(s)[:-4]
@@ -61,6 +91,10 @@ def check_device_asm(srcs: list[str]) -> None:
         if hits:
             raise RuntimeError(f"{name}.hip: generic (flat) memory instructions in device code: "
                                f"{hits[:4]} ({len(hits)} in all)")
+        hits = unguarded_asm(text)
+        if hits:
+            raise RuntimeError(f"{name}.hip: memory instructions in inline assembly without the waits "
+                               f"before them: {hits[:4]} ({len(hits)} in all)")
 
 
 def build(verbose: bool = False) -> str:

@@ -17,23 +17,29 @@ __device__ __forceinline__ i32x4_t make_rsrc4(const void* base, uint32_t bytes) 
 // 16 bytes per lane from a buffer straight into LDS at lds_base + 16*lane (lds_base is
 // wave-uniform).  Written as inline assembly so that the compiler does not order every later
 // LDS read after it: the waits are explicit (s_waitcnt vmcnt before the step's barrier).
+//
+// The compiler's hazard pass does not look inside, so each block holds the waits that gfx9 asks for
+// and the hardware does not make: one state between the write of M0 and a load to LDS, which takes
+// its address from there, and five between a vector instruction that wrote one of the descriptor's or
+// the offset's scalar registers (a lane read that fills a descriptor or brings a spilled one back)
+// and the load that reads it.  s_mov is one state and s_nop 3 four; the build checks every block.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t voff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds_base), "v"(voff), "s"(rsrc)
                  : "memory", "m0");
 }
 // The same with a wave-uniform offset on top of the lanes'.
 __device__ __forceinline__ void dma16_at(i32x4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(lds_base), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(i32x4_t rsrc, uint32_t voff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(lds_base), "v"(voff), "s"(rsrc)
                  : "memory", "m0");
