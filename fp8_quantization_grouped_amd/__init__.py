@@ -431,9 +431,10 @@ def _matrix(t: torch.Tensor, what: str, dtypes):
 
 
 def _ld(t: torch.Tensor, rows: int, cols: int) -> int:
-    """Leading dimension of a rows x cols matrix; the stride of a single or an empty row says
-    nothing."""
-    ld = t.stride()[0]
+    """Leading dimension of rows x cols elements (groups of matrices: rows of all of them); the
+    stride of a single or an empty row says nothing.  Any other is handed on as it is: rows that
+    overlap (an expanded tensor) are for the C entry point to refuse."""
+    ld = t.stride()[-2]
     return ld if rows > 1 and cols > 0 else 0 if cols == 0 else max(ld, cols)
 
 
@@ -520,7 +521,7 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
         else:
             _rows_of(s_rows, "s_rows", _F32, (_blocks(cols), rows), dev)
         row_args = (q.data_ptr(), _ld(q, rows, cols), s_rows.data_ptr(),
-                    max(_ld(s_rows, _blocks(cols), rows), rows))
+                    _ld(s_rows, _blocks(cols), rows))
     if q_t is None:
         q_t = _padded_bytes(cols, rows, dev)
     else:
@@ -530,8 +531,8 @@ def fp8_block_quant_dual(x: torch.Tensor, q: torch.Tensor | None = None,
     else:
         _rows_of(s_cols, "s_cols", _F32, (_blocks(rows), cols), dev)
     _call("fp8_block_quant_dual", dev, x.data_ptr(), rows, cols, _ld(x, rows, cols), *row_args,
-          q_t.data_ptr(), max(_ld(q_t, cols, rows), rows), s_cols.data_ptr(),
-          max(_ld(s_cols, _blocks(rows), cols), cols))
+          q_t.data_ptr(), _ld(q_t, cols, rows), s_cols.data_ptr(),
+          _ld(s_cols, _blocks(rows), cols))
     return (q, s_rows), (q_t, s_cols)
 
 
@@ -558,7 +559,7 @@ def fp8_block_quant_weights(w: torch.Tensor, experts: int, q: torch.Tensor | Non
         _rows_of(scales, "scales", _F32, shape, dev)
         _want(scales.is_contiguous(), "scales must be contiguous")
     _call("fp8_block_quant_weights", dev, w.data_ptr(), experts, rows, cols, _ld(w, total, cols),
-          q.data_ptr(), _ld(q, total, cols), q_t.data_ptr(), max(_ld(q_t, cols, total), total),
+          q.data_ptr(), _ld(q, total, cols), q_t.data_ptr(), _ld(q_t, cols, total),
           scales.data_ptr())
     return q, q_t, scales
 
@@ -590,7 +591,7 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
     _rows_of(b, "b", _BYTES, (groups, N, inner) if fwd else (N, inner), dev)
     kb = -(-inner // BLOCK)
     _rows_of(a_scales, "a_scales", _F32, (kb, rows), dev)
-    ld_sa = max(a_scales.stride(0), rows) if kb > 1 else rows
+    ld_sa = _ld(a_scales, kb, rows)
     if fwd:
         nb = -(-N // BLOCK)
         _factors(b_scales, "b_scales", (groups, nb, kb), dev)
@@ -609,7 +610,7 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
     else:
         _rows_of(b_scales, "b_scales", _F32, (kb, N), dev)
         bgs, ldb, sbg, sbn = 0, _ld(b, N, inner), 0, 1
-        sbk = max(b_scales.stride(0), N) if kb > 1 else N
+        sbk = _ld(b_scales, kb, N)
         M, K, shape = inner, rows, (groups, rows, N)
     if c is None:
         _want(out_dtype in _OUT, "the output must be bfloat16 or float32")
@@ -618,7 +619,7 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
     else:
         c = _gemm_out(c, shape, out_dtype, dev)
         _want(c.device == dev, "c must be on the operands' GPU")
-        ldc = c.stride(-2) if c.shape[-2] > 1 else max(c.stride(-2), N)
+        ldc = _ld(c, c.shape[-2] if fwd else groups * c.shape[-2], N)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     _call("fp8_block_grouped_gemm", dev, mode, a.data_ptr(), _ld(a, rows, inner),
           a_scales.data_ptr(), ld_sa, b.data_ptr(), ldb, bgs, b_scales.data_ptr(), sbn, sbk, sbg,

@@ -1,0 +1,106 @@
+"""What the binding of the block-scaled operators hands to the C entry points, without a GPU: host
+tensors that say they are on one, and a library that records its calls instead of making them."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import fp8_quantization_grouped_amd as fq
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that passes the binding's device checks."""
+    is_cuda = property(lambda self: True)
+
+
+def gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+def zeros(*shape, dtype=torch.float32):
+    return gpu(torch.zeros(*shape, dtype=dtype))
+
+
+class Recorder:
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if name.endswith("_size") or name.endswith("status_string"):
+            return getattr(self.real, name)
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    r = Recorder(fq.lib())
+    monkeypatch.setattr(fq, "_lib", r)
+    monkeypatch.setattr(fq, "_device_now", lambda: None)
+    monkeypatch.setattr(fq, "_raw_stream", lambda index: 0)
+    return r.calls
+
+
+BF16, U8, F32 = torch.bfloat16, torch.uint8, torch.float32
+
+
+# --------------------------------------- rows that overlap: the C checks have to see their stride
+
+def overlapping(rows, cols, dtype=F32, stride=0):
+    """[rows, cols] of one row's storage (stride 0), or of rows that begin stride apart."""
+    return gpu(torch.zeros(cols + stride * (rows - 1), dtype=dtype).as_strided((rows, cols), (stride, 1)))
+
+
+@pytest.mark.parametrize("stride", [0, 3])
+def test_overlapping_factors_of_a_product_reach_its_checks(calls, stride):
+    M, N, K, G = 64, 32, 512, 2
+    off = zeros(G, dtype=torch.int32)
+    fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, zeros(M, K, dtype=U8), overlapping(4, M, stride=stride),
+                              zeros(G, N, K, dtype=U8), zeros(G, 1, 4), off)
+    assert calls[-1][1][4] == stride < M  # ld_sa: refused
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, zeros(K, 512, dtype=U8), zeros(4, K), zeros(N, 512, dtype=U8),
+                              overlapping(4, N, stride=stride), off)
+    assert calls[-1][1][10] == stride < N  # sb_k: refused
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, zeros(K, 512, dtype=U8), overlapping(4, K, stride=stride),
+                              zeros(N, 512, dtype=U8), zeros(4, N), off)
+    assert calls[-1][1][4] == stride < K
+
+
+@pytest.mark.parametrize("stride", [0, 3])
+def test_overlapping_outputs_of_the_quantizers_reach_their_checks(calls, stride):
+    x = zeros(300, 256, dtype=BF16)
+    for kw, at in (({"s_rows": overlapping(2, 300, stride=stride)}, 7), ({"q_t": overlapping(256, 300, U8, stride)}, 9),
+                   ({"s_cols": overlapping(3, 256, stride=stride)}, 11), ({"q": overlapping(300, 256, U8, stride)}, 5)):
+        fq.fp8_block_quant_dual(x, **kw)
+        assert calls[-1][1][at] == stride, kw.keys()
+    fq.fp8_block_quant_weights(x, 3, q_t=overlapping(256, 300, U8, stride))
+    assert calls[-1][1][8] == stride
+
+
+@pytest.mark.parametrize("stride", [0, 1])
+def test_overlapping_gradients_of_one_row_each_reach_the_checks(calls, stride):
+    """[groups, 1, N] with the groups on top of each other."""
+    G, N = 3, 32
+    c = gpu(torch.zeros(64, dtype=BF16).as_strided((G, 1, N), (stride, stride, 1)))
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, zeros(1, 128, dtype=U8), zeros(1, 1), zeros(N, 128, dtype=U8), zeros(1, N),
+                              zeros(G, dtype=torch.int32), c=c)
+    assert calls[-1][1][18] == stride < N  # ldc
+
+
+def test_ordinary_strides_are_handed_on(calls):
+    M, N, K, G = 64, 32, 512, 2
+    off = zeros(G, dtype=torch.int32)
+    wide = zeros(4, M + 6)[:, :M]
+    c = zeros(M, N + 5, dtype=BF16)[:, :N]
+    fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, zeros(M, K, dtype=U8), wide, zeros(G, N, K, dtype=U8), zeros(G, 1, 4), off, c=c)
+    assert calls[-1][1][4] == M + 6 and calls[-1][1][18] == N + 5
+    c = zeros(G, K, N + 5, dtype=F32)[:, :, :N]
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, zeros(K, 512, dtype=U8), zeros(4, K), zeros(N, 512, dtype=U8),
+                              zeros(4, N + 3)[:, :N], off, c=c)
+    assert calls[-1][1][10] == N + 3 and calls[-1][1][18] == N + 5
+    one = gpu(torch.zeros(N, dtype=F32).as_strided((1, N), (1, 1)))  # one row: its stride says nothing
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, zeros(K, 128, dtype=U8), zeros(1, K), zeros(N, 128, dtype=U8), one, off)
+    assert calls[-1][1][10] >= N
+    fq.fp8_block_quant_dual(zeros(0, 256, dtype=BF16))
+    fq.fp8_block_quant_dual(zeros(5, 0, dtype=BF16))
+    args = calls[-1][1]
+    assert args[7] >= 5 and args[9] >= 5 and args[11] >= 0
