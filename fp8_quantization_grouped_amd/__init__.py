@@ -477,6 +477,13 @@ def _factors(s: torch.Tensor, what: str, shape, dev) -> None:
         raise ValueError(f"{what} must be float32 {shape} on the operands' GPU")
 
 
+def _workspace(ws: torch.Tensor, dev):
+    """Pointer and bytes of a caller's workspace: one run of memory on the operands' GPU."""
+    if not (ws.is_cuda and ws.device == dev and ws.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on the operands' GPU")
+    return ws.data_ptr(), ws.nbytes
+
+
 def fp8_block_quant_rowwise(x: torch.Tensor, q: torch.Tensor | None = None,
                             scales: torch.Tensor | None = None):
     """x: bf16 [rows, cols] in blocks of 1 x 128.  Returns (q [rows, cols] e4m3fn bytes, scales
@@ -620,7 +627,7 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
         c = _gemm_out(c, shape, out_dtype, dev)
         _want(c.device == dev, "c must be on the operands' GPU")
         ldc = _ld(c, c.shape[-2] if fwd else groups * c.shape[-2], N)
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace, dev)
     _call("fp8_block_grouped_gemm", dev, mode, a.data_ptr(), _ld(a, rows, inner),
           a_scales.data_ptr(), ld_sa, b.data_ptr(), ldb, bgs, b_scales.data_ptr(), sbn, sbk, sbg,
           off, groups, M, N, K, c.data_ptr(), ldc, _OUT[c.dtype], ws, ws_bytes)
@@ -662,18 +669,19 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     else:
         _rows_of(weights, "weights", _F32, (T, top_k), dev)
         _want(weights.is_contiguous(), "weights must be contiguous")
-    need = 0
+    ws = None
     if workspace is None:
         need = lib().moe_route_workspace_size(T, H, E)
         if need:  # a small router takes none
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
     else:
-        need = workspace.nbytes
+        ws, need = _workspace(workspace, dev)
     _call("moe_route", dev, x.data_ptr(), T, H, _ld(x, T, H), router.data_ptr(), E,
           _ld(router, E, H),
           None if bias is None else bias.data_ptr(), _SCORING[scoring], top_k, int(renormalize),
           scale, ids.data_ptr(), weights.data_ptr(),
-          None if workspace is None else workspace.data_ptr(), need)
+          ws, need)
     return ids, weights
 
 
@@ -723,7 +731,10 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     if workspace is None:
         need = fp8_moe_few_tokens_workspace_size(T, H, I, top_k)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    else:
+        ws, need = _workspace(workspace, dev)
     _call("fp8_moe_few_tokens", dev, x.data_ptr(), T, H, _ld(x, T, H), ids.data_ptr(),
           weights.data_ptr(), top_k, *args13, *args2, E, I, y.data_ptr(), _ld(y, T, H),
-          workspace.data_ptr(), workspace.nbytes)
+          ws, need)
     return y

@@ -104,3 +104,35 @@ def test_ordinary_strides_are_handed_on(calls):
     fq.fp8_block_quant_dual(zeros(5, 0, dtype=BF16))
     args = calls[-1][1]
     assert args[7] >= 5 and args[9] >= 5 and args[11] >= 0
+
+
+# ------------------------------------------------------------------------ workspaces of the caller
+
+def moe_args(T=4, H=256, I=128, E=3, k=2):
+    return (zeros(T, H, dtype=BF16), zeros(T, k, dtype=torch.int32), zeros(T, k), zeros(E, 2 * I, H, dtype=U8),
+            zeros(E, 2 * I // 128, 2), zeros(E, H, I, dtype=U8), zeros(E, 2, 1))
+
+
+def with_workspace(kind, ws):
+    if kind == "product":
+        return fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, zeros(4, 256, dtype=U8), zeros(2, 4), zeros(1, 8, 256, dtype=U8),
+                                         zeros(1, 1, 2), workspace=ws)
+    if kind == "route":
+        return fq.moe_route(zeros(4, 4096, dtype=BF16), zeros(64, 4096, dtype=BF16), 2, workspace=ws)
+    return fq.fp8_moe_few_tokens(*moe_args(), workspace=ws)
+
+
+@pytest.mark.parametrize("kind", ["product", "route", "layer"])
+def test_workspaces_are_checked(calls, kind):
+    n = 1 << 16
+    for bad in (torch.zeros(n, dtype=U8),                       # host memory
+                zeros(1, dtype=U8).expand(n),                   # one byte that says it is many
+                zeros(2 * n, dtype=U8)[::2],
+                gpu(torch.zeros(n, dtype=U8, device="meta"))):  # another device
+        with pytest.raises(ValueError, match="workspace"):
+            with_workspace(kind, bad)
+    assert calls == []
+    with_workspace(kind, zeros(n, dtype=U8))
+    with_workspace(kind, zeros(n // 4))  # any type
+    with_workspace(kind, zeros(8, n // 8, dtype=U8))
+    assert len(calls) == 3 and all(n in args for _, args in calls)
