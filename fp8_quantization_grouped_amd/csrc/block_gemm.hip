@@ -683,8 +683,8 @@ extern "C" fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uin
     // 32-bit tile indices, contraction positions and offsets within 256 rows; a column block's
     // factor is reached with a 32-bit byte offset
     constexpr int64_t most = 0x7FFFFF00LL;
-    if (groups > GMAX || M > most || N > most || K > most || 256 * lda > most || 256 * ldb > most || 256 * ldc * esz > most ||
-        (fwd && (N / GK + 1) * sb_n > (1LL << 29)))
+    if (groups > GMAX || M > most || N > most || K > most || lda > most / 256 || ldb > most / 256 || ldc > most / (256 * esz) ||
+        (fwd && sb_n > (1LL << 29) / (N / GK + 1)))
         return FP8Q_ERR_UNSUPPORTED;
     BlockGemmArgs p{};
     p.a = a; p.lda = lda; p.sa = a_scales; p.ld_sa = ld_sa; p.b = b; p.ldb = ldb; p.bgs = b_group_stride;

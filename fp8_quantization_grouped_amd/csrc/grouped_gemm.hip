@@ -830,7 +830,7 @@ static fp8q_status_t launch_gemm(GemmArgs p, hipStream_t stream) {
 
 // 32-bit buffer offsets: a 256-row tile of either operand must span less than 2^31 bytes.
 static inline bool offsets_fit(int64_t lda, int64_t ldb) {
-    return (int64_t)GT * lda < 0x7FFFFFFFLL && (int64_t)GT * ldb < 0x7FFFFFFFLL;
+    return lda <= 0x7FFFFFFELL / GT && ldb <= 0x7FFFFFFELL / GT;
 }
 
 // Workspace of every grouped GEMM: the two status words of the offsets check, padded.

@@ -710,7 +710,7 @@ extern "C" fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_
     if (T == 0) return FP8Q_OK;
     if (!x || !ids || !weights || !w13 || !s13 || !w2 || !s2 || !y) return FP8Q_ERR_INVALID_ARG;
     if (T > MOE_MAX_T || E > MOE_MAX_E || top_k > MOE_MAX_K || H % 16 || I % 16 || H > 0x3FFFFFFF || I > 0x3FFFFFFF || ld13 >= (1 << 26) ||
-        ld2 >= (1 << 26) || T * ld_x >= (1 << 30) ||
+        ld2 >= (1 << 26) || ld_x > ((1 << 30) - 1) / T ||
         T * top_k * I >= (1 << 29) || ld_x % 8 || ld13 % 16 || ld2 % 16 || w13_group_stride % 16 || w2_group_stride % 16 || !fp8q_aligned(x, 16) ||
         !fp8q_aligned(w13, 16) || !fp8q_aligned(w2, 16))
         return FP8Q_ERR_UNSUPPORTED;
