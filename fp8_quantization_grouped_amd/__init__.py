@@ -430,12 +430,18 @@ def _matrix(t: torch.Tensor, what: str, dtypes):
     return rows, cols, dev
 
 
+def _one_row(ld: int, cols: int) -> int:
+    """Leading dimension for a matrix of one row, whose stride ld says nothing but where it covers
+    the row's end up to whole 16 elements (padding that the products may read)."""
+    return min(max(ld, cols), -(-cols // 16) * 16)
+
+
 def _ld(t: torch.Tensor, rows: int, cols: int) -> int:
     """Leading dimension of rows x cols elements (groups of matrices: rows of all of them); the
     stride of a single or an empty row says nothing.  Any other is handed on as it is: rows that
     overlap (an expanded tensor) are for the C entry point to refuse."""
     ld = t.stride()[-2]
-    return ld if rows > 1 and cols > 0 else 0 if cols == 0 else max(ld, cols)
+    return ld if rows > 1 and cols > 0 else _one_row(ld, cols)
 
 
 # the current stream's handle without a Stream object made for it
@@ -612,7 +618,7 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
         if kb <= 1:
             sbk = 0
         if N <= 1:
-            ldb = max(ldb, inner)
+            ldb = _one_row(ldb, inner)
         M, K, shape = rows, inner, (rows, N)
     else:
         _rows_of(b_scales, "b_scales", _F32, (kb, N), dev)

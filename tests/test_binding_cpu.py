@@ -136,3 +136,39 @@ def test_workspaces_are_checked(calls, kind):
     with_workspace(kind, zeros(n // 4))  # any type
     with_workspace(kind, zeros(8, n // 8, dtype=U8))
     assert len(calls) == 3 and all(n in args for _, args in calls)
+
+
+# -------------------------------------------------- one row: whatever its stride, it is no limit
+
+def one_row(cols, stride, dtype):
+    return gpu(torch.zeros(cols, dtype=dtype).as_strided((1, cols), (stride, 1)))
+
+
+@pytest.mark.parametrize("stride", [1, 256, 257, 4097, 1 << 25, 1 << 34, 1 << 58])
+def test_one_row_of_any_stride(calls, stride):
+    """A token cut out of a longer buffer ([:1], or [:, -1] of a batch of one)."""
+    H, I, E, k = 256, 128, 3, 2
+    x = one_row(H, stride, BF16)
+    fq.moe_route(x, zeros(E, H, dtype=BF16), k)
+    assert calls[-1][1][3] == H
+    _, ids, weights, *w = moe_args(1, H, I, E, k)
+    fq.fp8_moe_few_tokens(x, ids, weights, *w, y=one_row(H, stride, BF16))
+    assert calls[-1][1][3] == H and calls[-1][1][24] == H
+    fq.fp8_block_quant_rowwise(x)
+    assert calls[-1][1][3] == H
+    a, b = one_row(H, stride, U8), gpu(torch.zeros(H, dtype=U8).as_strided((1, 1, H), (stride, stride, 1)))
+    fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, a, zeros(2, 1), b, zeros(1, 1, 2), c=one_row(1, stride, F32))
+    args = calls[-1][1]
+    assert args[2] == H and args[6] == H and args[7] == 0 and args[18] in (1, 16)
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, a, zeros(2, 1), a, zeros(2, 1))
+    assert calls[-1][1][2] == H and calls[-1][1][6] == H
+
+
+def test_one_padded_row_keeps_its_padding(calls):
+    """A row of 1333 bytes whose storage goes on to 1344: the product takes it, as it takes many."""
+    a = gpu(torch.zeros(1, 1344, dtype=U8))[:, :1333]
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, a, zeros(11, 1), a, zeros(11, 1))
+    assert calls[-1][1][2] == 1344 and calls[-1][1][6] == 1344
+    bare = zeros(1, 1333, dtype=U8)
+    fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, bare, zeros(11, 1), a, zeros(11, 1))
+    assert calls[-1][1][2] == 1333  # refused: nothing says that there are 1344 bytes
