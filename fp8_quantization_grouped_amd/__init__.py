@@ -619,6 +619,8 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
             sbk = 0
         if N <= 1:
             ldb = _one_row(ldb, inner)
+        if inner == 0:  # nothing is read, and the strides of no elements are no strides
+            bgs = ldb = 0
         M, K, shape = rows, inner, (rows, N)
     else:
         _rows_of(b_scales, "b_scales", _F32, (kb, N), dev)

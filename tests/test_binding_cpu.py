@@ -172,3 +172,11 @@ def test_one_padded_row_keeps_its_padding(calls):
     bare = zeros(1, 1333, dtype=U8)
     fq.fp8_block_grouped_gemm(fq.GEMM_WGRAD_KGROUPED, bare, zeros(11, 1), a, zeros(11, 1))
     assert calls[-1][1][2] == 1333  # refused: nothing says that there are 1344 bytes
+
+
+def test_a_contraction_of_length_zero_is_taken(calls):
+    """The strides of tensors without elements are 1, which is no multiple of 16."""
+    fq.fp8_block_grouped_gemm(fq.GEMM_FWD_MGROUPED, zeros(8, 0, dtype=U8), zeros(0, 8), zeros(2, 5, 0, dtype=U8), zeros(2, 1, 0),
+                              zeros(2, dtype=torch.int32))
+    args = calls[-1][1]
+    assert args[2] % 16 == 0 and args[6] % 16 == 0 and args[7] % 16 == 0 and args[14:17] == (8, 5, 0)
