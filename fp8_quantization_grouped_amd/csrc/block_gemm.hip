@@ -73,6 +73,31 @@ __device__ __forceinline__ v8i_t two_chunks(const uint8_t* lo, const uint8_t* hi
     return v8i_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
+// Group g's end, as the caller gave it.  Read as constant memory: a uniform group's comes by a scalar
+// load, which the waits on the operands' loads do not count.
+__device__ __forceinline__ int group_end(const BlockGemmArgs& p, int g) {
+    typedef const __attribute__((address_space(4))) int32_t* const_i32;
+    return p.offsets ? ((const_i32)(uintptr_t)p.offsets)[g] : p.M;
+}
+
+// The offsets check's two words, by one wave.
+__device__ __forceinline__ void report_offsets(const BlockGemmArgs& p, int lane) {
+    int bad = 0x7FFFFFFF;
+    for (int i = lane; i < p.G; i += 64) {
+        const int64_t lo = i == 0 ? 0 : group_end(p, i - 1), hi = group_end(p, i);
+        if ((hi < lo || hi > p.M || (i == p.G - 1 && hi != p.M)) && i < bad) bad = i;
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const int o = __shfl_xor(bad, off, 64);
+        bad = o < bad ? o : bad;
+    }
+    if (lane == 0) {
+        p.status[0] = bad == 0x7FFFFFFF ? (int32_t)FP8Q_OK : (int32_t)FP8Q_ERR_INVALID_ARG;
+        p.status[1] = bad == 0x7FFFFFFF ? -1 : bad;
+    }
+}
+
 template <int MODE, int TM, int TN, int NS>
 __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(const BlockGemmArgs p) {
     constexpr bool FWD = MODE == MODE_FWD;
@@ -92,11 +117,7 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
     const int wm = wave / WC, wn = wave % WC;
     const int lr = lane & 15, lq = lane >> 4;
 
-    // the offsets as constant memory: a uniform group's come by scalar loads, which the waits on the
-    // operands' loads do not count
-    typedef const __attribute__((address_space(4))) int32_t* const_i32;
-    const const_i32 offsets = (const_i32)(uintptr_t)p.offsets;
-    auto end_of = [&](int g) -> int { return p.offsets ? offsets[g] : p.M; };
+    auto end_of = [&](int g) -> int { return group_end(p, g); };
     // group g's rows, clamped so that any offsets content stays in range
     auto rows_of = [&](int lo, int hi, int& l, int& h) {
         l = lo < 0 ? 0 : lo > p.M ? p.M : lo;
@@ -105,22 +126,7 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
     auto group_rows = [&](int g, int& l, int& h) { rows_of(g == 0 ? 0 : end_of(g - 1), end_of(g), l, h); };
 
     // --- the offsets check (block 0's last wave) and the schedule's table
-    if (p.status != nullptr && blockIdx.x == 0 && wave == 7) {
-        int bad = 0x7FFFFFFF;
-        for (int i = lane; i < p.G; i += 64) {
-            const int64_t lo = i == 0 ? 0 : end_of(i - 1), hi = end_of(i);
-            if ((hi < lo || hi > p.M || (i == p.G - 1 && hi != p.M)) && i < bad) bad = i;
-        }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            const int o = __shfl_xor(bad, off, 64);
-            bad = o < bad ? o : bad;
-        }
-        if (lane == 0) {
-            p.status[0] = bad == 0x7FFFFFFF ? (int32_t)FP8Q_OK : (int32_t)FP8Q_ERR_INVALID_ARG;
-            p.status[1] = bad == 0x7FFFFFFF ? -1 : bad;
-        }
-    }
+    if (p.status != nullptr && blockIdx.x == 0 && wave == 7) report_offsets(p, lane);
     if (FWD) {
         if (wave == 0) {
             int base = 0;
@@ -595,8 +601,9 @@ __global__ __launch_bounds__(512, TM == 256 ? 2 : 4) void block_gemm_kernel(cons
     }
 }
 
-// The forward's output where there is nothing to sum (K == 0).
+// The forward's output where there is nothing to sum (K == 0), and its offsets check.
 __global__ __launch_bounds__(256) void block_zero_kernel(const BlockGemmArgs p) {
+    if (p.status != nullptr && blockIdx.x == 0 && threadIdx.x < 64) report_offsets(p, threadIdx.x);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.M * p.N; i += (int64_t)gridDim.x * 256) {
         const int64_t at = i / p.N * p.ldc + i % p.N;
         if (p.out_f32) reinterpret_cast<float*>(p.c)[at] = 0.0f;
