@@ -114,9 +114,22 @@ __global__ __launch_bounds__(256) void route_logits_kernel(const RouteArgs p) {
     }
 }
 
+// Renormalized weights come from the scores where their sum is at least this: a score that underflows
+// then weighs less than 2^-62.  Below it they come from the chosen logits l_j and their maximum m, as
+// exp(l_j - m) / sum exp(l_i - m): a softmax's chosen scores have these ratios, and so have sigmoids
+// of logits below -44, whose 1 + exp(l) is 1 in 32 bits.
+constexpr float kTinySum = 5.421010862427522e-20f;  // 2^-64
+
+// What a block needs beside the logits to choose a token's experts.
+struct Choice {
+    float logit[256], by[256], chosen[MOE_MAX_K], chosen_logit[MOE_MAX_K];
+};
+
 // Scores, choice and weights of one token from its logits in LDS, by a whole block of at least E
 // threads: an expert's place is the number of experts that go before it.
-__device__ __forceinline__ void choose(const RouteArgs& p, int64_t t, const float* logit, float* by, float* chosen) {
+__device__ __forceinline__ void choose(const RouteArgs& p, int64_t t, Choice& s) {
+    const float* logit = s.logit;
+    float* by = s.by;
     const int e = threadIdx.x;
     const float l = e < p.E ? logit[e] : 0.0f;
     float score = 1.0f / (1.0f + expf(-l));
@@ -142,39 +155,48 @@ __device__ __forceinline__ void choose(const RouteArgs& p, int64_t t, const floa
         const float v = by[e];
         place = 0;
         for (int j = 0; j < p.E; j++) place += by[j] > v || (by[j] == v && j < e);
-        if (place < p.top_k) chosen[place] = score;
+        if (place < p.top_k) {
+            s.chosen[place] = score;
+            s.chosen_logit[place] = l;
+        }
     }
     __syncthreads();
     if (place < p.top_k) {
         float total = 0.0f;
-        for (int j = 0; j < p.top_k; j++) total += chosen[j];
-        // a sum that vanished (every chosen score underflowed) gives zeros, not 0 / 0; fmaxf drops
-        // a NaN: keep it visible
-        const float w = p.renorm ? score / fmaxf(total, 1e-30f) : score;
+        for (int j = 0; j < p.top_k; j++) total += s.chosen[j];
+        float w = score;
+        if (p.renorm && total < kTinySum) {
+            float m = -INFINITY, sum = 0.0f;
+            for (int j = 0; j < p.top_k; j++) m = fmaxf(m, s.chosen_logit[j]);
+            for (int j = 0; j < p.top_k; j++) sum += expf(s.chosen_logit[j] - m);
+            w = m > -INFINITY ? expf(l - m) / sum : 0.0f;  // all of them at minus infinity: no weight
+        } else if (p.renorm) {
+            w = score / total;
+        }
         p.ids[t * p.top_k + place] = e;
-        p.weights[t * p.top_k + place] = (total == total ? w : total) * p.scale;
+        p.weights[t * p.top_k + place] = (total == total ? w : total) * p.scale;  // a NaN stays visible
     }
 }
 
 __global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs p) {
-    __shared__ float logit[256], by[256], chosen[MOE_MAX_K];
+    __shared__ Choice s;
     const int64_t t = blockIdx.x;
     const int e = threadIdx.x;
     if (e < p.E) {
         float part[16], l = 0.0f;
 #pragma unroll
-        for (int s = 0; s < 16; s++) part[s] = s < p.splits ? p.part[((int64_t)s * p.T + t) * p.E + e] : 0.0f;
+        for (int i = 0; i < 16; i++) part[i] = i < p.splits ? p.part[((int64_t)i * p.T + t) * p.E + e] : 0.0f;
 #pragma unroll
-        for (int s = 0; s < 16; s++) l += part[s];
-        logit[e] = l;
+        for (int i = 0; i < 16; i++) l += part[i];
+        s.logit[e] = l;
     }
     __syncthreads();
-    choose(p, t, logit, by, chosen);
+    choose(p, t, s);
 }
 
 // Small routers in one kernel: a block of 16 waves per token, each wave an expert at a time.
 __global__ __launch_bounds__(1024) void route_small_kernel(const RouteArgs p) {
-    __shared__ float logit[256], by[256], chosen[MOE_MAX_K];
+    __shared__ Choice s;
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint16_t* xr = p.x + t * p.ld_x;
@@ -192,10 +214,10 @@ __global__ __launch_bounds__(1024) void route_small_kernel(const RouteArgs p) {
         }
 #pragma unroll
         for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
-        if (lane == 0) logit[e] = acc;
+        if (lane == 0) s.logit[e] = acc;
     }
     __syncthreads();
-    choose(p, t, logit, by, chosen);
+    choose(p, t, s);
 }
 
 // Order of choice: NaN last, then by value; the lower index wins a tie.
@@ -282,12 +304,27 @@ __global__ __launch_bounds__(64) void route_select_kernel(const RouteArgs p) {
         }
         total += best_score;
     }
+    float w = mine;
+    if (p.renorm && total < kTinySum) {  // (the same in every lane)
+        float l = -INFINITY;
+        if (lane < p.top_k) {
+            l = 0.0f;
+            for (int s = 0; s < p.splits; s++) l += p.part[((int64_t)s * p.T + t) * p.E + my_id];
+        }
+        float m = l;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+        float all = m > -INFINITY ? expf(l - m) : 0.0f;  // all of them at minus infinity: no weight
+        w = all;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off, 64);
+        w = m > -INFINITY ? w / all : 0.0f;
+    } else if (p.renorm) {
+        w = mine / total;
+    }
     if (lane < p.top_k) {
-        // a sum that vanished (every chosen score underflowed) gives zeros, not 0 / 0
-        const float w = p.renorm ? mine / fmaxf(total, 1e-30f) : mine;
         p.ids[t * p.top_k + lane] = my_id;
-        // fmaxf drops a NaN: keep it visible
-        p.weights[t * p.top_k + lane] = (total == total ? w : total) * p.scale;
+        p.weights[t * p.top_k + lane] = (total == total ? w : total) * p.scale;  // a NaN stays visible
     }
 }
 

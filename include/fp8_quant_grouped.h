@@ -412,7 +412,9 @@ fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uint8_t* a, in
  *   choice      the top_k experts by scores + bias (bias fp32 [E], or null: by logits), in
  *               descending order; ties go to the lowest index, NaN goes last
  *   weights     the chosen scores (without the bias), divided by their sum if renormalize, times
- *               scale
+ *               scale; the quotients keep their precision where the scores leave fp32's range
+ *               below (sums under 2^-64 are formed from the logits), and are zeros where every
+ *               chosen logit is minus infinity
  *   ids int32 [T][top_k], weights fp32 [T][top_k]; workspace moe_route_workspace_size bytes, any
  *   content, 4-byte aligned; it may be null where that is 0 (small routers).
  * Limits (FP8Q_ERR_UNSUPPORTED): E <= 1024, top_k <= 32, H, ld_x and ld_r multiples of 8, x and
