@@ -61,6 +61,13 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
     return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
+// The same, but a finite value past bf16's largest gives that one, so that the rest is finite too.
+__device__ __forceinline__ uint16_t to_bf16_finite(float f) {
+    const uint32_t u = __float_as_uint(f);
+    const uint16_t r = to_bf16(f);
+    return (r & 0x7FFFu) == 0x7F80u && (u & 0x7FFFFFFFu) < 0x7F800000u ? (uint16_t)(r - 1) : r;
+}
+
 // ------------------------------------------------------------------------------------- routing
 
 struct RouteArgs {
@@ -576,7 +583,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_stream_kernel(const MoeArgs p)
                         const float u = acc[0][m][i], v = acc[1][m][i];
                         if (!DOWN) {
                             const float h = u / (1.0f + expf(-u)) * v;
-                            const uint16_t hi = to_bf16(h);
+                            const uint16_t hi = to_bf16_finite(h);
                             const float rest = h - __uint_as_float((uint32_t)hi << 16);
                             if (on0) {
                                 p.h[a * p.I + row0 + r] = hi;
