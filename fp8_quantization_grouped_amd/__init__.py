@@ -644,6 +644,12 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
 
 # ------------------------------------------------- a mixture-of-experts layer for a few tokens
 
+def _no_grad(what: str, *tensors) -> None:
+    """Refuses operands whose gradient the call would lose."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{what} has no gradient: detach its operands, or call it under torch.no_grad()")
+
+
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 _SCORING = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
@@ -659,8 +665,10 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
               weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The experts of each token: x bf16 [T, H], router bf16 [E, H], bias float32 [E] (added to the
     scores for the choice alone).  scoring: "softmax" or "sigmoid".  Returns (ids int32 [T, top_k],
-    weights float32 [T, top_k]) in descending order; ties go to the lowest index."""
+    weights float32 [T, top_k]) in descending order; ties go to the lowest index.  No gradient:
+    operands that require one are refused while torch records."""
     T, H, dev = _matrix(x, "x", _BF16)
+    _no_grad("moe_route", x, router, bias)
     E = router.shape[0]
     _rows_of(router, "router", _BF16, (E, H), dev)
     _want(scoring in _SCORING, "scoring must be softmax or sigmoid")
@@ -721,8 +729,10 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     """The experts' feed-forward of a few tokens (at most 128): x bf16 [T, H]; ids int32 and
     weights float32 [T, top_k] (moe_route's); w13 [E, 2I, H] and w2 [E, H, I] e4m3fn bytes with
     scales [E, ceil(2I/128), ceil(H/128)] and [E, ceil(H/128), ceil(I/128)]
-    (fp8_block_quant_weights').  Returns y bf16 [T, H].  An id outside [0, E) adds nothing."""
+    (fp8_block_quant_weights').  Returns y bf16 [T, H].  An id outside [0, E) adds nothing.  No
+    gradient: operands that require one are refused while torch records."""
     T, H, dev = _matrix(x, "x", _BF16)
+    _no_grad("fp8_moe_few_tokens", x, weights)
     _want(ids.dim() == 2, "ids must be a matrix")
     top_k = ids.shape[1]
     _rows_of(ids, "ids", _I32T, (T, top_k), dev)

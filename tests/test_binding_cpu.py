@@ -180,3 +180,30 @@ def test_a_contraction_of_length_zero_is_taken(calls):
                               zeros(2, dtype=torch.int32))
     args = calls[-1][1]
     assert args[2] % 16 == 0 and args[6] % 16 == 0 and args[7] % 16 == 0 and args[14:17] == (8, 5, 0)
+
+
+# ------------------------------------------------------------------------------- no lost gradients
+
+def test_operands_that_require_a_gradient_are_refused(calls):
+    """moe_route and the layer have no backward: a result cut from autograd is not given out silently."""
+    def operands(which):
+        x, ids, weights, *w = moe_args()
+        t = {"x": x, "router": zeros(3, 256, dtype=BF16), "bias": zeros(3), "weights": weights}
+        t[which].requires_grad_()
+        return t, ids, w
+
+    for which in ("x", "router", "bias"):
+        t, _, _ = operands(which)
+        route = lambda: fq.moe_route(t["x"], t["router"], 2, bias=t["bias"])
+        with pytest.raises(ValueError, match="gradient"):
+            route()
+        with torch.no_grad():
+            route()
+    for which in ("x", "weights"):
+        t, ids, w = operands(which)
+        layer = lambda: fq.fp8_moe_few_tokens(t["x"], ids, t["weights"], *w)
+        with pytest.raises(ValueError, match="gradient"):
+            layer()
+        with torch.inference_mode():
+            layer()
+    assert len(calls) == 5
