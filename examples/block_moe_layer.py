@@ -3,10 +3,10 @@ decoding, on the same quantized bytes.
 
     python examples/block_moe_layer.py [--tokens 4096 --hidden 2048 --inner 1408 --experts 64 --top 6]
 
-Training quantizes the expert weights once per step in both layouts, routes the tokens, runs the
-experts' two products and their gradients as grouped products, and leaves the routing's and the
-activation's gradients to torch.  Decoding routes a few tokens and runs the whole layer on the
-forward's weight bytes.
+Training quantizes the expert weights once per step in both layouts, routes the tokens, and runs the
+experts' two products and their gradients as grouped products; the activation's and the routing's
+gradients are torch operations on their results.  Decoding routes a few tokens and runs the whole
+layer on the forward's weight bytes.
 """
 from __future__ import annotations
 
@@ -67,9 +67,10 @@ class Layer:
         gu = self.w13.product(rows, offsets).float()
         gate, up = gu.chunk(2, 1)
         h, h_t = fq.fp8_block_quant_dual((torch.nn.functional.silu(gate) * up).to(torch.bfloat16))
-        o = self.w2.product(h, offsets).float()
+        o = self.w2.product(h, offsets)
         self.saved = token, offsets, share, rows_t, gate, up, h_t
-        return torch.zeros(x.shape, device=x.device).index_add_(0, token, o * share)
+        self.routed = x, ids, weights, order, o
+        return torch.zeros(x.shape, device=x.device).index_add_(0, token, o.float() * share)
 
     def backward(self, dy):
         """dy float32 [T, H] -> gradients of x [T, H] (through the experts), w13 and w2."""
@@ -83,6 +84,17 @@ class Layer:
         dx = self.w13.data_gradient(dgu, offsets).float()
         dw13 = weight_gradient(dgu_t, x_t, offsets)
         return torch.zeros(dy.shape, device=dy.device).index_add_(0, token, dx), dw13, dw2
+
+    def backward_routing(self, dy):
+        """dy float32 [T, H] -> gradients of x [T, H] (through the routing weights) and the router
+        [E, H], both float32.  The renormalized weights are a softmax of the chosen logits alone."""
+        x, ids, weights, order, o = self.routed
+        dw = torch.empty(order.shape, device=dy.device)
+        dw[order] = (dy[order // self.top] * o.float()).sum(1)
+        dw = dw.view(ids.shape)
+        chosen = weights * (dw - (weights * dw).sum(1, keepdim=True))
+        dlogits = torch.zeros(x.shape[0], self.router.shape[0], device=dy.device).scatter_(1, ids.long(), chosen)
+        return dlogits @ self.router.float(), dlogits.t() @ x.float()
 
     def decode(self, x):
         """x bf16 [T <= 128, H] -> y bf16 [T, H]."""
@@ -122,7 +134,8 @@ def main() -> None:
 
     def step():
         y = layer.forward(x)
-        return layer.backward(torch.ones_like(y))
+        dy = torch.ones_like(y)
+        return layer.backward(dy), layer.backward_routing(dy)
 
     print(f"training step, {a.tokens} tokens: {timed(step):.0f} us")
     print(f"decoding 8 tokens: {timed(lambda: layer.decode(few)):.0f} us")
