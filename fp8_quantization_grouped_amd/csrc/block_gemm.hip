@@ -20,7 +20,7 @@
 //   256 x 256, 2 stages, one block per CU: a wave's 128 x 64 results fill its registers, and with
 //     them the waves read 192 KB of LDS a step, the least that eight of them can.
 //   128 x 128, 2 stages, two blocks per CU; 128 x 64, 3 stages, and 64 x 64, 4 stages, one block per
-//     CU: for problems whose larger tiles would leave CUs without work (see pick_block_gemm).
+//     CU: for problems whose larger tiles would leave CUs without work (see pick_block_tile).
 //
 // Bound: delivery of the operands to the matrix cores, which are busy half of the time (48% by
 // counters); at 256 x 256 a step's matrix instructions take 2048 cycles of a SIMD, and the step 3700.
@@ -46,6 +46,7 @@
 #include "common.hpp"
 #include "gemm_tile.hpp"
 #include "lds_dma.hpp"
+#include "plan.hpp"
 
 namespace fp8q {
 
@@ -632,32 +633,15 @@ static fp8q_status_t launch_block_gemm(BlockGemmArgs p, hipStream_t stream) {
 }
 
 template <int MODE>
-static fp8q_status_t pick_block_gemm(const BlockGemmArgs& p, hipStream_t stream) {
-    // Where CUs would be left over, smaller tiles and loads further ahead, one block per CU (1 group, 7168
-    // long): 512 x 2048 in 64-tiles 24 us, in 128 x 64-tiles 27, in 128-tiles 42; 1024 x 2048 in 128 x
-    // 64-tiles 28 us, in 128-tiles 42, in 64-tiles, two for every CU, 34.  Every group but one ends inside
-    // a tile, on average half way.
-    const int64_t ends = (p.G - 1) / 2, cus = num_cus();
-    auto up = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
-    if (MODE == MODE_FWD) {
-        if ((up(p.M, 64) + ends) * up(p.N, 64) <= cus) return launch_block_gemm<MODE, 64, 64, 4>(p, stream);
-        if ((up(p.M, 128) + ends) * up(p.N, 64) <= cus) return launch_block_gemm<MODE_FWD, 128, 64, 3>(p, stream);
-    } else if (p.G * up(p.K, 64) * up(p.N, 64) <= cus) {
-        return launch_block_gemm<MODE, 64, 64, 4>(p, stream);
+static fp8q_status_t launch_picked(const BlockGemmArgs& p, hipStream_t stream) {
+    constexpr bool FWD = MODE == MODE_FWD;
+    switch (pick_block_tile(FWD, p.M, p.N, p.K, p.G, num_cus())) {
+        case TILE_64: return launch_block_gemm<MODE, 64, 64, 4>(p, stream);
+        case TILE_128X64: return launch_block_gemm<MODE_FWD, 128, 64, 3>(p, stream);
+        case TILE_128: return launch_block_gemm<MODE, 128, 128, 2>(p, stream);
+        case TILE_256: break;
     }
-    // 128-tiles where 256-tiles would not give every CU one: 2048 x 2048 x 2048 in one group 26 against
-    // 40 us, 4096 x 2048 x 2048 34 against 43 us; with a tile for each, 256 is faster: 4096 x 4096 x
-    // 2048 47 against 53 us, weight gradient of 8 groups of 1024 x 2048 28 against 31 us
-    const int64_t rows = MODE == MODE_FWD ? p.M : (int64_t)p.G * p.K;
-    const int64_t tiles = (rows + 255) / 256 * ((p.N + 255) / 256);
-    // Forward tiles are of one length, so a launch takes whole rounds of them: a round of 512 128-tiles
-    // takes 0.65 as long as one of 256 256-tiles, and few rounds of cut tiles can come out shorter (16384
-    // rows in 64 groups, 1408 x 2048: 76 against 92 us; 4096 rows in 8 groups, 4096 x 4096: 91 against
-    // 110).  Past three rounds the larger tile's fewer loads count (49152 rows in 64 groups: 235 against
-    // 207 us, though the rounds are even).
-    const int64_t r256 = up((up(p.M, 256) + ends) * up(p.N, 256), cus), r128 = up((up(p.M, 128) + ends) * up(p.N, 128), 2 * cus);
-    const bool small = tiles < 256 || (MODE == MODE_FWD && r256 <= 3 && 65 * r128 < 100 * r256);
-    return small ? launch_block_gemm<MODE, 128, 128, 2>(p, stream) : launch_block_gemm<MODE, 256, 256, 2>(p, stream);
+    return launch_block_gemm<MODE, 256, 256, 2>(p, stream);
 }
 
 }  // namespace fp8q
@@ -702,5 +686,5 @@ extern "C" fp8q_status_t fp8_block_grouped_gemm(fp8q_gemm_mode_t mode, const uin
     // 32 experts 862 -> 839 us)
     p.stream_out = (double)(fwd ? M : groups * K) * N * esz > kStreamBytes;
     p.vec_store = N % 8 == 0 && ldc % 8 == 0 && fp8q_aligned(c, 16);
-    return fwd ? pick_block_gemm<MODE_FWD>(p, stream) : pick_block_gemm<MODE_WGRAD>(p, stream);
+    return fwd ? launch_picked<MODE_FWD>(p, stream) : launch_picked<MODE_WGRAD>(p, stream);
 }

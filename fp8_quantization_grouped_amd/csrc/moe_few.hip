@@ -30,7 +30,9 @@
 // waves a CU with twice the registers (242 to 265 us), non-temporal weight loads, a second pass over
 // the weights for more than 32 tokens (65 us), h in one bf16 (its rounding shows in the result).
 #include "common.hpp"
+#include "gemm_tile.hpp"
 #include "lds_dma.hpp"
+#include "plan.hpp"
 
 namespace fp8q {
 
@@ -378,8 +380,6 @@ __device__ __forceinline__ int choices_of(const int32_t* __restrict__ ids, int n
     return count;
 }
 
-constexpr int moe_lds(int nw) { return 8192 * nw; }  // staged activations of a block: 16 waves share a CU
-
 // One expert's product with its chosen tokens.  DOWN = false: h[a] = silu(G x) * (U x), a wave's two
 // weight tiles being 16 gate rows and the same 16 up rows; DOWN = true: o[a] = W2 h[a], two
 // neighbouring tiles of 16 rows.  A block's NW waves are NW / S such pairs times S parts of the
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_stream_kernel(const MoeArgs p)
         int lr = 0;
         while ((1 << lr) < toks) lr++;
         // contraction blocks of each part in a chunk, of which two are held: a power of two, and
-        // launch_stream sees to it that one fits
+        // pick_stream sees to it that one fits
         int lc = 0;
         while ((LDS / 2 >> (lc + 1 + lr + 8)) >= PL * S && (1 << lc) < most) lc++;
 
@@ -630,66 +630,33 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const MoeArgs p) {
 }
 
 template <int MT, bool DOWN>
-static void launch_stream(MoeArgs p, hipStream_t stream) {
-    const int n = p.T * p.top_k;
-    const int64_t experts = n < p.E ? n : p.E;
-    p.pass = 1;
-    while (p.pass < p.T && p.pass < 16 * MT) p.pass *= 2;
-    const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
-    // Parts of the contraction: two unless there are waves for the chip twice over (4096 run at a time),
-    // four below half of it, each with 4 blocks or more, or 2 where most of the chip is idle (layers of 32 experts of 2048 x 7168, 8 of them a
-    // token: 1 token 78 us in four parts, 79 in two, 88 in one; 5 tokens 231, 230 and 252; 24 tokens of 64
-    // experts of 1408 x 2048 120 us in two, 129 in one).  In passes of 64 tokens one part stages them best
-    // (64 tokens 315 us, in two parts 326).  One block of every part has to fit half the staging buffer
-    // (2^8 bytes a row and plane).
-    constexpr int NW = MT == 1 ? 4 : 8, PL = DOWN ? 2 : 1, SMAX = MT == 1 ? 4 : MT == 2 ? 4 / PL : 1;
-    static_assert(moe_lds(NW) / 2 >= SMAX * PL * (MT == 1 ? 1 : 16 * MT) * 256, "a block of every part fits");
-    int S = 1;
-    while (2 * S <= SMAX && 2 * S * PL * p.pass * 256 <= moe_lds(NW) / 2 && experts * pairs * S < (S == 1 ? 8192 : 4096) && kbs >= (experts * pairs * S < 2048 ? 3 : 8) * S) S *= 2;
-    const dim3 grid((unsigned)((pairs * S + NW - 1) / NW), (unsigned)(p.by_choice ? n : p.E)), block(64 * NW);
-    if (S == 1) moe_stream_kernel<MT, 1, DOWN, NW><<<grid, block, 0, stream>>>(p);
-    else if (S == 2) moe_stream_kernel<MT, SMAX < 2 ? 1 : 2, DOWN, NW><<<grid, block, 0, stream>>>(p);
+static void launch_stream(MoeArgs p, const StreamPlan& plan, hipStream_t stream) {
+    constexpr int NW = moe_waves(MT), SMAX = moe_parts(MT, DOWN);
+    static_assert(moe_lds(NW) / 2 >= SMAX * (DOWN ? 2 : 1) * (MT == 1 ? 1 : 16 * MT) * 256, "a block of every part fits");
+    p.pass = plan.pass;
+    const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16;
+    const dim3 grid((unsigned)((pairs * plan.parts + NW - 1) / NW), (unsigned)(p.by_choice ? p.T * p.top_k : p.E)), block(64 * NW);
+    if (plan.parts == 1) moe_stream_kernel<MT, 1, DOWN, NW><<<grid, block, 0, stream>>>(p);
+    else if (plan.parts == 2) moe_stream_kernel<MT, SMAX < 2 ? 1 : 2, DOWN, NW><<<grid, block, 0, stream>>>(p);
     else moe_stream_kernel<MT, SMAX, DOWN, NW><<<grid, block, 0, stream>>>(p);
 }
 
-// The tokens of an expert that one pass takes: as many as may come, since a second pass reads the
-// weights again (65 us for 64 tokens of 32 experts of 2048 x 7168 in passes of 32).  Where the waves
-// leave half of the chip idle, the chain of one wave's blocks counts instead, and passes of 32 leave
-// room for two parts of it: 34 tokens of 4 experts of 4096 x 1024, 2 a token, 78 -> 52 us, 128 tokens
-// 165 -> 125; 64 tokens of 4 experts of 816 x 1920, all four of them, 63 -> 52 us.  Passes of 16 were
-// slower than those of 32 from 17 tokens on (1024 x 4096, 28 tokens: 52 against 45 us).
 template <bool DOWN>
-static void pick_stream(const MoeArgs& p, hipStream_t stream) {
-    const int n = p.T * p.top_k;
-    const int64_t experts = n < p.E ? n : p.E;
-    const int pairs = DOWN ? (p.H + 31) / 32 : p.I / 16, kbs = ((DOWN ? p.I : p.H) + MB - 1) / MB;
-    const bool idle = experts * pairs < 2048 && kbs >= 3;
-    if (p.T <= 16) launch_stream<1, DOWN>(p, stream);
-    else if (p.T <= 32 || idle) launch_stream<2, DOWN>(p, stream);
-    else launch_stream<4, DOWN>(p, stream);
+static void launch_product(const MoeArgs& p, hipStream_t stream) {
+    const StreamPlan plan = pick_stream(DOWN, p.T, p.top_k, p.E, p.H, p.I, num_cus());
+    if (plan.mt == 1) launch_stream<1, DOWN>(p, plan, stream);
+    else if (plan.mt == 2) launch_stream<2, DOWN>(p, plan, stream);
+    else launch_stream<4, DOWN>(p, plan, stream);
 }
 
 static fp8q_status_t launch_moe(const MoeArgs& p, hipStream_t stream) {
-    pick_stream<false>(p, stream);
+    launch_product<false>(p, stream);
     FP8Q_CHECK_LAUNCH();
-    pick_stream<true>(p, stream);
+    launch_product<true>(p, stream);
     FP8Q_CHECK_LAUNCH();
     moe_join_kernel<<<dim3((unsigned)(((int64_t)p.T * p.H / 4 + 255) / 256)), dim3(256), 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
-}
-
-// One block takes a token's whole router: 4 x 256 in 3.4 us against 5.5 us in two launches, but 64 x
-// 2048 in 15 us against 10 us.
-static bool route_is_small(int64_t H, int64_t E) { return E <= 256 && E * H <= (1 << 14); }
-
-static int route_splits(int64_t T, int64_t H, int64_t E) {
-    // enough blocks for the chip's CUs, at least 8 instructions' worth of H for each of a block's waves
-    const int64_t blocks = ((T + 15) / 16) * ((E + 15) / 16);
-    int64_t s = 128 / blocks;
-    const int64_t most = H / (4 * 8 * 32);
-    s = s < most ? s : most;
-    return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
 
 }  // namespace fp8q

@@ -1,0 +1,40 @@
+"""The launch rules of the block-scaled kernels, without a GPU."""
+from __future__ import annotations
+
+import random
+
+import pytest
+
+from tests import planlib
+
+
+def test_the_rules_count_the_chips_compute_units():
+    """The same products on chips of other sizes: a 256-tile for every compute unit there is."""
+    for cus in (64, 128, 256, 304):
+        assert planlib.tile(True, 16 * 256, cus // 16 * 256, 512, 1, cus) == "256x256"  # one each
+        assert planlib.tile(True, 15 * 256, cus // 16 * 256, 512, 1, cus) == "128x128"
+        assert planlib.tile(False, 4096, cus // 16 * 256, 512, 8, cus) == "256x256"     # 8 x 2 row tiles
+        assert planlib.tile(False, 4096, cus // 16 * 256 - 256, 512, 8, cus) == "128x128"
+        # the layer: 33 tokens take passes of 64 where the waves fill half of the chip, else of 32
+        assert planlib.stream(False, 33, 1, 1, 512, 16 * 8 * cus, cus)[:2] == (4, 64)
+        assert planlib.stream(False, 33, 1, 1, 512, 16 * (8 * cus - 1), cus)[:2] == (2, 32)
+
+
+@pytest.mark.parametrize("fwd", [True, False])
+def test_small_products_take_small_tiles(fwd):
+    assert planlib.tile(fwd, 1, 1, 16, 1) == "64x64"
+    assert planlib.tile(fwd, 1 << 20, 1 << 14, 1 << 14, 2048) == "256x256"
+
+
+def test_a_plans_parts_fit_the_staging_buffer():
+    rng = random.Random(1)
+    for _ in range(20000):
+        T, E, k = rng.randint(1, 128), rng.randint(1, 1024), rng.randint(1, 32)
+        H, I = 16 * int(2 ** rng.uniform(0, 12)), 16 * int(2 ** rng.uniform(0, 12))
+        for down in (False, True):
+            mt, tokens, parts = planlib.stream(down, T, k, E, H, I)
+            assert mt in (1, 2, 4) and parts in (1, 2, 4) and tokens & (tokens - 1) == 0
+            assert tokens <= 16 * mt and (tokens >= T or tokens == 16 * mt)
+            assert parts * (2 if down else 1) * tokens * 256 <= 8192 * (4 if mt == 1 else 8) // 2
+            assert parts <= (4 if mt == 1 else (2 if down else 4) if mt == 2 else 1)  # what is compiled
+            assert parts <= max(1, -(-(I if down else H) // 128))
