@@ -5,7 +5,7 @@ import random
 
 import pytest
 
-from tests import planlib
+from tests import block_cases, planlib
 
 
 def test_the_rules_count_the_chips_compute_units():
@@ -38,3 +38,35 @@ def test_a_plans_parts_fit_the_staging_buffer():
             assert parts * (2 if down else 1) * tokens * 256 <= 8192 * (4 if mt == 1 else 8) // 2
             assert parts <= (4 if mt == 1 else (2 if down else 4) if mt == 2 else 1)  # what is compiled
             assert parts <= max(1, -(-(I if down else H) // 128))
+
+
+def _cases(table):
+    return [(tile, case) for tile, cases in table.items() for case in cases]
+
+
+@pytest.mark.parametrize("tile,case", _cases(block_cases.FORWARD))
+def test_forward_cases_take_their_tile(tile, case):
+    M, N, K, G, _ = case
+    assert planlib.tile(True, M, N, K, G) == tile
+
+
+@pytest.mark.parametrize("tile,case", _cases(block_cases.DATA_GRADIENT))
+def test_data_gradient_cases_take_their_tile(tile, case):
+    M, N, K, G, _ = case
+    assert planlib.tile(True, M, K, N, G) == tile  # the same product with N and K exchanged
+
+
+@pytest.mark.parametrize("tile,case", _cases(block_cases.WEIGHT_GRADIENT))
+def test_weight_gradient_cases_take_their_tile(tile, case):
+    M, N, K, G, _ = case
+    assert planlib.tile(False, M, N, K, G) == tile
+
+
+def test_every_tile_has_cases():
+    """Several groups, empty ones, columns that allow wide stores and columns that do not."""
+    for table, tiles in ((block_cases.FORWARD, planlib.TILES), (block_cases.WEIGHT_GRADIENT, ["64x64", "128x128", "256x256"])):
+        assert sorted(table) == sorted(tiles)
+        for tile in tiles:
+            assert any(c[3] > 1 for c in table[tile])
+            assert any(c[1] % 8 == 0 for c in table[tile]) and any(c[1] % 8 for c in table[tile])
+        assert {c[4] for c in table["256x256"]} >= {"cuts", "empties"}
