@@ -21,3 +21,18 @@ WEIGHT_GRADIENT = {
     "128x128": [(900, 704, 1032, 3, "cuts"), (900, 701, 1030, 3, "cuts")],
     "256x256": [(700, 1504, 1304, 9, "cuts"), (1100, 2048, 2056, 4, "empties"), (400, 1530, 1290, 12, "empties")],
 }
+
+# The layer: T, top_k, experts of the call, hidden, inner, and the experts that tokens may choose
+# (the launch goes by the sizes alone).  Then (token tiles, tokens of a pass, parts) of the gate and up
+# product and of the down product.
+LAYERS = {
+    # 33 blocks of the contraction and more than 64: a part's factors are read twice (four parts)
+    "long contraction": ((3, 2, 2, 33280, 16, 2), (1, 4, 4), (1, 4, 1)),
+    "long inner": ((2, 1, 3, 16, 33280, 3), (1, 2, 1), (1, 2, 4)),
+    # two parts over passes of 32 tokens, three passes, chunks in turn
+    "passes of 32": ((70, 1, 4, 1040, 528, 4), (2, 32, 4), (2, 32, 2)),
+    # passes of 64 over 5 blocks and over 66, down over 4: chunks of two blocks and of one, in turn
+    "passes of 64": ((40, 8, 8, 640, 4096, 8), (4, 64, 1), (2, 32, 2)),
+    "passes of 64, long": ((40, 2, 64, 8336, 512, 3), (4, 64, 1), (4, 64, 1)),
+    "two passes of 64": ((128, 1, 16, 2064, 2048, 2), (4, 64, 1), (2, 32, 2)),
+}

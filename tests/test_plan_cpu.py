@@ -70,3 +70,27 @@ def test_every_tile_has_cases():
             assert any(c[3] > 1 for c in table[tile])
             assert any(c[1] % 8 == 0 for c in table[tile]) and any(c[1] % 8 for c in table[tile])
         assert {c[4] for c in table["256x256"]} >= {"cuts", "empties"}
+
+
+@pytest.mark.parametrize("name", list(block_cases.LAYERS))
+def test_layer_cases_take_their_plans(name):
+    (T, k, E, H, I, _), gate_up, down = block_cases.LAYERS[name]
+    assert planlib.stream(False, T, k, E, H, I) == gate_up
+    assert planlib.stream(True, T, k, E, H, I) == down
+
+
+def test_the_layers_paths_have_cases():
+    """Each size of a pass with more blocks of the contraction than are staged at once, and more blocks of a
+    part than a wave holds factors of (64), in both products."""
+    seen = set()
+    for (T, k, E, H, I, _), *plans in block_cases.LAYERS.values():
+        for down, (mt, tokens, parts) in enumerate(plans):
+            blocks = -(-(-(-(I if down else H) // 128)) // parts)
+            rows = parts * (2 if down else 1) * tokens * 256  # bytes that one block of every part takes
+            chunk = 1
+            while 2 * chunk * rows <= 8192 * (4 if mt == 1 else 8) // 2 and chunk < blocks:
+                chunk *= 2
+            seen.add((down, mt, "turns") if blocks > 2 * chunk else None)
+            seen.add((down, "factors") if blocks > 64 else None)
+            seen.add((down, mt, "passes") if T > tokens else None)
+    assert seen >= {(d, mt, "turns") for d in (0, 1) for mt in (1, 2, 4)} | {(0, "factors"), (1, "factors"), (0, 4, "passes"), (0, 2, "passes")}
