@@ -212,8 +212,11 @@ __global__ __launch_bounds__(256) void block_quant_kernel(const BlockQuantArgs p
 
 template <int LAY>
 static fp8q_status_t launch_block_quant(BlockQuantArgs& p, int64_t mats, hipStream_t stream) {
+    // a launch takes fewer than 2^32 threads along x
+    constexpr int64_t most = (1LL << 32) / 256 - 1;
+    if (p.rows > most * QB || p.cols > most * QB || mats > 65535) return FP8Q_ERR_UNSUPPORTED;
     const int64_t tr = (p.rows + QB - 1) / QB, tc = (p.cols + QB - 1) / QB;
-    if (tr * tc > 0x7FFFFFFFLL || mats > 65535) return FP8Q_ERR_UNSUPPORTED;
+    if (tr * tc > most) return FP8Q_ERR_UNSUPPORTED;
     p.tiles_c = (int)tc;
     p.vec_x = p.cols % 8 == 0 && p.ld_x % 8 == 0 && fp8q_aligned(p.x, 16);
     p.vec_q = p.cols % 8 == 0 && p.ld_q % 8 == 0 && fp8q_aligned(p.q, 8) ? 8 : 1;

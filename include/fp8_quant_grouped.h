@@ -332,7 +332,8 @@ fp8q_status_t fp8_mx_grouped_gemm_wgrad(const uint8_t* a, int64_t lda, const uin
  * the STORED factor is d, the one that dequantization multiplies by (x ~ dec(q) * d): the products
  * below use a factor per contraction block inside their sums, where a division has no place.
  * Blocks are counted from index 0 of their matrix; the last one of a row, column or matrix may be
- * shorter.
+ * shorter.  The quantizers take matrices of fewer than 2^24 tiles of 128 x 128, cut ones counted
+ * (FP8Q_ERR_UNSUPPORTED beyond).
  *
  * fp8_block_quant_rowwise: blocks of 1 x 128 along each row (activations of the forward, output
  * gradients of the data gradient).

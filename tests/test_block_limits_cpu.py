@@ -44,3 +44,11 @@ def test_layer_strides_of_any_size_are_refused(power):
     size = fq.lib().fp8_moe_few_tokens_workspace_size(T, H, I, k)
     good = [P, T, H, H, P, P, k, P, H, 2 * I * H, P, 2, 1, 4, P, I, H * I, P, 1, 1, 2, E, I, P, H, P, size, None]
     refuse("fp8_moe_few_tokens", good, [({3: big}, UNSUPPORTED), ({8: big}, UNSUPPORTED), ({15: big}, UNSUPPORTED), ({1: 128, 3: big}, UNSUPPORTED)])
+
+
+@pytest.mark.parametrize("rows,cols", [(1 << 31, 1), (1, 1 << 31), (1 << 24, 129 * 128), (1 << 62, 1), ((1 << 63) - 1, 1), (1 << 40, 1 << 40)])
+def test_quantizers_of_more_tiles_than_a_launch_takes(rows, cols):
+    big = (1 << 63) - 1
+    refuse("fp8_block_quant_rowwise", [P, rows, cols, big, P, big, P, big, None], [({}, UNSUPPORTED)])
+    refuse("fp8_block_quant_dual", [P, rows, cols, big, P, big, P, big, P, big, P, big, None], [({}, UNSUPPORTED)])
+    refuse("fp8_block_quant_weights", [P, 1, rows, cols, big, P, big, P, big, P, None], [({}, UNSUPPORTED)])
