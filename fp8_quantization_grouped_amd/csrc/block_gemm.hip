@@ -22,14 +22,14 @@
 //   128 x 128, 2 stages, two blocks per CU; 128 x 64, 3 stages, and 64 x 64, 4 stages, one block per
 //     CU: for problems whose larger tiles would leave CUs without work (see pick_block_tile).
 //
-// Bound: delivery of the operands to the matrix cores, which are busy half of the time (48% by
+// Bound: delivery of the operands to the matrix cores, which are busy half of the time (49% by
 // counters); at 256 x 256 a step's matrix instructions take 2048 cycles of a SIMD, and the step 3700.
-// Measured: 8192 x 14336 x 4096 in one group 430 us, 2.2 PFLOP/s (20 us less with the loads taken away
+// Measured: 8192 x 14336 x 4096 in one group 423 us, 2.3 PFLOP/s (20 us less with the loads taken away
 // after the first step, half without the reads of A's fragments, 6% less without the factors); 49152
-// rows in 64 groups, 1408 x 2048, 202 us (1.4 PFLOP/s of the products asked for: groups and columns
-// that end inside a tile add a third); data gradient of 16384 rows in 32 groups, 2048 x 7168, 325 us,
-// their weight gradient 497 us, of which 40 are stores, 56 the columns' factors and a quarter of the
-// rest the groups' ends inside blocks.  Small: 512 x 2048 x 7168 24 us, a chain of 56 steps of 0.35 us.
+// rows in 64 groups, 1408 x 2048, 209 us (1.4 PFLOP/s of the products asked for: groups and columns
+// that end inside a tile add a third); data gradient of 16384 rows in 32 groups, 2048 x 7168, 326 us,
+// their weight gradient 498 us, of which 40 are stores, 56 the columns' factors and a quarter of the
+// rest the groups' ends inside blocks.  Small: 512 x 2048 x 7168 26 us, a chain of 56 steps of 0.4 us.
 //
 // Measured and not kept: 16 waves per block, fragments of A read two rows ahead, wave priorities, the
 // loads issued later in a step and B two steps ahead of the arithmetic (all within 1%); leaving out

@@ -23,6 +23,8 @@ __device__ __forceinline__ i32x4_t make_rsrc4(const void* base, uint32_t bytes) 
 // its address from there, and five between a vector instruction that wrote one of the descriptor's or
 // the offset's scalar registers (a lane read that fills a descriptor or brings a spilled one back)
 // and the load that reads it.  s_mov is one state and s_nop 3 four; the build checks every block.
+// Against one state alone: block-scaled 8192 x 14336 x 4096 431 and 423 us, backward of 32 experts of
+// 2048 x 7168 807 and 802, others within 1%.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t voff, uint32_t lds_base) {

@@ -19,10 +19,10 @@
 // Every sum has a fixed order: a contraction's parts are added in wave order, a token's experts in
 // the order of its choices.
 //
-// Measured (32 experts of 2048 x 7168, 8 of them a token): 1 token's gate and up products 46 us (5.1
-// TB/s of weights) and down product 26 us (4.5 TB/s), 64 tokens' 193 and 117 us (4.9 and 4.0 TB/s),
+// Measured (32 experts of 2048 x 7168, 8 of them a token): 1 token's gate and up products 47 us (4.9
+// TB/s of weights) and down product 27 us (4.4 TB/s), 64 tokens' 198 and 117 us (4.8 and 4.0 TB/s),
 // where a copy of large buffers reaches 4.9 TB/s and a kernel that only reads as these do 5.4 at 240
-// MB and 6.2 at 960 MB.  64 experts of 1408 x 2048, 6 of them, 5 tokens: 37 and 19 us (3.8 TB/s: each
+// MB and 6.2 at 960 MB.  64 experts of 1408 x 2048, 6 of them, 5 tokens: 37 and 20 us (3.8 TB/s: each
 // wave has 16 and 11 blocks to stream, so starting and ending count).  Routing and the join take 2
 // to 6 us each, a launch's time.
 //

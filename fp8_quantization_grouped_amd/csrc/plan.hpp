@@ -1,5 +1,6 @@
 // Which variant of the block-scaled kernels a call takes: rules on sizes and the chip's CUs alone, in
-// plain C++ so that they can be checked without a GPU.  Times are of an MI355X (256 CUs).
+// plain C++ so that they can be checked without a GPU.  Times are of an MI355X (256 CUs), those of one
+// comparison taken together.
 #pragma once
 
 #include <stdint.h>
