@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -29,7 +30,7 @@ _lib = None
 
 # name -> (restype, argtypes)
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-_I = ctypes.c_int
+_I, _F = ctypes.c_int, ctypes.c_float
 SIGNATURES = {
     "fp8q_abi_version": (_I, []),
     "fp8q_status_string": (ctypes.c_char_p, [_I]),
@@ -70,6 +71,11 @@ SIGNATURES = {
     "fp8_moe_few_tokens": (_I, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _I64, _I64, _P, _I64, _I64,
                                 _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64,
                                 _P, _SZ, _P]),
+    "fp8_rms_norm": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I, _F, _P, _I64, _P, _I64, _I, _I, _P,
+                          _I64, _P, _I64, _P, _P]),
+    "fp8_rms_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "fp8_rms_norm_backward": (_I, [_P, _I64, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _P, _I, _P, _I64,
+                                   _P, _P, _SZ, _P]),
 }
 
 
@@ -398,6 +404,7 @@ def fp8_mx_grouped_gemm_wgrad(a: torch.Tensor, a_e8m0: torch.Tensor, b: torch.Te
 
 BLOCK = 128
 _BYTES = (torch.uint8, torch.float8_e4m3fn)  # how e4m3fn bytes may be held
+_FP8_BYTES = {E4M3FN: _BYTES, E4M3FNUZ: (torch.uint8, torch.float8_e4m3fnuz)}
 
 
 def _want(ok: bool, what: str) -> None:
@@ -756,3 +763,131 @@ def fp8_moe_few_tokens(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
           weights.data_ptr(), top_k, *args13, *args2, E, I, y.data_ptr(), _ld(y, T, H),
           ws, need)
     return y
+
+
+# ------------------------------------------------- norm with the residual's addition and 8-bit rows
+
+NORM_NONE, NORM_ROW, NORM_BLOCK = 0, 1, 2
+_NORM_SCALING = {None: NORM_NONE, "row": NORM_ROW, "block": NORM_BLOCK}
+_WIDE = (torch.bfloat16, torch.float32)
+
+
+class Normed(NamedTuple):
+    """What fp8_rms_norm returns; None where an output was not asked for."""
+    h: torch.Tensor
+    y: torch.Tensor | None
+    q: torch.Tensor | None
+    scales: torch.Tensor | None
+    rstd: torch.Tensor
+
+
+def _no_record(what: str, backward: str, *tensors) -> None:
+    """Refuses operands whose gradient torch would record: it is another call's."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{what} is not recorded, its gradient is {backward}: detach its operands, or call "
+                         "it under torch.no_grad()")
+
+
+def fp8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 residual: torch.Tensor | None = None, scaling: str | None = "block", fmt: int = E4M3FN,
+                 bf16: bool = False, h: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                 q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                 rstd: torch.Tensor | None = None) -> Normed:
+    """Norm of h = x + residual over each row: x, residual bf16 [rows, cols], weight bf16 or float32
+    [cols].  scaling: "block" (q and scales as fp8_block_quant_rowwise gives them), "row" (as
+    fp8_quant_rowwise does, in fmt) or None (no 8 bits).  bf16: the rows y in bfloat16 too (always
+    without 8 bits).  Returns (h, y, q, scales, rstd): h bf16 is x itself without a residual, and may be
+    given as x or residual to replace it; rstd float32 [rows] is what fp8_rms_norm_backward takes.
+    Operands that require a gradient are refused while torch records."""
+    rows, cols, dev = _matrix(x, "x", _BF16)
+    _no_record("fp8_rms_norm", "fp8_rms_norm_backward", x, weight, residual)
+    _rows_of(weight, "weight", _WIDE, (cols,), dev)
+    _want(scaling in _NORM_SCALING, "scaling must be block, row or None")
+    _want(eps > 0, "eps must be positive")
+    shape = (rows, cols)
+    res_args = (None, 0, weight.data_ptr(), _OUT[weight.dtype], eps, None, 0)
+    if residual is not None:
+        _rows_of(residual, "residual", _BF16, shape, dev)
+        if h is None:
+            h = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+        else:
+            _rows_of(h, "h", _BF16, shape, dev)
+        res_args = (residual.data_ptr(), _ld(residual, rows, cols), weight.data_ptr(), _OUT[weight.dtype], eps,
+                    h.data_ptr(), _ld(h, rows, cols))
+    else:
+        _want(h is None, "h is x without a residual")
+        h = x
+    y_args = (None, 0)
+    if y is not None:
+        _rows_of(y, "y", _BF16, shape, dev)
+    elif bf16 or scaling is None:
+        y = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+    if y is not None:
+        y_args = (y.data_ptr(), _ld(y, rows, cols))
+    q_args = (None, 0, None, 0)
+    if scaling is None:
+        _want(q is None and scales is None, "scaling=None takes no q and scales")
+    else:
+        _want(fmt in FMAX, "unknown format")
+        if scaling == "block":
+            _want(fmt == E4M3FN, "blocks are of e4m3fn")
+            s_shape = (_blocks(cols), rows)
+        else:
+            s_shape = (rows,)
+        if q is None:
+            q = _padded_bytes(rows, cols, dev)
+        else:
+            _rows_of(q, "q", _FP8_BYTES[fmt], shape, dev)
+        if scales is None:
+            scales = torch.empty(s_shape, dtype=torch.float32, device=dev)
+        else:
+            _rows_of(scales, "scales", _F32, s_shape, dev)
+        q_args = (q.data_ptr(), _ld(q, rows, cols), scales.data_ptr(),
+                  _ld(scales, s_shape[0], rows) if scaling == "block" else rows)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _rows_of(rstd, "rstd", _F32, (rows,), dev)
+    _call("fp8_rms_norm", dev, x.data_ptr(), rows, cols, _ld(x, rows, cols), *res_args, *y_args,
+          _NORM_SCALING[scaling], fmt, *q_args, rstd.data_ptr())
+    return Normed(h, y, q, scales, rstd)
+
+
+def fp8_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().fp8_rms_norm_backward_workspace_size(rows, cols))
+
+
+def fp8_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                          dh: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                          dweight: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Gradients of fp8_rms_norm from dy, the gradient of its y (the 8-bit rounding taken as the
+    identity), and dh, the one that reaches h from elsewhere: both bf16 or both float32 [rows, cols].
+    h, rstd: what the forward returned.  Returns (dx [rows, cols] like dy, the gradient of x and of the
+    residual alike, dweight float32 [cols]).  dx may be given as dy or dh to replace it."""
+    rows, cols, dev = _matrix(dy, "dy", _WIDE)
+    shape = (rows, cols)
+    _rows_of(h, "h", _BF16, shape, dev)
+    _rows_of(rstd, "rstd", _F32, (rows,), dev)
+    _rows_of(weight, "weight", _WIDE, (cols,), dev)
+    dh_args = (None, 0)
+    if dh is not None:
+        _rows_of(dh, "dh", (dy.dtype,), shape, dev)
+        dh_args = (dh.data_ptr(), _ld(dh, rows, cols))
+    if dx is None:
+        dx = torch.empty(rows, cols, dtype=dy.dtype, device=dev)
+    else:
+        _rows_of(dx, "dx", (dy.dtype,), shape, dev)
+    if dweight is None:
+        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+    else:
+        _rows_of(dweight, "dweight", _F32, (cols,), dev)
+    if workspace is None:
+        need = lib().fp8_rms_norm_backward_workspace_size(rows, cols)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    else:
+        ws, need = _workspace(workspace, dev)
+    _call("fp8_rms_norm_backward", dev, dy.data_ptr(), _ld(dy, rows, cols), *dh_args, _OUT[dy.dtype],
+          h.data_ptr(), rows, cols, _ld(h, rows, cols), rstd.data_ptr(), weight.data_ptr(),
+          _OUT[weight.dtype], dx.data_ptr(), _ld(dx, rows, cols), dweight.data_ptr(), ws, need)
+    return dx, dweight

@@ -454,6 +454,49 @@ fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_t H, int64_
                                  uint16_t* y, int64_t ld_y, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Root-mean-square norm before a layer, with the residual's addition and 8-bit rows for the products.
+ *   h    = RN_bf16(x + residual), or x where residual is null          (the residual stream)
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps)                      (fp32; sums in fp32)
+ *   y    = h * rstd * weight                                             (fp32)
+ * and of y, each in one rounding from its 32 bits:
+ *   y     bf16 [rows][ld_y], or null
+ *   scaling FP8Q_NORM_ROW: q u8 [rows][ld_q] and scales fp32 [rows] as fp8_quant_rowwise keeps them
+ *           (one multiplier s = FMAX / max(absmax, 1e-12f) a row, either fmt; ld_s is ignored)
+ *   scaling FP8Q_NORM_BLOCK: q and scales [ceil(cols/128)][ld_s >= rows] as fp8_block_quant_rowwise
+ *           keeps them (the factor d = 1 / s of each block of 1 x 128; e4m3fn only)
+ *   scaling FP8Q_NORM_NONE: q and scales are null, y is not
+ * x, residual bf16 [rows][ld >= cols]; weight [cols] of weight_dtype; eps > 0.
+ *   h     bf16 [rows][ld_h], required with a residual, may be x or residual itself (the same pointer
+ *         and leading dimension); null without one.  No other output may overlap an input.
+ *   rstd  fp32 [rows] for the backward, or null
+ * Rows of any finite h: where the squares' sum leaves fp32's range it is formed of h * 2^-80.
+ * Any sizes and alignments; cols and leading dimensions that are multiples of 8 with x, residual, h,
+ * y and weight 16-byte and q 8-byte aligned take the wide accesses.  rows < 2^31
+ * (FP8Q_ERR_UNSUPPORTED beyond).  rows == 0 or cols == 0 is a no-op. */
+typedef enum { FP8Q_NORM_NONE = 0, FP8Q_NORM_ROW = 1, FP8Q_NORM_BLOCK = 2 } fp8q_norm_scaling_t;
+fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x,
+                           const uint16_t* residual, int64_t ld_res, const void* weight,
+                           fp8q_out_t weight_dtype, float eps, uint16_t* h, int64_t ld_h, uint16_t* y,
+                           int64_t ld_y, fp8q_norm_scaling_t scaling, fp8q_format_t fmt, uint8_t* q,
+                           int64_t ld_q, float* scales, int64_t ld_s, float* rstd, hipStream_t stream);
+
+/* Its gradients, the 8-bit rounding taken as the identity: with xh = h * rstd and g = dy * weight
+ *   dx      = rstd * (g - xh * mean over the row of g * xh) + dh
+ *   dweight = sum over rows of dy * xh                                   (fp32 [cols])
+ * dx is the gradient of x and of the residual alike; dh is the gradient that reaches the residual
+ * stream h from elsewhere, or null.
+ *   dy, dh, dx [rows][ld] of grad_dtype; dx may be dy or dh itself (the same pointer and leading
+ *   dimension)
+ *   workspace  fp8_rms_norm_backward_workspace_size bytes, any content, 16-byte aligned
+ * Sums in fp32, every one in a fixed order.  rows == 0 gives a dweight of zeros. */
+size_t fp8_rms_norm_backward_workspace_size(int64_t rows, int64_t cols);
+fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,
+                                    fp8q_out_t grad_dtype, const uint16_t* h, int64_t rows,
+                                    int64_t cols, int64_t ld_h, const float* rstd, const void* weight,
+                                    fp8q_out_t weight_dtype, void* dx, int64_t ld_dx, float* dweight,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
