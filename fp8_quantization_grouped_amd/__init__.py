@@ -71,6 +71,12 @@ SIGNATURES = {
     "fp8_moe_few_tokens": (_I, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _I64, _I64, _P, _I64, _I64,
                                 _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64,
                                 _P, _SZ, _P]),
+    "moe_route_with_logits": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I32, _I, _F, _P, _P,
+                                   _P, _I64, _P, _SZ, _P]),
+    "moe_balance_workspace_size": (_SZ, [_I64, _I64, _I32]),
+    "moe_balance": (_I, [_P, _I, _I64, _I64, _I64, _I, _P, _I32, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "moe_route_backward": (_I, [_P, _I, _I64, _I64, _I64, _I, _P, _I32, _P, _I, _F, _P, _P, _P, _I32,
+                                _P, _I64, _P]),
     "fp8_rms_norm": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I, _F, _P, _I64, _P, _I64, _I, _I, _P,
                           _I64, _P, _I64, _P, _P]),
     "fp8_rms_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
@@ -669,11 +675,13 @@ def moe_route_workspace_size(T: int, H: int, E: int) -> int:
 def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
               bias: torch.Tensor | None = None, scoring: str = "softmax",
               renormalize: bool = True, scale: float = 1.0, ids: torch.Tensor | None = None,
-              weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+              weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              logits: torch.Tensor | None = None):
     """The experts of each token: x bf16 [T, H], router bf16 [E, H], bias float32 [E] (added to the
     scores for the choice alone).  scoring: "softmax" or "sigmoid".  Returns (ids int32 [T, top_k],
-    weights float32 [T, top_k]) in descending order; ties go to the lowest index.  No gradient:
-    operands that require one are refused while torch records."""
+    weights float32 [T, top_k]) in descending order; ties go to the lowest index.  logits: float32
+    [T, E] to leave the logits in, for moe_balance and moe_route_backward.  Operands that require a
+    gradient are refused while torch records."""
     T, H, dev = _matrix(x, "x", _BF16)
     _no_grad("moe_route", x, router, bias)
     E = router.shape[0]
@@ -700,11 +708,14 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
             ws = workspace.data_ptr()
     else:
         ws, need = _workspace(workspace, dev)
-    _call("moe_route", dev, x.data_ptr(), T, H, _ld(x, T, H), router.data_ptr(), E,
-          _ld(router, E, H),
-          None if bias is None else bias.data_ptr(), _SCORING[scoring], top_k, int(renormalize),
-          scale, ids.data_ptr(), weights.data_ptr(),
-          ws, need)
+    args = (x.data_ptr(), T, H, _ld(x, T, H), router.data_ptr(), E, _ld(router, E, H),
+            None if bias is None else bias.data_ptr(), _SCORING[scoring], top_k, int(renormalize), scale,
+            ids.data_ptr(), weights.data_ptr())
+    if logits is None:
+        _call("moe_route", dev, *args, ws, need)
+    else:
+        _rows_of(logits, "logits", _F32, (T, E), dev)
+        _call("moe_route_with_logits", dev, *args, logits.data_ptr(), _ld(logits, T, E), ws, need)
     return ids, weights
 
 
@@ -891,3 +902,91 @@ def fp8_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
           h.data_ptr(), rows, cols, _ld(h, rows, cols), rstd.data_ptr(), weight.data_ptr(),
           _OUT[weight.dtype], dx.data_ptr(), _ld(dx, rows, cols), dweight.data_ptr(), ws, need)
     return dx, dweight
+
+
+# ------------------------------------------------- a router's training: balance loss and gradients
+
+def _choice(logits, ids, scoring):
+    """Checks what both calls take; returns T, E, device, top_k and the C calls' first arguments."""
+    T, E, dev = _matrix(logits, "logits", _WIDE)
+    _want(scoring in _SCORING, "scoring must be softmax or sigmoid")
+    _want(ids.dim() == 2, "ids must be a matrix")
+    top_k = ids.shape[1]
+    _rows_of(ids, "ids", _I32T, (T, top_k), dev)
+    _want(ids.is_contiguous(), "ids must be contiguous")
+    return T, E, dev, top_k, (logits.data_ptr(), _OUT[logits.dtype], T, E, _ld(logits, T, E),
+                              _SCORING[scoring], ids.data_ptr(), top_k)
+
+
+def _sequences(sequences, dev):
+    """Pointer and number of the sequences' ends."""
+    if sequences is None:
+        return None, 1
+    _want(sequences.dim() == 1, "sequences must have one dimension")
+    _rows_of(sequences, "sequences", _I32T, sequences.shape, dev)
+    return sequences.data_ptr(), sequences.shape[0]
+
+
+def moe_balance_workspace_size(T: int, E: int, sequences: int) -> int:
+    return int(lib().moe_balance_workspace_size(T, E, sequences))
+
+
+def moe_balance(logits: torch.Tensor, ids: torch.Tensor, scoring: str = "softmax",
+                sequences: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """How evenly tokens choose their experts: logits bf16 or float32 [T, E], ids int32 [T, top_k]
+    (moe_route's); sequences: int32 [S] cumulative ends on the device, None for one of all tokens;
+    tokens behind the last end belong to none.  Returns (loss float32 [S], 1 for an even choice, counts
+    int32 [S, E]).  The gradient is moe_route_backward's: logits that require one are refused while
+    torch records."""
+    T, E, dev, top_k, args = _choice(logits, ids, scoring)
+    _no_record("moe_balance", "moe_route_backward", logits)
+    seq, S = _sequences(sequences, dev)
+    if loss is None:
+        loss = torch.empty(S, dtype=torch.float32, device=dev)
+    else:
+        _rows_of(loss, "loss", _F32, (S,), dev)
+    if counts is None:
+        counts = torch.empty(S, E, dtype=torch.int32, device=dev)
+    else:
+        _rows_of(counts, "counts", _I32T, (S, E), dev)
+        _want(counts.is_contiguous(), "counts must be contiguous")
+    if workspace is None:
+        need = lib().moe_balance_workspace_size(T, E, S)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    else:
+        ws, need = _workspace(workspace, dev)
+    _call("moe_balance", dev, *args, seq, S, loss.data_ptr(), counts.data_ptr(), ws, need)
+    return loss, counts
+
+
+def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor | None = None,
+                       scoring: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                       dloss: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                       sequences: torch.Tensor | None = None, dlogits: torch.Tensor | None = None):
+    """Gradient of the logits, like them: from dweights float32 [T, top_k], of the weights that
+    moe_route forms with scoring, renormalize and scale, and from dloss float32 [S], of moe_balance's
+    loss with its counts and sequences; either may be None.  dlogits may be given as logits to replace
+    them."""
+    T, E, dev, top_k, args = _choice(logits, ids, scoring)
+    if dweights is not None:
+        _rows_of(dweights, "dweights", _F32, (T, top_k), dev)
+        _want(dweights.is_contiguous(), "dweights must be contiguous")
+    loss_args = (None, None, None, 0)
+    if dloss is None:
+        _want(counts is None and sequences is None, "counts and sequences go with dloss")
+    else:
+        seq, S = _sequences(sequences, dev)
+        _rows_of(dloss, "dloss", _F32, (S,), dev)
+        _want(counts is not None, "dloss needs moe_balance's counts")
+        _rows_of(counts, "counts", _I32T, (S, E), dev)
+        _want(counts.is_contiguous(), "counts must be contiguous")
+        loss_args = (dloss.data_ptr(), counts.data_ptr(), seq, S)
+    if dlogits is None:
+        dlogits = torch.empty(T, E, dtype=logits.dtype, device=dev)
+    else:
+        _rows_of(dlogits, "dlogits", (logits.dtype,), logits.shape, dev)
+    _call("moe_route_backward", dev, *args, None if dweights is None else dweights.data_ptr(),
+          int(renormalize), scale, *loss_args, dlogits.data_ptr(), _ld(dlogits, T, E))
+    return dlogits

@@ -81,6 +81,8 @@ struct RouteArgs {
     float* part;       // [splits][T][E] partial logits
     int32_t* ids;
     float* weights;
+    float* logits;     // [T][ld_l], or null
+    int64_t ld_l;
     int T, E, H, top_k, splits, sigmoid, renorm;
     float scale;
 };
@@ -141,6 +143,7 @@ __device__ __forceinline__ void choose(const RouteArgs& p, int64_t t, Choice& s)
     float* by = s.by;
     const int e = threadIdx.x;
     const float l = e < p.E ? logit[e] : 0.0f;
+    if (p.logits && e < p.E) p.logits[t * p.ld_l + e] = l;
     float score = 1.0f / (1.0f + expf(-l));
     if (!p.sigmoid) {
         float top = -INFINITY;
@@ -250,6 +253,7 @@ __global__ __launch_bounds__(64) void route_select_kernel(const RouteArgs p) {
             for (int s = 0; s < p.splits; s++) l += p.part[((int64_t)s * p.T + t) * p.E + e];
         score[v] = l;
         if (e < p.E) top = fmaxf(top, l);
+        if (p.logits && e < p.E) p.logits[t * p.ld_l + e] = l;
     }
     if (!p.sigmoid) {
 #pragma unroll
@@ -667,12 +671,13 @@ extern "C" size_t moe_route_workspace_size(int64_t T, int64_t H, int64_t E) {
     return (size_t)fp8q::route_splits(T, H, E) * (size_t)T * (size_t)E * 4;
 }
 
-extern "C" fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, const uint16_t* router,
-                                   int64_t E, int64_t ld_r, const float* bias, fp8q_scoring_t scoring, int32_t top_k,
-                                   int renormalize, float scale, int32_t* ids, float* weights, void* workspace,
-                                   size_t workspace_bytes, hipStream_t stream) {
+extern "C" fp8q_status_t moe_route_with_logits(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x,
+                                               const uint16_t* router, int64_t E, int64_t ld_r, const float* bias,
+                                               fp8q_scoring_t scoring, int32_t top_k, int renormalize, float scale,
+                                               int32_t* ids, float* weights, float* logits, int64_t ld_l,
+                                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
     using namespace fp8q;
-    if (T < 0 || H < 1 || E < 1 || ld_x < H || ld_r < H || top_k < 1 || top_k > E ||
+    if (T < 0 || H < 1 || E < 1 || ld_x < H || ld_r < H || top_k < 1 || top_k > E || (logits && ld_l < E) ||
         (scoring != FP8Q_SCORE_SOFTMAX && scoring != FP8Q_SCORE_SIGMOID))
         return FP8Q_ERR_INVALID_ARG;
     if (T == 0) return FP8Q_OK;
@@ -684,7 +689,7 @@ extern "C" fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int6
     if (!fp8q_aligned(workspace, 4)) return FP8Q_ERR_INVALID_ARG;
     RouteArgs p{};
     p.x = x; p.ld_x = ld_x; p.router = router; p.ld_r = ld_r; p.bias = bias; p.part = reinterpret_cast<float*>(workspace);
-    p.ids = ids; p.weights = weights; p.T = (int)T; p.E = (int)E; p.H = (int)H; p.top_k = top_k;
+    p.ids = ids; p.weights = weights; p.logits = logits; p.ld_l = ld_l; p.T = (int)T; p.E = (int)E; p.H = (int)H; p.top_k = top_k;
     p.splits = route_splits(T, H, E); p.sigmoid = scoring == FP8Q_SCORE_SIGMOID; p.renorm = renormalize != 0; p.scale = scale;
     if (route_is_small(H, E)) {
         route_small_kernel<<<dim3((unsigned)T), dim3(1024), 0, stream>>>(p);
@@ -698,6 +703,14 @@ extern "C" fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int6
     else route_select_kernel<16><<<grid, block, 0, stream>>>(p);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
+}
+
+extern "C" fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, const uint16_t* router,
+                                   int64_t E, int64_t ld_r, const float* bias, fp8q_scoring_t scoring, int32_t top_k,
+                                   int renormalize, float scale, int32_t* ids, float* weights, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+    return moe_route_with_logits(x, T, H, ld_x, router, E, ld_r, bias, scoring, top_k, renormalize, scale, ids, weights,
+                                 nullptr, 0, workspace, workspace_bytes, stream);
 }
 
 // Workspace: h, then the experts' outputs, both 32-bit.

@@ -427,6 +427,14 @@ fp8q_status_t moe_route(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x, c
                         int32_t top_k, int renormalize, float scale, int32_t* ids, float* weights,
                         void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* moe_route that also leaves the logits behind, fp32 [T][ld_l >= E] (or null), for the balance loss
+ * and the gradients below.  The same ids and weights. */
+fp8q_status_t moe_route_with_logits(const uint16_t* x, int64_t T, int64_t H, int64_t ld_x,
+                                    const uint16_t* router, int64_t E, int64_t ld_r, const float* bias,
+                                    fp8q_scoring_t scoring, int32_t top_k, int renormalize, float scale,
+                                    int32_t* ids, float* weights, float* logits, int64_t ld_l,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* fp8_moe_few_tokens: for every token t
  *   y[t] = sum_j weights[t,j] * W2_e (silu(G_e x_t) * (U_e x_t)),  e = ids[t,j]
  * with e4m3fn weights in blocks of 128 x 128 (fp8_block_quant_weights): [G_e; U_e] = w13[e] is
@@ -496,6 +504,42 @@ fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* d
                                     int64_t cols, int64_t ld_h, const float* rstd, const void* weight,
                                     fp8q_out_t weight_dtype, void* dx, int64_t ld_dx, float* dweight,
                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * A router's training: balance loss, counts, and the gradient of the logits.
+ *
+ * Of logits [T][ld_l >= E] of logits_dtype:
+ *   p[t,e] = softmax over e, or sigmoid(l[t,e]) over the row's sum of sigmoids (formed as a softmax
+ *            where that sum is under 2^-64; a row whose logits are all minus infinity has p = 0)
+ * moe_balance: tokens belong to sequences, int32[S] cumulative END rows on the device like offsets
+ * (null with S == 1: one sequence of all T tokens); tokens behind the last end belong to none.  With
+ * n_s tokens in sequence s and counts[s,e] = how often ids names expert e there
+ *   loss[s] = E / (top_k * n_s^2) * sum_e counts[s,e] * sum_{t in s} p[t,e]     (fp32; 0 if n_s = 0)
+ * which is 1 where both are even.
+ *   ids int32 [T][top_k]; an id outside [0, E) counts nowhere, one named twice counts twice
+ *   loss fp32 [S], counts int32 [S][E]
+ *   workspace  moe_balance_workspace_size bytes, any content, 16-byte aligned
+ * Sums in fp32, every one in a fixed order; counts are whole numbers.
+ *
+ * moe_route_backward: dlogits [T][ld_d] of logits_dtype, of the sum of
+ *   dloss[s] * loss[s], where dloss fp32 [S] is not null: counts and sequences are moe_balance's, the
+ *   counts held fixed (they have no gradient);
+ *   dweights[t,j] * weights[t,j], where dweights fp32 [T][top_k] is not null: weights as moe_route
+ *   forms them from these logits and ids with scoring, renormalize and scale (its bias enters the
+ *   choice alone).
+ * Without dloss, counts, sequences and S are ignored.  dlogits may be logits itself (the same pointer
+ * and leading dimension).
+ * Limits (FP8Q_ERR_UNSUPPORTED): E <= 1024, top_k <= 32, T < 2^31. */
+size_t moe_balance_workspace_size(int64_t T, int64_t E, int32_t sequences);
+fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype, int64_t T, int64_t E,
+                          int64_t ld_l, fp8q_scoring_t scoring, const int32_t* ids, int32_t top_k,
+                          const int32_t* sequences, int32_t S, float* loss, int32_t* counts,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream);
+fp8q_status_t moe_route_backward(const void* logits, fp8q_out_t logits_dtype, int64_t T, int64_t E,
+                                 int64_t ld_l, fp8q_scoring_t scoring, const int32_t* ids,
+                                 int32_t top_k, const float* dweights, int renormalize, float scale,
+                                 const float* dloss, const int32_t* counts, const int32_t* sequences,
+                                 int32_t S, void* dlogits, int64_t ld_d, hipStream_t stream);
 
 #ifdef __cplusplus
 }
