@@ -77,6 +77,7 @@ SIGNATURES = {
     "moe_balance": (_I, [_P, _I, _I64, _I64, _I64, _I, _P, _I32, _P, _I32, _P, _P, _P, _SZ, _P]),
     "moe_route_backward": (_I, [_P, _I, _I64, _I64, _I64, _I, _P, _I32, _P, _I, _F, _P, _P, _P, _I32,
                                 _P, _I64, _P]),
+    "adamw_step": (_I, [_P, _I32, _P, _P]),
     "fp8_rms_norm": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I, _F, _P, _I64, _P, _I64, _I, _I, _P,
                           _I64, _P, _I64, _P, _P]),
     "fp8_rms_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
@@ -990,3 +991,124 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
     _call("moe_route_backward", dev, *args, None if dweights is None else dweights.data_ptr(),
           int(renormalize), scale, *loss_args, dlogits.data_ptr(), _ld(dlogits, T, E))
     return dlogits
+
+
+# --------------------------------------------------------------------- AdamW over many tensors
+
+class _AdamTensor(ctypes.Structure):
+    _fields_ = [("param", _P), ("master", _P), ("grad", _P), ("exp_avg", _P), ("exp_avg_scales", _P),
+                ("exp_avg_sq", _P), ("exp_avg_sq_scales", _P), ("n", _I64), ("param_dtype", _I), ("grad_dtype", _I)]
+
+
+class _Adam(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("lr_device", _P), ("step_device", _P),
+                ("grad_scale", _P), ("step", _I64), ("seed", ctypes.c_uint64), ("lr", _F), ("eps", _F),
+                ("weight_decay", _F), ("state_bits", _I32)]
+
+
+class AdamWStates:
+    """The states of AdamW for a list of parameters (bf16 or float32, contiguous, all on one GPU), which
+    adamw_step updates in place.
+
+    bits=32: exp_avg and exp_avg_sq are lists of float32 tensors like the parameters.  bits=8: exp_avg
+    holds the first moments and exp_avg_sq the roots of the second ones as e4m3fn bytes, with the block
+    factors float32 [ceil(n/128)] in exp_avg_scales and exp_avg_sq_scales: of a flattened parameter the
+    layout that fp8_block_quant_rowwise gives one row.  masters: float32 copies of bf16 parameters, where
+    the steps add up; None for a parameter without one.  States given (those of an earlier run) are used
+    as they are, others begin with zeros."""
+
+    def __init__(self, params, bits: int = 8, masters=None, exp_avg=None, exp_avg_sq=None,
+                 exp_avg_scales=None, exp_avg_sq_scales=None):
+        self.params, self.bits = list(params), bits
+        _want(bits in (8, 32), "states have 8 or 32 bits")
+        n = len(self.params)
+        self.device = dev = self.params[0].device if n else None
+        self.masters = [None] * n if masters is None else list(masters)
+        given = [exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales]
+        eight = bits == 8
+        used = [None if g is None else list(g) for g in (given if eight else given[:2])]
+        _want(eight or (exp_avg_scales is None and exp_avg_sq_scales is None), "states of 32 bits have no scales")
+        _want(all((g is None) == (exp_avg is None) for g in used), "states are given all together or not at all")
+        lists = [self.masters] + [g for g in used if g is not None]
+        _want(all(len(g) == n for g in lists), "masters and states must be as many as the parameters")
+        for p in self.params:
+            self._flat(p, "a parameter", _WIDE, p.numel())
+        if exp_avg is None:
+            zeros = lambda m, dtype: torch.zeros(m, dtype=dtype, device=dev)
+            if eight:
+                used = [[zeros(p.numel(), torch.uint8) for p in self.params] for _ in range(2)]
+                used += [[zeros(_blocks(p.numel()), torch.float32) for p in self.params] for _ in range(2)]
+            else:
+                used = [[zeros(p.shape, torch.float32) for p in self.params] for _ in range(2)]
+        self.exp_avg, self.exp_avg_sq = used[:2]
+        self.exp_avg_scales, self.exp_avg_sq_scales = used[2:] if eight else ([None] * n, [None] * n)
+        self._table = (_AdamTensor * n)()
+        taken = set()
+        for i, p in enumerate(self.params):
+            m = p.numel()
+            mine = [p, self.masters[i], self.exp_avg[i], self.exp_avg_sq[i]]
+            if mine[1] is not None:
+                _want(p.dtype is torch.bfloat16, "masters are of bfloat16 parameters")
+                self._flat(mine[1], "a master", _F32, m)
+            for t in mine[2:]:
+                self._flat(t, "a state", _BYTES if eight else _F32, m)
+            if eight:
+                mine += [self.exp_avg_scales[i], self.exp_avg_sq_scales[i]]
+                for t in mine[4:]:
+                    self._flat(t, "a state's scales", _F32, _blocks(m))
+            for t in mine:
+                if t is not None and m:
+                    _want(t.data_ptr() not in taken, "no two parameters or states may share memory")
+                    taken.add(t.data_ptr())
+            row = self._table[i]
+            row.param, row.n, row.param_dtype = p.data_ptr(), m, _OUT[p.dtype]
+            row.master = None if mine[1] is None else mine[1].data_ptr()
+            row.exp_avg, row.exp_avg_sq = mine[2].data_ptr(), mine[3].data_ptr()
+            if eight:
+                row.exp_avg_scales, row.exp_avg_sq_scales = mine[4].data_ptr(), mine[5].data_ptr()
+
+    def _flat(self, t, what, dtypes, n):
+        _want(t.is_cuda and t.device == self.device, f"{what} must be on the first parameter's GPU")
+        _want(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+        _want(t.numel() == n and t.is_contiguous(), f"{what} must be contiguous, of {n} elements")
+
+
+def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
+               weight_decay: float = 0.01, seed: int = 0, grad_scale: torch.Tensor | None = None) -> None:
+    """One step for all parameters of states, in place: grads bf16 or float32 like the parameters, None
+    where one has none (it and its states stay).  step counts from 1; step (int32) and lr (float32) may
+    be device tensors of one element, which a replayed graph reads anew.  grad_scale: float32 device
+    tensor of one element that the gradients are multiplied by.  The random bits that 8-bit states are
+    rounded by are a function of seed + step."""
+    dev, table = states.device, states._table
+    grads = list(grads)
+    _want(len(grads) == len(states.params), "grads must be as many as the parameters")
+    _want(0 <= betas[0] < 1 and 0 <= betas[1] < 1, "betas must lie in [0, 1)")
+    _want(eps > 0, "eps must be positive")
+    h = _Adam(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay, state_bits=states.bits,
+              seed=seed & 0xFFFFFFFF)
+    for i, g in enumerate(grads):
+        row = table[i]
+        if g is None:
+            row.grad = None
+            continue
+        if not (g.is_cuda and g.device == dev and g.dtype in _OUT and g.is_contiguous()
+                and g.shape == states.params[i].shape):
+            raise ValueError("a gradient must be contiguous, bfloat16 or float32, of its parameter's shape and on "
+                             "its GPU")
+        row.grad, row.grad_dtype = g.data_ptr(), _OUT[g.dtype]
+    for name, t, dtype in (("step", step, torch.int32), ("lr", lr, torch.float32), ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(t, torch.Tensor):
+            _want(t.is_cuda and t.device == dev and t.dtype is dtype and t.numel() == 1,
+                  f"{name} must be one {dtype} on the parameters' GPU")
+            setattr(h, name if name == "grad_scale" else name + "_device", t.data_ptr())
+        elif name == "lr":
+            h.lr = lr
+        elif name == "step":
+            _want(step >= 1, "step counts from 1")
+            h.step = step
+        else:
+            _want(t is None, "grad_scale must be a device tensor")
+    if not grads:
+        return
+    _call("adamw_step", dev, ctypes.addressof(table), len(grads), ctypes.addressof(h))

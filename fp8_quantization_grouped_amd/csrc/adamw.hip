@@ -1,0 +1,297 @@
+// One AdamW step over a list of tensors, with the states in 32 bits or in 8.
+//
+//   m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,
+//   p' = p - lr (m' / (1 - b1^t) / (sqrt(v' / (1 - b2^t)) + eps) + decay p)
+//
+// 8 bits: m and r = sqrt(v) are kept as e4m3fn values with one fp32 factor d per block of 128 elements
+// (s = 448 / max(amax, 1e-12), d = 1 / s, as the block quantizers).  r instead of v, since a square has
+// twice the range.  The new value goes to the grid's next value down or up, at random in proportion: with
+// b2 = 0.999 one step changes r by 2^-11 of itself and the grid's steps are 2^-4 of it, so the nearest
+// value would mostly be the old one for ever.  A nonzero r never becomes zero, which would divide a
+// remaining m by eps.  What the step itself uses is m' and v' in 32 bits, before they are kept.  The kept r
+// of a stationary gradient spreads about its true value by a sixth of it (b2 = 0.999) to a ninth (0.95),
+// the mean being 1% above: a value on the grid that moves by a small e of itself is rounded with a variance
+// of e times the step, so slow averages take little noise a step.
+//
+// Random bits: word(tensor, element) = mix(mix(seed * 0x9E3779B1 + tensor) + element), mix two rounds of
+// xor-shift and odd product (as in the finalizers of published hash functions, with constants of its
+// own); m takes the word, r the word with its halves exchanged, the conversion the upper 20 bits of each.
+//
+// Bound: HBM.
+#include "common.hpp"
+
+namespace fp8q {
+
+constexpr int AB = 128;            // elements of a block with one factor
+constexpr int ADAMW_TENSORS = 40;  // of one launch: its arguments fit the 4 KB that a launch takes
+constexpr int CHUNK = 2048;        // elements that a block of threads takes at a time
+
+struct AdamTensor {
+    void* param;
+    float* master;
+    const void* grad;
+    void* m;
+    float* m_scales;
+    void* v;
+    float* v_scales;
+    int64_t n;
+    uint32_t index;          // place in the caller's list
+    uint8_t param32, grad32, wide, pad;
+};
+
+struct AdamArgs {
+    AdamTensor t[ADAMW_TENSORS];
+    int64_t chunk_end[ADAMW_TENSORS];  // chunks up to and with tensor i
+    int count;
+    float lr, b1, b2, one_b1, one_b2, eps, decay, inv_bc1, inv_bc2;
+    float log_b1, log_b2;
+    uint32_t seed;
+    const float* lr_device;
+    const int32_t* step_device;
+    const float* grad_scale;
+};
+
+__device__ __forceinline__ float ad_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ uint16_t ad_to_bf16(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);  // NaN stays NaN
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+// An access that is always one to global memory, also where the compiler would choose between this
+// pointer and the address of an argument.
+template <class T>
+using Global = __attribute__((address_space(1))) T*;
+template <class T>
+__device__ __forceinline__ T global_at(const T* p, int64_t i) { return ((Global<const T>)p)[i]; }
+
+__device__ __forceinline__ uint32_t mix(uint32_t z) {
+    z = (z ^ z >> 16) * 0x7F4A7C15u;
+    z = (z ^ z >> 15) * 0x2C9277B5u;
+    return z ^ z >> 16;
+}
+
+// Eight consecutive elements as 32-bit values; n of them exist.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* src, int64_t at, int n, bool wide, float (&out)[8]) {
+    if (F32) {
+        const float* p = static_cast<const float*>(src) + at;
+        if (wide && n == 8) {
+            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+            out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w; out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) out[i] = i < n ? p[i] : 0.0f;
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(src) + at;
+        if (wide && n == 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            out[0] = bf16_lo(a.x); out[1] = bf16_hi(a.x); out[2] = bf16_lo(a.y); out[3] = bf16_hi(a.y);
+            out[4] = bf16_lo(a.z); out[5] = bf16_hi(a.z); out[6] = bf16_lo(a.w); out[7] = bf16_hi(a.w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) out[i] = i < n ? ad_bf16(p[i]) : 0.0f;
+        }
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* dst, int64_t at, int n, bool wide, const float (&v)[8]) {
+    if (F32) {
+        float* p = static_cast<float*>(dst) + at;
+        if (wide && n == 8) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (i < n) p[i] = v[i];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(dst) + at;
+        if (wide && n == 8) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(ad_to_bf16(v[0]) | (uint32_t)ad_to_bf16(v[1]) << 16,
+                                                      ad_to_bf16(v[2]) | (uint32_t)ad_to_bf16(v[3]) << 16,
+                                                      ad_to_bf16(v[4]) | (uint32_t)ad_to_bf16(v[5]) << 16,
+                                                      ad_to_bf16(v[6]) | (uint32_t)ad_to_bf16(v[7]) << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (i < n) p[i] = ad_to_bf16(v[i]);
+        }
+    }
+}
+
+typedef float f2_t __attribute__((ext_vector_type(2)));
+
+// Eight e4m3fn bytes times their block's factor.
+__device__ __forceinline__ void load8_fp8(const void* src, int64_t at, int n, bool wide, float d, float (&out)[8]) {
+    const uint8_t* p = static_cast<const uint8_t*>(src) + at;
+    uint32_t w[2] = {0, 0};
+    if (wide && n == 8) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p);
+        w[0] = a.x; w[1] = a.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], true);
+        out[4 * i] = lo.x * d; out[4 * i + 1] = lo.y * d; out[4 * i + 2] = hi.x * d; out[4 * i + 3] = hi.y * d;
+    }
+}
+
+// Keeps eight values of a block that 16 lanes share: factor and bytes.  ROOT: nonzero values, all of one
+// sign, do not become zero.
+template <bool ROOT>
+__device__ __forceinline__ void keep8(void* dst, float* scales, int64_t at, int n, bool wide, const float (&x)[8], const uint32_t (&bits)[8]) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+    const float s = scale_from_amax<FP8Q_E4M3FN>(amax);
+    if ((threadIdx.x & 15) == 0 && n > 0) scales[at / AB] = 1.0f / s;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float y = __builtin_amdgcn_fmed3f(x[i] * s, -kFmaxFn, kFmaxFn);
+        const uint32_t r = ROOT ? bits[i] << 16 | bits[i] >> 16 : bits[i];
+        uint32_t b = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, 0, 0) & 0xFFu;
+        if (ROOT) b = x[i] > 0.0f && b == 0 ? 1u : b;
+        w[i >> 2] |= b << (8 * (i & 3));
+    }
+    uint8_t* p = static_cast<uint8_t*>(dst) + at;
+    if (wide && n == 8) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+    }
+}
+
+template <bool EIGHT>
+__global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
+    int lo = 0, hi = a.count - 1;  // the tensor of this chunk
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.chunk_end[mid] > (int64_t)blockIdx.x) hi = mid; else lo = mid + 1;
+    }
+    const AdamTensor& t = a.t[lo];
+    const int64_t first = lo ? a.chunk_end[lo - 1] : 0;
+    const int64_t at = ((int64_t)blockIdx.x - first) * CHUNK + 8 * threadIdx.x;
+    const int n = t.n - at >= 8 ? 8 : t.n > at ? (int)(t.n - at) : 0;
+    const float lr = a.lr_device ? global_at(a.lr_device, 0) : a.lr;
+    float inv_bc1 = a.inv_bc1, inv_bc2 = a.inv_bc2;
+    uint32_t seed = a.seed;
+    if (a.step_device) {
+        const int32_t step = global_at(a.step_device, 0);
+        inv_bc1 = -1.0f / expm1f((float)step * a.log_b1);
+        inv_bc2 = -1.0f / expm1f((float)step * a.log_b2);
+        seed += (uint32_t)step;
+    }
+    const bool wide = t.wide;
+    float p[8], g[8], m[8], v[8], r[8];
+    if (t.master) load8<true>(t.master, at, n, wide, p);
+    else if (t.param32) load8<true>(t.param, at, n, wide, p);
+    else load8<false>(t.param, at, n, wide, p);
+    if (t.grad32) load8<true>(t.grad, at, n, wide, g);
+    else load8<false>(t.grad, at, n, wide, g);
+    if (a.grad_scale) {
+        const float gs = global_at(a.grad_scale, 0);
+#pragma unroll
+        for (int i = 0; i < 8; i++) g[i] *= gs;
+    }
+    if (EIGHT) {
+        const bool any = n > 0;
+        load8_fp8(t.m, at, n, wide, any ? t.m_scales[at / AB] : 0.0f, m);
+        load8_fp8(t.v, at, n, wide, any ? t.v_scales[at / AB] : 0.0f, v);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] *= v[i];
+    } else {
+        load8<true>(t.m, at, n, wide, m);
+        load8<true>(t.v, at, n, wide, v);
+    }
+    const float root_bc2 = sqrtf(inv_bc2);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        m[i] = a.b1 * m[i] + a.one_b1 * g[i];
+        v[i] = a.b2 * v[i] + a.one_b2 * g[i] * g[i];
+        r[i] = sqrtf(v[i]);
+        const float d = (m[i] * inv_bc1) / (r[i] * root_bc2 + a.eps);
+        p[i] = p[i] - lr * (d + a.decay * p[i]);
+    }
+    if (t.master) store8<true>(t.master, at, n, wide, p);
+    if (t.param32) store8<true>(t.param, at, n, wide, p);
+    else store8<false>(t.param, at, n, wide, p);
+    if (EIGHT) {
+        const uint32_t key = mix(seed * 0x9E3779B1u + t.index) + (uint32_t)at + (uint32_t)(at >> 32) * 0x632BE5A7u;
+        uint32_t bits[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) bits[i] = mix(key + i);
+        keep8<false>(t.m, t.m_scales, at, n, wide, m, bits);
+        keep8<true>(t.v, t.v_scales, at, n, wide, r, bits);
+    } else {
+        store8<true>(t.m, at, n, wide, m);
+        store8<true>(t.v, at, n, wide, v);
+    }
+}
+
+static inline bool ad_real(const fp8q_adamw_tensor_t& t) { return t.n > 0 && t.grad; }
+
+}  // namespace fp8q
+
+extern "C" fp8q_status_t adamw_step(const fp8q_adamw_tensor_t* tensors, int32_t count, const fp8q_adamw_t* h, hipStream_t stream) {
+    using namespace fp8q;
+    if (count < 0 || !h || (count > 0 && !tensors) || (h->state_bits != 8 && h->state_bits != 32) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
+        !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps > 0.0f) || (!h->step_device && h->step < 1))
+        return FP8Q_ERR_INVALID_ARG;
+    const bool eight = h->state_bits == 8;
+    for (int32_t i = 0; i < count; i++) {  // all of them before the first launch
+        const fp8q_adamw_tensor_t& t = tensors[i];
+        if (t.n < 0 || (t.param_dtype != FP8Q_OUT_BF16 && t.param_dtype != FP8Q_OUT_FP32) ||
+            (t.grad_dtype != FP8Q_OUT_BF16 && t.grad_dtype != FP8Q_OUT_FP32) || (t.master && t.param_dtype != FP8Q_OUT_BF16))
+            return FP8Q_ERR_INVALID_ARG;
+        if (!ad_real(t)) continue;
+        if (!t.param || !t.exp_avg || !t.exp_avg_sq || (eight && (!t.exp_avg_scales || !t.exp_avg_sq_scales))) return FP8Q_ERR_INVALID_ARG;
+        if (t.n > (int64_t)CHUNK << 23) return FP8Q_ERR_UNSUPPORTED;  // a launch takes fewer than 2^32 threads
+    }
+    AdamArgs a{};
+    a.b1 = (float)h->beta1; a.b2 = (float)h->beta2; a.one_b1 = (float)(1.0 - h->beta1); a.one_b2 = (float)(1.0 - h->beta2);
+    a.eps = h->eps; a.decay = h->weight_decay; a.lr = h->lr; a.lr_device = h->lr_device; a.step_device = h->step_device;
+    a.grad_scale = h->grad_scale; a.seed = (uint32_t)h->seed;
+    if (h->step_device) {
+        a.log_b1 = (float)log(h->beta1);
+        a.log_b2 = (float)log(h->beta2);
+    } else {
+        a.inv_bc1 = (float)(1.0 / (1.0 - pow(h->beta1, (double)h->step)));
+        a.inv_bc2 = (float)(1.0 / (1.0 - pow(h->beta2, (double)h->step)));
+        a.seed += (uint32_t)h->step;
+    }
+    for (int32_t i = 0; i < count;) {
+        int64_t chunks = 0;
+        a.count = 0;
+        for (; i < count && a.count < ADAMW_TENSORS; i++) {
+            const fp8q_adamw_tensor_t& t = tensors[i];
+            if (!ad_real(t)) continue;
+            const int64_t more = (t.n + CHUNK - 1) / CHUNK;
+            if (chunks + more >= 1LL << 24) break;
+            AdamTensor& to = a.t[a.count];
+            to.param = t.param; to.master = t.master; to.grad = t.grad; to.m = t.exp_avg; to.m_scales = t.exp_avg_scales;
+            to.v = t.exp_avg_sq; to.v_scales = t.exp_avg_sq_scales; to.n = t.n; to.index = (uint32_t)i;
+            to.param32 = t.param_dtype == FP8Q_OUT_FP32; to.grad32 = t.grad_dtype == FP8Q_OUT_FP32;
+            to.wide = fp8q_aligned(t.param, 16) && fp8q_aligned(t.master, 16) && fp8q_aligned(t.grad, 16) &&
+                      fp8q_aligned(t.exp_avg, eight ? 8 : 16) && fp8q_aligned(t.exp_avg_sq, eight ? 8 : 16);
+            chunks += more;
+            a.chunk_end[a.count++] = chunks;
+        }
+        if (a.count == 0) break;
+        if (eight) adamw_kernel<true><<<dim3((unsigned)chunks), dim3(256), 0, stream>>>(a);
+        else adamw_kernel<false><<<dim3((unsigned)chunks), dim3(256), 0, stream>>>(a);
+        FP8Q_CHECK_LAUNCH();
+    }
+    return FP8Q_OK;
+}

@@ -541,6 +541,51 @@ fp8q_status_t moe_route_backward(const void* logits, fp8q_out_t logits_dtype, in
                                  const float* dloss, const int32_t* counts, const int32_t* sequences,
                                  int32_t S, void* dlogits, int64_t ld_d, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * AdamW over a list of tensors, in place, in one launch for each 40 of them.  With gradient g (times
+ * *grad_scale, where that is not null), step t >= 1 and every operation in 32 bits:
+ *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
+ *   p' = p - lr (m' / (1 - beta1^t) / (sqrt(v' / (1 - beta2^t)) + eps) + weight_decay p)
+ * p is the master (fp32) where there is one, and then goes to both; else the parameter itself.  bf16
+ * parameters are rounded to the nearest.
+ * state_bits 32: exp_avg and exp_avg_sq hold m and v, fp32 [n]; the scales are ignored.
+ * state_bits 8: exp_avg and exp_avg_sq hold m and the root r = sqrt(v), e4m3fn [n], with factors
+ *   d = 1 / s fp32 [ceil(n/128)], s = 448 / max(absmax, 1e-12f), for each 128 consecutive elements: the
+ *   blocks of fp8_block_quant_rowwise of the tensor as one row.  m' and r' are kept as the grid's value
+ *   below or above at random, in proportion to the distance (the step itself takes them unrounded); a
+ *   nonzero r' is kept as one.  The random bits are a function of (seed + step) mod 2^32, the tensor's place in
+ *   the list and the element's place in the tensor, so a step repeats to the bit.  States of zeros
+ *   (bytes and factors) begin.
+ * Where step_device (int32) or lr_device (fp32) is not null the value there takes the place of step or
+ * lr, so that a captured step can be replayed: the device's value is read at each replay.
+ * tensors, h: on the host, read before the call returns.  A tensor with n == 0 or a null gradient is left
+ * as it is.  No two tensors may share memory.  Any alignment; 16-byte aligned pointers (8-bit states: 8)
+ * take the wide accesses.  n <= 2^34 (FP8Q_ERR_UNSUPPORTED beyond). */
+typedef struct {
+    void* param;             /* param_dtype [n] */
+    float* master;           /* fp32 [n] of a bf16 param, or null */
+    const void* grad;        /* grad_dtype [n], or null */
+    void* exp_avg;
+    float* exp_avg_scales;
+    void* exp_avg_sq;
+    float* exp_avg_sq_scales;
+    int64_t n;
+    fp8q_out_t param_dtype;
+    fp8q_out_t grad_dtype;
+} fp8q_adamw_tensor_t;
+typedef struct {
+    double beta1, beta2;     /* in [0, 1) */
+    const float* lr_device;
+    const int32_t* step_device;
+    const float* grad_scale;
+    int64_t step;
+    uint64_t seed;
+    float lr, eps, weight_decay;
+    int32_t state_bits;
+} fp8q_adamw_t;
+fp8q_status_t adamw_step(const fp8q_adamw_tensor_t* tensors, int32_t count, const fp8q_adamw_t* h,
+                         hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
