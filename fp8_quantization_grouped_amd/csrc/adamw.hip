@@ -173,6 +173,14 @@ __device__ __forceinline__ void keep8(void* dst, float* scales, int64_t at, int 
     }
 }
 
+// The states' averages, each operation rounded by itself: what is kept of them can be told to the bit from
+// elementary operations in 32 bits, and a value next to the grid's border falls where those say.
+__device__ __forceinline__ void moments(const AdamArgs& a, float g, float& m, float& v) {
+#pragma clang fp contract(off)
+    m = a.b1 * m + a.one_b1 * g;
+    v = a.b2 * v + a.one_b2 * g * g;
+}
+
 template <bool EIGHT>
 __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
     int lo = 0, hi = a.count - 1;  // the tensor of this chunk
@@ -218,8 +226,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
     const float root_bc2 = sqrtf(inv_bc2);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        m[i] = a.b1 * m[i] + a.one_b1 * g[i];
-        v[i] = a.b2 * v[i] + a.one_b2 * g[i] * g[i];
+        moments(a, g[i], m[i], v[i]);
         r[i] = sqrtf(v[i]);
         const float d = (m[i] * inv_bc1) / (r[i] * root_bc2 + a.eps);
         p[i] = p[i] - lr * (d + a.decay * p[i]);
