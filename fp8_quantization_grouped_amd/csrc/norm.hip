@@ -13,7 +13,7 @@ constexpr int NB = 128;  // elements of a block with one factor
 
 struct NormArgs {
     const uint16_t* x;
-    int64_t cols, ld_x;
+    int64_t rows, cols, ld_x;
     const uint16_t* residual;
     int64_t ld_res;
     const void* w;
@@ -64,7 +64,212 @@ __device__ __forceinline__ float rstd_of(float sum, float cols, float eps) { ret
 // Where the sum of squares has overflowed: from the squares' sum of h * 2^-80; eps is far below them.
 __device__ __forceinline__ float rstd_of_shrunk(float sum, float cols) { return kShrink / sqrtf(sum / cols); }
 
-// Any size and alignment: a block of 4 waves per row, a wave takes blocks of 128 columns in turn, a lane
+// Eight consecutive elements from 8 c on of a row of 8 or more, zeros past its end.  A wide access need not
+// be aligned here.  A chunk that the row's end cuts is read as the row's last eight, which stay inside it
+// in one access, and moved down: reading it by elements costs the loop 7 registers for every such load.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int64_t c, int64_t cols) {
+    const int64_t over = 8 * c + 8 - cols;
+    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(row + 8 * c - (over > 0 ? over : 0));
+    if (over <= 0) return make_uint4(v.x, v.y, v.z, v.w);
+    uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+    const int k = 16 * (int)over;  // bits, under 128
+    lo = k >= 64 ? hi >> (k - 64) : k ? lo >> k | hi << (64 - k) : lo;
+    hi = k >= 64 ? 0 : hi >> k;
+    return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+}
+__device__ __forceinline__ void store_chunk(uint16_t* row, int64_t c, int64_t cols, uint4 v) {
+    if (8 * c + 8 <= cols) {
+        *reinterpret_cast<u32x4_any*>(row + 8 * c) = u32x4_any{v.x, v.y, v.z, v.w};
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+        if (8 * c + i < cols) row[8 * c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+}
+__device__ __forceinline__ void store_bytes(uint8_t* row, int64_t c, int64_t cols, uint32_t a, uint32_t b) {
+    if (8 * c + 8 <= cols) {
+        *reinterpret_cast<u32x2_any*>(row + 8 * c) = u32x2_any{a, b};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+        if (8 * c + i < cols) row[8 * c + i] = (uint8_t)((i < 4 ? a : b) >> (8 * (i & 3)));
+}
+__device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) { return (uint32_t)bf16_rn(a) | (uint32_t)bf16_rn(b) << 16; }
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+__device__ __forceinline__ void load_floats(const float* row, int64_t c, int64_t cols, float (&f)[8]) {
+    const int64_t over = 8 * c + 8 - cols;
+    const float* p = row + 8 * c - (over > 0 ? over : 0);
+    const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    if (over > 0) {
+#pragma unroll
+        for (int k = 4; k > 0; k >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] = over & k ? (i + k < 8 ? f[i + k] : 0.0f) : f[i];
+    }
+}
+__device__ __forceinline__ void load_weight(const void* w, bool w32, int64_t c, int64_t cols, float (&f)[8]) {
+    if (w32) load_floats(static_cast<const float*>(w), c, cols, f);
+    else unpack(load_chunk(static_cast<const uint16_t*>(w), c, cols), f);
+}
+
+// Block b of n in an order that gives each XCD (blocks go to the 8 of them in turn) one run of rows: what
+// neighbouring rows write side by side, the factors of a block column, then meets in one L2.
+__device__ __forceinline__ int64_t xcd_run(unsigned b, unsigned n) {
+    const unsigned x = b % 8, q = n / 8, r = n % 8;
+    return (int64_t)x * q + (x < r ? x : r) + b / 8;
+}
+
+// Sum (SUM) or maximum over the WPR waves of a row; red: a float for each of the block's waves.
+template <int WPR, bool SUM>
+__device__ __forceinline__ float across(float v, float* red) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const float o = __shfl_xor(v, off, 64);
+        v = SUM ? v + o : fmaxf(v, o);
+    }
+    if (WPR == 1) return v;
+    const int wave = threadIdx.x >> 6, w0 = wave / WPR * WPR;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    v = red[w0];
+#pragma unroll
+    for (int w = 1; w < WPR; w++) v = SUM ? v + red[w0 + w] : fmaxf(v, red[w0 + w]);
+    return v;
+}
+
+// Rows held in registers: WPR waves a row, NV chunks of 8 elements a lane.
+template <int SC, int FMT, int WPR, int NV>
+__global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const NormArgs p) {
+    constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR, TPR = 64 * WPR;
+    __shared__ float red[3][WAVES];
+    const int wave = threadIdx.x >> 6, t = threadIdx.x % TPR;
+    const int64_t group = SC == FP8Q_NORM_BLOCK ? xcd_run(blockIdx.x, gridDim.x) : (int64_t)blockIdx.x;
+    const int64_t r = group * RPB + wave / WPR;
+    const bool row_ok = r < p.rows;
+    const int64_t row = row_ok ? r : p.rows - 1, cols = row_ok ? p.cols : 0;  // no columns of a row past the last
+    uint4 h[NV], res[NV];
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int64_t c = t + (int64_t)j * TPR;
+        h[j] = res[j] = make_uint4(0, 0, 0, 0);
+        if (8 * c < cols) {
+            h[j] = load_chunk(p.x + row * p.ld_x, c, cols);
+            if (p.residual) res[j] = load_chunk(p.residual + row * p.ld_res, c, cols);
+        }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int64_t c = t + (int64_t)j * TPR;
+        float f[8];
+        unpack(h[j], f);
+        if (p.residual) {
+            float g[8];
+            unpack(res[j], g);
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] += g[i];
+            h[j] = pack(f);
+            unpack(h[j], f);
+            if (8 * c < cols) store_chunk(p.h + row * p.ld_h, c, cols, h[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum += f[i] * f[i];
+    }
+    sum = across<WPR, true>(sum, red[0]);
+    float rstd;
+    if (sum == INFINITY) {  // (the same in the whole row)
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            float f[8];
+            unpack(h[j], f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum += (f[i] * kShrink) * (f[i] * kShrink);
+        }
+        rstd = rstd_of_shrunk(across<WPR, true>(sum, red[1]), (float)p.cols);
+    } else {
+        rstd = rstd_of(sum, (float)p.cols, p.eps);
+        if (WPR > 1) __syncthreads();  // as many barriers as in the other case
+    }
+    if (t == 0 && row_ok && p.rstd) p.rstd[row] = rstd;
+    float y[NV][8], amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int64_t c = t + (int64_t)j * TPR;
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = 0.0f;
+        if (8 * c < cols) load_weight(p.w, p.w32, c, cols, w);
+        unpack(h[j], y[j]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) y[j][i] = y[j][i] * rstd * w[i];
+        if (p.y && 8 * c < cols) store_chunk(p.y + row * p.ld_y, c, cols, pack(y[j]));
+        if (SC == FP8Q_NORM_NONE) continue;
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(y[j][i]));
+        if (SC == FP8Q_NORM_ROW) {
+            amax = fmaxf(amax, m);
+            continue;
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));  // 16 lanes have a block
+        const float s = scale_from_amax<FMT>(m), sm = s * Fmt<FMT>::mult;
+        if (8 * c < cols) {
+            if ((t & 15) == 0) p.scales[c / 16 * p.ld_s + row] = 1.0f / s;
+            store_bytes(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
+                        enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
+        }
+    }
+    if (SC != FP8Q_NORM_ROW) return;
+    const float s = scale_from_amax<FMT>(across<WPR, false>(amax, red[2])), sm = s * Fmt<FMT>::mult;
+    if (t == 0 && row_ok) p.scales[row] = s;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int64_t c = t + (int64_t)j * TPR;
+        if (8 * c < cols)
+            store_bytes(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
+                        enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
+    }
+}
+
+template <int SC, int FMT, int WPR, int NV>
+static void launch_norm(const NormArgs& p, hipStream_t stream) {
+    constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR;
+    norm_kernel<SC, FMT, WPR, NV><<<dim3((unsigned)((p.rows + RPB - 1) / RPB)), dim3(64 * WAVES), 0, stream>>>(p);
+}
+
+template <int FMT>
+__global__ void norm_generic_kernel(const NormArgs p);
+
+template <int SC, int FMT>
+static void pick_norm(const NormArgs& p, hipStream_t stream) {
+    if (p.cols < 8) norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
+    else if (p.rows <= 256 && p.cols > 1024 && p.cols <= 8192) launch_norm<SC, FMT, 16, 1>(p, stream);
+    else if (p.cols <= 512) launch_norm<SC, FMT, 1, 1>(p, stream);
+    else if (p.cols <= 1024) launch_norm<SC, FMT, 1, 2>(p, stream);
+    else if (p.cols <= 2048) launch_norm<SC, FMT, 1, 4>(p, stream);
+    else if (p.cols <= 4096) launch_norm<SC, FMT, 2, 4>(p, stream);
+    else if (p.cols <= 8192) launch_norm<SC, FMT, 4, 4>(p, stream);
+    else if (p.cols <= 16384) launch_norm<SC, FMT, 8, 4>(p, stream);
+    else if (p.cols <= 32768) launch_norm<SC, FMT, 16, 4>(p, stream);
+    else norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
+}
+
+// Rows longer than registers hold, or shorter than a vector: a block of 4 waves per row, a wave takes blocks of 128 columns in turn, a lane
 // two of each; the row is read again (from cache) for the maximum and for the bytes.  A thread reads
 // only what it wrote of h, so h may be x or the residual.
 template <int FMT>
@@ -165,7 +370,132 @@ __device__ __forceinline__ float grad_at(const void* g, int64_t i) {
     return G32 ? static_cast<const float*>(g)[i] : bf16_f(static_cast<const uint16_t*>(g)[i]);
 }
 
-// Any size and alignment: blocks take rows in turn, a thread the same columns of each; its columns' sums
+// Rows held in registers: WPR waves a row, NV chunks of 8 columns a lane, the same ones of each of its rows,
+// whose sums for dw it keeps; the rows of a block's waves are added at the end.
+template <bool G32>
+struct Grads {  // eight gradients
+    uint4 v[G32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* g, int64_t at, int64_t c, int64_t cols) {
+        if (G32) {
+            float f[8];
+            load_floats(static_cast<const float*>(g) + at, c, cols, f);
+            v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            v[G32 ? 1 : 0] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+        } else {
+            v[0] = load_chunk(static_cast<const uint16_t*>(g) + at, c, cols);
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        if (G32) {
+            const uint4 a = v[0], b = v[G32 ? 1 : 0];
+            f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+            f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+        } else {
+            unpack(v[0], f);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < (G32 ? 2 : 1); i++) v[i] = make_uint4(0, 0, 0, 0);
+    }
+};
+__device__ __forceinline__ void store_floats(float* row, int64_t c, int64_t cols, const float (&f)[8]) {
+    if (8 * c + 8 <= cols) {
+        *reinterpret_cast<f32x4_any*>(row + 8 * c) = f32x4_any{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f32x4_any*>(row + 8 * c + 4) = f32x4_any{f[4], f[5], f[6], f[7]};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+        if (8 * c + i < cols) row[8 * c + i] = f[i];
+}
+
+template <bool G32, int WPR, int NV>
+__global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_back_kernel(const NormBackArgs p) {
+    constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR, TPR = 64 * WPR;
+    __shared__ float red[2][WAVES];
+    __shared__ float sums[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * 8 : 1];
+    const int wave = threadIdx.x >> 6, t = threadIdx.x % TPR, mine = wave / WPR;
+    float acc[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[j][i] = 0.0f;
+    int turn = 0;
+    // the rows of a block stay together, for its barriers
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
+        const int64_t r = r0 + mine;
+        const bool row_ok = r < p.rows;
+        const int64_t row = row_ok ? r : p.rows - 1, cols = row_ok ? p.cols : 0;
+        uint4 h[NV];
+        Grads<G32> dy[NV], dh[NV];
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int64_t c = t + (int64_t)j * TPR;
+            h[j] = make_uint4(0, 0, 0, 0);
+            dy[j].clear();
+            dh[j].clear();
+            if (8 * c < cols) {
+                h[j] = load_chunk(p.h + row * p.ld_h, c, cols);
+                dy[j].load(p.dy, row * p.ld_dy, c, cols);
+                if (p.dh) dh[j].load(p.dh, row * p.ld_dh, c, cols);
+            }
+        }
+        const float rstd = p.rstd[row];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int64_t c = t + (int64_t)j * TPR;
+            float w[8], x[8], g[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = 0.0f;
+            if (8 * c < cols) load_weight(p.w, p.w32, c, cols, w);
+            unpack(h[j], x);
+            dy[j].get(g);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float xh = x[i] * rstd;
+                sum += g[i] * w[i] * xh;
+                acc[j][i] += g[i] * xh;
+            }
+        }
+        const float mean = across<WPR, true>(sum, red[turn]) / (float)p.cols;
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int64_t c = t + (int64_t)j * TPR;
+            if (8 * c >= cols) continue;
+            float w[8], x[8], g[8], e[8];
+            load_weight(p.w, p.w32, c, cols, w);
+            unpack(h[j], x);
+            dy[j].get(g);
+            dh[j].get(e);
+#pragma unroll
+            for (int i = 0; i < 8; i++) e[i] += rstd * (g[i] * w[i] - (x[i] * rstd) * mean);
+            if (G32) store_floats(static_cast<float*>(p.dx) + row * p.ld_dx, c, cols, e);
+            else store_chunk(static_cast<uint16_t*>(p.dx) + row * p.ld_dx, c, cols, pack(e));
+        }
+    }
+    float* part = p.part + (int64_t)blockIdx.x * p.cols;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int64_t c = t + (int64_t)j * TPR;
+        if (RPB > 1) {
+            __syncthreads();
+            if (mine > 0)
+#pragma unroll
+                for (int i = 0; i < 8; i++) sums[mine - 1][i * TPR + t] = acc[j][i];
+            __syncthreads();
+            if (mine == 0)
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+#pragma unroll
+                    for (int k = 0; k < RPB - 1; k++) acc[j][i] += sums[k][i * TPR + t];
+        }
+        if (mine == 0 && 8 * c < p.cols) store_floats(part, c, p.cols, acc[j]);
+    }
+}
+
+// Rows longer than registers hold, or shorter than a vector: blocks take rows in turn, a thread the same columns of each; its columns' sums
 // for dw are kept in the block's own piece of the workspace.
 template <bool G32>
 __global__ __launch_bounds__(256) void norm_back_generic_kernel(const NormBackArgs p) {
@@ -191,21 +521,35 @@ __global__ __launch_bounds__(256) void norm_back_generic_kernel(const NormBackAr
     }
 }
 
-// dw from the blocks' sums: a block takes 32 columns, 8 threads a column's parts in turn.
-__global__ __launch_bounds__(256) void norm_back_join_kernel(const float* part, int parts, int64_t cols, float* dw) {
-    __shared__ float red[8][32];
+// dw from the blocks' sums: a block takes 32 columns, 32 threads a column's parts in turn.
+__global__ __launch_bounds__(1024) void norm_back_join_kernel(const float* part, int parts, int64_t cols, float* dw) {
+    __shared__ float red[32][33];
     const int i = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + i;
     float s = 0.0f;
-    if (c < cols)
-        for (int b = k; b < parts; b += 8) s += part[(int64_t)b * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int b = k; b < parts; b += 32) s += part[(int64_t)b * cols + c];
+    }
     red[k][i] = s;
     __syncthreads();
     if (k == 0 && c < cols) {
 #pragma unroll
-        for (int j = 1; j < 8; j++) s += red[j][i];
+        for (int j = 1; j < 32; j++) s += red[j][i];
         dw[c] = s;
     }
+}
+
+template <bool G32>
+static void pick_norm_back(const NormBackArgs& p, unsigned blocks, hipStream_t stream) {
+    const dim3 grid(blocks);
+    if (p.cols < 8 || p.cols > 16384) norm_back_generic_kernel<G32><<<grid, dim3(256), 0, stream>>>(p);
+    else if (p.cols <= 512) norm_back_kernel<G32, 1, 1><<<grid, dim3(256), 0, stream>>>(p);
+    else if (p.cols <= 1024) norm_back_kernel<G32, 2, 1><<<grid, dim3(256), 0, stream>>>(p);
+    else if (p.cols <= 2048) norm_back_kernel<G32, 4, 1><<<grid, dim3(256), 0, stream>>>(p);
+    else if (p.cols <= 4096) norm_back_kernel<G32, 4, 2><<<grid, dim3(256), 0, stream>>>(p);
+    else if (p.cols <= 8192) norm_back_kernel<G32, 4, 4><<<grid, dim3(256), 0, stream>>>(p);
+    else norm_back_kernel<G32, 8, 4><<<grid, dim3(512), 0, stream>>>(p);
 }
 
 static inline int64_t norm_back_parts(int64_t rows) { return rows < 512 ? rows : 512; }
@@ -233,11 +577,13 @@ extern "C" fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t c
     if (h && ((h == x && ld_h != ld_x) || (h == residual && ld_h != ld_res))) return FP8Q_ERR_INVALID_ARG;
     if (rows > 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
     NormArgs p{};
-    p.x = x; p.cols = cols; p.ld_x = ld_x; p.residual = residual; p.ld_res = ld_res; p.w = weight; p.h = h; p.ld_h = ld_h;
+    p.x = x; p.rows = rows; p.cols = cols; p.ld_x = ld_x; p.residual = residual; p.ld_res = ld_res; p.w = weight; p.h = h; p.ld_h = ld_h;
     p.y = y; p.ld_y = ld_y; p.q = q; p.ld_q = ld_q; p.scales = scales; p.ld_s = ld_s; p.rstd = rstd; p.eps = eps;
     p.w32 = weight_dtype == FP8Q_OUT_FP32; p.scaling = scaling;
-    if (fmt == FP8Q_E4M3FN) norm_generic_kernel<FP8Q_E4M3FN><<<dim3((unsigned)rows), dim3(256), 0, stream>>>(p);
-    else norm_generic_kernel<FP8Q_E4M3FNUZ><<<dim3((unsigned)rows), dim3(256), 0, stream>>>(p);
+    if (scaling == FP8Q_NORM_NONE) pick_norm<FP8Q_NORM_NONE, FP8Q_E4M3FN>(p, stream);
+    else if (scaling == FP8Q_NORM_BLOCK) pick_norm<FP8Q_NORM_BLOCK, FP8Q_E4M3FN>(p, stream);
+    else if (fmt == FP8Q_E4M3FN) pick_norm<FP8Q_NORM_ROW, FP8Q_E4M3FN>(p, stream);
+    else pick_norm<FP8Q_NORM_ROW, FP8Q_E4M3FNUZ>(p, stream);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
@@ -268,11 +614,11 @@ extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, co
     p.w32 = weight_dtype == FP8Q_OUT_FP32;
     const int64_t parts = norm_back_parts(rows);
     if (rows > 0) {
-        if (grad_dtype == FP8Q_OUT_FP32) norm_back_generic_kernel<true><<<dim3((unsigned)parts), dim3(256), 0, stream>>>(p);
-        else norm_back_generic_kernel<false><<<dim3((unsigned)parts), dim3(256), 0, stream>>>(p);
+        if (grad_dtype == FP8Q_OUT_FP32) pick_norm_back<true>(p, (unsigned)parts, stream);
+        else pick_norm_back<false>(p, (unsigned)parts, stream);
         FP8Q_CHECK_LAUNCH();
     }
-    norm_back_join_kernel<<<dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, stream>>>(p.part, (int)parts, cols, dweight);
+    norm_back_join_kernel<<<dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream>>>(p.part, (int)parts, cols, dweight);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
