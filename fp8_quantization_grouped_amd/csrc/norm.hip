@@ -64,52 +64,66 @@ __device__ __forceinline__ float rstd_of(float sum, float cols, float eps) { ret
 // Where the sum of squares has overflowed: from the squares' sum of h * 2^-80; eps is far below them.
 __device__ __forceinline__ float rstd_of_shrunk(float sum, float cols) { return kShrink / sqrtf(sum / cols); }
 
-// Eight consecutive elements from 8 c on of a row of 8 or more, zeros past its end.  A wide access need not
-// be aligned here.  A chunk that the row's end cuts is read as the row's last eight, which stay inside it
-// in one access, and moved down: reading it by elements costs the loop 7 registers for every such load.
+// Eight consecutive elements from 8 c on of a row of 8 or more, zeros past its end.  WIDE: rows are whole
+// chunks that start on 16 bytes; else a wide access need not be aligned, and a chunk that the row's end cuts
+// is read as the row's last eight, which stay inside it in one access, and moved down: reading it by elements
+// costs the loop 7 registers for every such load.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int64_t c, int64_t cols) {
-    const int64_t over = 8 * c + 8 - cols;
+template <bool WIDE>
+__device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int c, int cols) {
+    if (WIDE) return *reinterpret_cast<const uint4*>(row + 8 * c);
+    const int over = 8 * c + 8 - cols;
     const u32x4_any v = *reinterpret_cast<const u32x4_any*>(row + 8 * c - (over > 0 ? over : 0));
     if (over <= 0) return make_uint4(v.x, v.y, v.z, v.w);
     uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
-    const int k = 16 * (int)over;  // bits, under 128
-    lo = k >= 64 ? hi >> (k - 64) : k ? lo >> k | hi << (64 - k) : lo;
+    const int k = 16 * over;  // bits, under 128
+    lo = k >= 64 ? hi >> (k - 64) : lo >> k | hi << (64 - k);
     hi = k >= 64 ? 0 : hi >> k;
     return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
 }
-__device__ __forceinline__ void store_chunk(uint16_t* row, int64_t c, int64_t cols, uint4 v) {
-    if (8 * c + 8 <= cols) {
+template <bool WIDE>
+__device__ __forceinline__ void store_chunk(uint16_t* row, int c, int cols, uint4 v) {
+    if (WIDE) {
+        *reinterpret_cast<uint4*>(row + 8 * c) = v;
+    } else if (8 * c + 8 <= cols) {
         *reinterpret_cast<u32x4_any*>(row + 8 * c) = u32x4_any{v.x, v.y, v.z, v.w};
-        return;
-    }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 7; i++)
-        if (8 * c + i < cols) row[8 * c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < 7; i++)
+            if (8 * c + i < cols) row[8 * c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
 }
-__device__ __forceinline__ void store_bytes(uint8_t* row, int64_t c, int64_t cols, uint32_t a, uint32_t b) {
-    if (8 * c + 8 <= cols) {
+template <bool WIDE>
+__device__ __forceinline__ void store_bytes(uint8_t* row, int c, int cols, uint32_t a, uint32_t b) {
+    if (WIDE) {
+        *reinterpret_cast<uint2*>(row + 8 * c) = make_uint2(a, b);
+    } else if (8 * c + 8 <= cols) {
         *reinterpret_cast<u32x2_any*>(row + 8 * c) = u32x2_any{a, b};
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 7; i++)
-        if (8 * c + i < cols) row[8 * c + i] = (uint8_t)((i < 4 ? a : b) >> (8 * (i & 3)));
+        for (int i = 0; i < 7; i++)
+            if (8 * c + i < cols) row[8 * c + i] = (uint8_t)((i < 4 ? a : b) >> (8 * (i & 3)));
+    }
 }
 __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) { return (uint32_t)bf16_rn(a) | (uint32_t)bf16_rn(b) << 16; }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {  // to the nearest, ties to even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
 __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
-__device__ __forceinline__ void load_floats(const float* row, int64_t c, int64_t cols, float (&f)[8]) {
-    const int64_t over = 8 * c + 8 - cols;
+template <bool WIDE>
+__device__ __forceinline__ void load_floats(const float* row, int c, int cols, float (&f)[8]) {
+    const int over = WIDE ? 0 : 8 * c + 8 - cols;
     const float* p = row + 8 * c - (over > 0 ? over : 0);
     const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -120,9 +134,21 @@ __device__ __forceinline__ void load_floats(const float* row, int64_t c, int64_t
             for (int i = 0; i < 8; i++) f[i] = over & k ? (i + k < 8 ? f[i + k] : 0.0f) : f[i];
     }
 }
-__device__ __forceinline__ void load_weight(const void* w, bool w32, int64_t c, int64_t cols, float (&f)[8]) {
-    if (w32) load_floats(static_cast<const float*>(w), c, cols, f);
-    else unpack(load_chunk(static_cast<const uint16_t*>(w), c, cols), f);
+template <bool WIDE>
+__device__ __forceinline__ void store_floats(float* row, int c, int cols, const float (&f)[8]) {
+    if (WIDE || 8 * c + 8 <= cols) {
+        *reinterpret_cast<f32x4_any*>(row + 8 * c) = f32x4_any{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f32x4_any*>(row + 8 * c + 4) = f32x4_any{f[4], f[5], f[6], f[7]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; i++)
+            if (8 * c + i < cols) row[8 * c + i] = f[i];
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void load_weight(const void* w, bool w32, int c, int cols, float (&f)[8]) {
+    if (w32) load_floats<WIDE>(static_cast<const float*>(w), c, cols, f);
+    else unpack(load_chunk<WIDE>(static_cast<const uint16_t*>(w), c, cols), f);
 }
 
 // Block b of n in an order that gives each XCD (blocks go to the 8 of them in turn) one run of rows: what
@@ -151,29 +177,34 @@ __device__ __forceinline__ float across(float v, float* red) {
 }
 
 // Rows held in registers: WPR waves a row, NV chunks of 8 elements a lane.
-template <int SC, int FMT, int WPR, int NV>
+template <int SC, int FMT, int WPR, int NV, bool WIDE>
 __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const NormArgs p) {
     constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR, TPR = 64 * WPR;
     __shared__ float red[3][WAVES];
-    const int wave = threadIdx.x >> 6, t = threadIdx.x % TPR;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), t = threadIdx.x % TPR;
     const int64_t group = SC == FP8Q_NORM_BLOCK ? xcd_run(blockIdx.x, gridDim.x) : (int64_t)blockIdx.x;
     const int64_t r = group * RPB + wave / WPR;
     const bool row_ok = r < p.rows;
-    const int64_t row = row_ok ? r : p.rows - 1, cols = row_ok ? p.cols : 0;  // no columns of a row past the last
+    const int64_t row = row_ok ? r : p.rows - 1;
+    const int cols = row_ok ? (int)p.cols : 0;  // no columns of a row past the last
+    const uint16_t* x = p.x + row * p.ld_x;
     uint4 h[NV], res[NV];
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        const int64_t c = t + (int64_t)j * TPR;
+        const int c = t + j * TPR;
         h[j] = res[j] = make_uint4(0, 0, 0, 0);
-        if (8 * c < cols) {
-            h[j] = load_chunk(p.x + row * p.ld_x, c, cols);
-            if (p.residual) res[j] = load_chunk(p.residual + row * p.ld_res, c, cols);
-        }
+        if (8 * c < cols) h[j] = load_chunk<WIDE>(x, c, cols);
+    }
+    if (p.residual) {
+        const uint16_t* from = p.residual + row * p.ld_res;
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            if (8 * (t + j * TPR) < cols) res[j] = load_chunk<WIDE>(from, t + j * TPR, cols);
     }
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        const int64_t c = t + (int64_t)j * TPR;
+        const int c = t + j * TPR;
         float f[8];
         unpack(h[j], f);
         if (p.residual) {
@@ -183,7 +214,7 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
             for (int i = 0; i < 8; i++) f[i] += g[i];
             h[j] = pack(f);
             unpack(h[j], f);
-            if (8 * c < cols) store_chunk(p.h + row * p.ld_h, c, cols, h[j]);
+            if (8 * c < cols) store_chunk<WIDE>(p.h + row * p.ld_h, c, cols, h[j]);
         }
 #pragma unroll
         for (int i = 0; i < 8; i++) sum += f[i] * f[i];
@@ -208,15 +239,15 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
     float y[NV][8], amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        const int64_t c = t + (int64_t)j * TPR;
+        const int c = t + j * TPR;
         float w[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = 0.0f;
-        if (8 * c < cols) load_weight(p.w, p.w32, c, cols, w);
+        if (8 * c < cols) load_weight<WIDE>(p.w, p.w32, c, cols, w);
         unpack(h[j], y[j]);
 #pragma unroll
         for (int i = 0; i < 8; i++) y[j][i] = y[j][i] * rstd * w[i];
-        if (p.y && 8 * c < cols) store_chunk(p.y + row * p.ld_y, c, cols, pack(y[j]));
+        if (p.y && 8 * c < cols) store_chunk<WIDE>(p.y + row * p.ld_y, c, cols, pack(y[j]));
         if (SC == FP8Q_NORM_NONE) continue;
         float m = 0.0f;
 #pragma unroll
@@ -230,8 +261,8 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
         const float s = scale_from_amax<FMT>(m), sm = s * Fmt<FMT>::mult;
         if (8 * c < cols) {
             if ((t & 15) == 0) p.scales[c / 16 * p.ld_s + row] = 1.0f / s;
-            store_bytes(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
-                        enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
+            store_bytes<WIDE>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
+                              enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
         }
     }
     if (SC != FP8Q_NORM_ROW) return;
@@ -239,33 +270,41 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
     if (t == 0 && row_ok) p.scales[row] = s;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        const int64_t c = t + (int64_t)j * TPR;
+        const int c = t + j * TPR;
         if (8 * c < cols)
-            store_bytes(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
-                        enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
+            store_bytes<WIDE>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
+                              enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
     }
 }
 
 template <int SC, int FMT, int WPR, int NV>
-static void launch_norm(const NormArgs& p, hipStream_t stream) {
+static void launch_norm(const NormArgs& p, bool wide, hipStream_t stream) {
     constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR;
-    norm_kernel<SC, FMT, WPR, NV><<<dim3((unsigned)((p.rows + RPB - 1) / RPB)), dim3(64 * WAVES), 0, stream>>>(p);
+    const dim3 grid((unsigned)((p.rows + RPB - 1) / RPB)), block(64 * WAVES);
+    if (wide) norm_kernel<SC, FMT, WPR, NV, true><<<grid, block, 0, stream>>>(p);
+    else norm_kernel<SC, FMT, WPR, NV, false><<<grid, block, 0, stream>>>(p);
 }
+
+// Rows that start on whole vectors of 8 elements; none where there is no matrix.
+static inline bool fp8q_rows_wide(const void* p, int64_t ld, uintptr_t align) { return !p || (ld % 8 == 0 && fp8q_aligned(p, align)); }
 
 template <int FMT>
 __global__ void norm_generic_kernel(const NormArgs p);
 
 template <int SC, int FMT>
 static void pick_norm(const NormArgs& p, hipStream_t stream) {
+    const bool wide = p.cols % 8 == 0 && fp8q_rows_wide(p.x, p.ld_x, 16) && fp8q_rows_wide(p.residual, p.ld_res, 16) &&
+                      fp8q_rows_wide(p.h, p.ld_h, 16) && fp8q_rows_wide(p.y, p.ld_y, 16) && fp8q_rows_wide(p.q, p.ld_q, 8) &&
+                      fp8q_aligned(p.w, 16);
     if (p.cols < 8) norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
-    else if (p.rows <= 256 && p.cols > 1024 && p.cols <= 8192) launch_norm<SC, FMT, 16, 1>(p, stream);
-    else if (p.cols <= 512) launch_norm<SC, FMT, 1, 1>(p, stream);
-    else if (p.cols <= 1024) launch_norm<SC, FMT, 1, 2>(p, stream);
-    else if (p.cols <= 2048) launch_norm<SC, FMT, 1, 4>(p, stream);
-    else if (p.cols <= 4096) launch_norm<SC, FMT, 2, 4>(p, stream);
-    else if (p.cols <= 8192) launch_norm<SC, FMT, 4, 4>(p, stream);
-    else if (p.cols <= 16384) launch_norm<SC, FMT, 8, 4>(p, stream);
-    else if (p.cols <= 32768) launch_norm<SC, FMT, 16, 4>(p, stream);
+    else if (p.rows <= 256 && p.cols > 1024 && p.cols <= 8192) launch_norm<SC, FMT, 16, 1>(p, wide, stream);
+    else if (p.cols <= 512) launch_norm<SC, FMT, 1, 1>(p, wide, stream);
+    else if (p.cols <= 1024) launch_norm<SC, FMT, 1, 2>(p, wide, stream);
+    else if (p.cols <= 2048) launch_norm<SC, FMT, 1, 4>(p, wide, stream);
+    else if (p.cols <= 4096) launch_norm<SC, FMT, 2, 4>(p, wide, stream);
+    else if (p.cols <= 8192) launch_norm<SC, FMT, 4, 4>(p, wide, stream);
+    else if (p.cols <= 16384) launch_norm<SC, FMT, 8, 4>(p, wide, stream);
+    else if (p.cols <= 32768) launch_norm<SC, FMT, 16, 4>(p, wide, stream);
     else norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
 }
 
@@ -362,6 +401,7 @@ struct NormBackArgs {
     void* dx;
     int64_t ld_dx;
     float* part;   // [blocks][cols] sums of dy xh
+    int waves;     // of a row
     bool w32;
 };
 
@@ -370,19 +410,17 @@ __device__ __forceinline__ float grad_at(const void* g, int64_t i) {
     return G32 ? static_cast<const float*>(g)[i] : bf16_f(static_cast<const uint16_t*>(g)[i]);
 }
 
-// Rows held in registers: WPR waves a row, NV chunks of 8 columns a lane, the same ones of each of its rows,
-// whose sums for dw it keeps; the rows of a block's waves are added at the end.
-template <bool G32>
+template <bool G32, bool WIDE>
 struct Grads {  // eight gradients
     uint4 v[G32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void* g, int64_t at, int64_t c, int64_t cols) {
+    __device__ __forceinline__ void load(const void* g, int64_t at, int c, int cols) {
         if (G32) {
             float f[8];
-            load_floats(static_cast<const float*>(g) + at, c, cols, f);
+            load_floats<WIDE>(static_cast<const float*>(g) + at, c, cols, f);
             v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
             v[G32 ? 1 : 0] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
         } else {
-            v[0] = load_chunk(static_cast<const uint16_t*>(g) + at, c, cols);
+            v[0] = load_chunk<WIDE>(static_cast<const uint16_t*>(g) + at, c, cols);
         }
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -394,104 +432,113 @@ struct Grads {  // eight gradients
             unpack(v[0], f);
         }
     }
-    __device__ __forceinline__ void clear() {
+};
+
+// What a lane has of a row.
+template <bool G32, int NV, bool WIDE>
+struct BackRow {
+    uint4 h[NV];
+    Grads<G32, WIDE> dy[NV], dh[NV];
+    float rstd;
+    __device__ __forceinline__ void load(const NormBackArgs& p, int64_t row, int t, int tpr) {
+        const bool ok = row < p.rows;
+        const int cols = ok ? (int)p.cols : 0;
+        rstd = ok ? p.rstd[row] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < (G32 ? 2 : 1); i++) v[i] = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < NV; j++) {
+            const int c = t + j * tpr;
+            h[j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < (G32 ? 2 : 1); i++) dy[j].v[i] = dh[j].v[i] = make_uint4(0, 0, 0, 0);
+            if (8 * c < cols) {
+                h[j] = load_chunk<WIDE>(p.h + row * p.ld_h, c, cols);
+                dy[j].load(p.dy, row * p.ld_dy, c, cols);
+                if (p.dh) dh[j].load(p.dh, row * p.ld_dh, c, cols);
+            }
+        }
     }
 };
-__device__ __forceinline__ void store_floats(float* row, int64_t c, int64_t cols, const float (&f)[8]) {
-    if (8 * c + 8 <= cols) {
-        *reinterpret_cast<f32x4_any*>(row + 8 * c) = f32x4_any{f[0], f[1], f[2], f[3]};
-        *reinterpret_cast<f32x4_any*>(row + 8 * c + 4) = f32x4_any{f[4], f[5], f[6], f[7]};
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 7; i++)
-        if (8 * c + i < cols) row[8 * c + i] = f[i];
-}
 
-template <bool G32, int WPR, int NV>
-__global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_back_kernel(const NormBackArgs p) {
-    constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR, TPR = 64 * WPR;
-    __shared__ float red[2][WAVES];
-    __shared__ float sums[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * 8 : 1];
-    const int wave = threadIdx.x >> 6, t = threadIdx.x % TPR, mine = wave / WPR;
+// Rows held in registers: p.waves waves a row, NV chunks of 8 columns a lane, the same ones of each of its
+// rows, whose sums for dw it keeps; a row's loads go out while the one before it is worked on.  The rows of a
+// block's waves are added at the end.
+template <bool G32, int NV, bool WIDE>
+__global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
+    __shared__ float red[2][16];
+    extern __shared__ float sums[];  // [rows of a block less one][8][threads of a row]
+    const int waves = p.waves, tpr = 64 * waves, rpb = blockDim.x / tpr;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), mine = wave / waves, t = threadIdx.x - mine * tpr;
     float acc[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; j++)
 #pragma unroll
         for (int i = 0; i < 8; i++) acc[j][i] = 0.0f;
-    int turn = 0;
-    // the rows of a block stay together, for its barriers
-    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
-        const int64_t r = r0 + mine;
-        const bool row_ok = r < p.rows;
-        const int64_t row = row_ok ? r : p.rows - 1, cols = row_ok ? p.cols : 0;
-        uint4 h[NV];
-        Grads<G32> dy[NV], dh[NV];
+    BackRow<G32, NV, WIDE> cur, next;
+    int64_t r0 = (int64_t)blockIdx.x * rpb;
+    cur.load(p, r0 + mine, t, tpr);
+    const float inv_cols = 1.0f / (float)p.cols;
+    for (int turn = 0; r0 < p.rows; turn ^= 1) {  // the rows of a block stay together, for its barriers
+        const int64_t row = r0 + mine;
+        r0 += (int64_t)gridDim.x * rpb;
+        next.load(p, r0 + mine, t, tpr);
+        float w[NV][8], sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            const int64_t c = t + (int64_t)j * TPR;
-            h[j] = make_uint4(0, 0, 0, 0);
-            dy[j].clear();
-            dh[j].clear();
-            if (8 * c < cols) {
-                h[j] = load_chunk(p.h + row * p.ld_h, c, cols);
-                dy[j].load(p.dy, row * p.ld_dy, c, cols);
-                if (p.dh) dh[j].load(p.dh, row * p.ld_dh, c, cols);
-            }
-        }
-        const float rstd = p.rstd[row];
-        float sum = 0.0f;
+            const int c = t + j * tpr;
+            float x[8], g[8];
 #pragma unroll
-        for (int j = 0; j < NV; j++) {
-            const int64_t c = t + (int64_t)j * TPR;
-            float w[8], x[8], g[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) w[i] = 0.0f;
-            if (8 * c < cols) load_weight(p.w, p.w32, c, cols, w);
-            unpack(h[j], x);
-            dy[j].get(g);
+            for (int i = 0; i < 8; i++) w[j][i] = 0.0f;
+            if (8 * c < p.cols) load_weight<WIDE>(p.w, p.w32, c, (int)p.cols, w[j]);
+            unpack(cur.h[j], x);
+            cur.dy[j].get(g);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float xh = x[i] * rstd;
-                sum += g[i] * w[i] * xh;
+                const float xh = x[i] * cur.rstd;
+                sum += g[i] * w[j][i] * xh;
                 acc[j][i] += g[i] * xh;
             }
         }
-        const float mean = across<WPR, true>(sum, red[turn]) / (float)p.cols;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        if (waves > 1) {
+            if ((threadIdx.x & 63) == 0) red[turn][wave] = sum;
+            __syncthreads();
+            sum = 0.0f;
+            for (int i = 0; i < waves; i++) sum += red[turn][mine * waves + i];
+        }
+        const float mean = sum * inv_cols;
+        const int cols = row < p.rows ? (int)p.cols : 0;
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            const int64_t c = t + (int64_t)j * TPR;
+            const int c = t + j * tpr;
             if (8 * c >= cols) continue;
-            float w[8], x[8], g[8], e[8];
-            load_weight(p.w, p.w32, c, cols, w);
-            unpack(h[j], x);
-            dy[j].get(g);
-            dh[j].get(e);
+            float x[8], g[8], e[8];
+            unpack(cur.h[j], x);
+            cur.dy[j].get(g);
+            cur.dh[j].get(e);
 #pragma unroll
-            for (int i = 0; i < 8; i++) e[i] += rstd * (g[i] * w[i] - (x[i] * rstd) * mean);
-            if (G32) store_floats(static_cast<float*>(p.dx) + row * p.ld_dx, c, cols, e);
-            else store_chunk(static_cast<uint16_t*>(p.dx) + row * p.ld_dx, c, cols, pack(e));
+            for (int i = 0; i < 8; i++) e[i] += cur.rstd * (g[i] * w[j][i] - (x[i] * cur.rstd) * mean);
+            if (G32) store_floats<WIDE>(static_cast<float*>(p.dx) + row * p.ld_dx, c, cols, e);
+            else store_chunk<WIDE>(static_cast<uint16_t*>(p.dx) + row * p.ld_dx, c, cols, pack(e));
         }
+        cur = next;
     }
     float* part = p.part + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        const int64_t c = t + (int64_t)j * TPR;
-        if (RPB > 1) {
+        const int c = t + j * tpr;
+        if (rpb > 1) {
             __syncthreads();
             if (mine > 0)
 #pragma unroll
-                for (int i = 0; i < 8; i++) sums[mine - 1][i * TPR + t] = acc[j][i];
+                for (int i = 0; i < 8; i++) sums[((mine - 1) * 8 + i) * tpr + t] = acc[j][i];
             __syncthreads();
             if (mine == 0)
+                for (int k = 0; k < rpb - 1; k++)
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-#pragma unroll
-                    for (int k = 0; k < RPB - 1; k++) acc[j][i] += sums[k][i * TPR + t];
+                    for (int i = 0; i < 8; i++) acc[j][i] += sums[(k * 8 + i) * tpr + t];
         }
-        if (mine == 0 && 8 * c < p.cols) store_floats(part, c, p.cols, acc[j]);
+        if (mine == 0 && 8 * c < p.cols) store_floats<WIDE>(part, c, (int)p.cols, acc[j]);
     }
 }
 
@@ -540,19 +587,36 @@ __global__ __launch_bounds__(1024) void norm_back_join_kernel(const float* part,
     }
 }
 
-template <bool G32>
-static void pick_norm_back(const NormBackArgs& p, unsigned blocks, hipStream_t stream) {
-    const dim3 grid(blocks);
-    if (p.cols < 8 || p.cols > 16384) norm_back_generic_kernel<G32><<<grid, dim3(256), 0, stream>>>(p);
-    else if (p.cols <= 512) norm_back_kernel<G32, 1, 1><<<grid, dim3(256), 0, stream>>>(p);
-    else if (p.cols <= 1024) norm_back_kernel<G32, 2, 1><<<grid, dim3(256), 0, stream>>>(p);
-    else if (p.cols <= 2048) norm_back_kernel<G32, 4, 1><<<grid, dim3(256), 0, stream>>>(p);
-    else if (p.cols <= 4096) norm_back_kernel<G32, 4, 2><<<grid, dim3(256), 0, stream>>>(p);
-    else if (p.cols <= 8192) norm_back_kernel<G32, 4, 4><<<grid, dim3(256), 0, stream>>>(p);
-    else norm_back_kernel<G32, 8, 4><<<grid, dim3(512), 0, stream>>>(p);
+// Waves of a row, chunks of a lane and rows of a block of at most 16 waves; chunks is 0 where registers do
+// not hold a row.
+struct NormBackPlan {
+    int waves, chunks, rows;
+    int64_t blocks;
+};
+static inline NormBackPlan norm_back_plan(int64_t rows, int64_t cols) {
+    NormBackPlan p{1, 0, 1, 0};
+    if (cols >= 8 && cols <= 16384) {
+        p.chunks = cols <= 8192 ? 1 : 2;
+        p.waves = (int)((cols + 512 * p.chunks - 1) / (512 * p.chunks));
+        p.rows = 16 / p.waves;
+    }
+    p.blocks = (rows + p.rows - 1) / p.rows;
+    p.blocks = p.blocks < 512 ? p.blocks : 512;
+    return p;
 }
 
-static inline int64_t norm_back_parts(int64_t rows) { return rows < 512 ? rows : 512; }
+template <bool G32>
+static void launch_norm_back(const NormBackArgs& p, const NormBackPlan& n, hipStream_t stream) {
+    const bool wide = p.cols % 8 == 0 && fp8q_rows_wide(p.h, p.ld_h, 16) && fp8q_rows_wide(p.dy, p.ld_dy, 16) &&
+                      fp8q_rows_wide(p.dh, p.ld_dh, 16) && fp8q_rows_wide(p.dx, p.ld_dx, 16) && fp8q_aligned(p.w, 16);
+    const dim3 grid((unsigned)n.blocks), block(64 * n.waves * n.rows);
+    const size_t lds = (size_t)(n.rows - 1) * 8 * 64 * n.waves * 4;
+    if (n.chunks == 0) norm_back_generic_kernel<G32><<<grid, dim3(256), 0, stream>>>(p);
+    else if (n.chunks == 1 && wide) norm_back_kernel<G32, 1, true><<<grid, block, lds, stream>>>(p);
+    else if (n.chunks == 1) norm_back_kernel<G32, 1, false><<<grid, block, lds, stream>>>(p);
+    else if (wide) norm_back_kernel<G32, 2, true><<<grid, block, lds, stream>>>(p);
+    else norm_back_kernel<G32, 2, false><<<grid, block, lds, stream>>>(p);
+}
 
 static inline bool dtype_ok(int d) { return d == FP8Q_OUT_BF16 || d == FP8Q_OUT_FP32; }
 
@@ -590,7 +654,7 @@ extern "C" fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t c
 
 extern "C" size_t fp8_rms_norm_backward_workspace_size(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0) return 256;
-    return (size_t)fp8q::norm_back_parts(rows) * (size_t)cols * 4;
+    return (size_t)fp8q::norm_back_plan(rows, cols).blocks * (size_t)cols * 4;
 }
 
 extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,
@@ -612,13 +676,14 @@ extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, co
     p.dy = dy; p.ld_dy = ld_dy; p.dh = dh; p.ld_dh = ld_dh; p.h = h; p.rows = rows; p.cols = cols; p.ld_h = ld_h;
     p.rstd = rstd; p.w = weight; p.dx = dx; p.ld_dx = ld_dx; p.part = static_cast<float*>(workspace);
     p.w32 = weight_dtype == FP8Q_OUT_FP32;
-    const int64_t parts = norm_back_parts(rows);
+    const NormBackPlan n = norm_back_plan(rows, cols);
+    p.waves = n.waves;
     if (rows > 0) {
-        if (grad_dtype == FP8Q_OUT_FP32) pick_norm_back<true>(p, (unsigned)parts, stream);
-        else pick_norm_back<false>(p, (unsigned)parts, stream);
+        if (grad_dtype == FP8Q_OUT_FP32) launch_norm_back<true>(p, n, stream);
+        else launch_norm_back<false>(p, n, stream);
         FP8Q_CHECK_LAUNCH();
     }
-    norm_back_join_kernel<<<dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream>>>(p.part, (int)parts, cols, dweight);
+    norm_back_join_kernel<<<dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream>>>(p.part, (int)n.blocks, cols, dweight);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
