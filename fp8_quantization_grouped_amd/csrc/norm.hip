@@ -67,19 +67,26 @@ __device__ __forceinline__ float rstd_of_shrunk(float sum, float cols) { return 
 // Eight consecutive elements from 8 c on of a row of 8 or more, zeros past its end.  WIDE: rows are whole
 // chunks that start on 16 bytes; else a wide access need not be aligned, and a chunk that the row's end cuts
 // is read as the row's last eight, which stay inside it in one access, and moved down: reading it by elements
-// costs the loop 7 registers for every such load.
+// costs the loop 7 registers for every such load.  20000 x 5457 in the backward: 322 us where it was moved at
+// the load, 271 us where it is used.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
+// load_chunk only reads; settle moves a cut chunk down, where it is used: the loads ahead of it stay in flight.
 template <bool WIDE>
 __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int c, int cols) {
     if (WIDE) return *reinterpret_cast<const uint4*>(row + 8 * c);
     const int over = 8 * c + 8 - cols;
     const u32x4_any v = *reinterpret_cast<const u32x4_any*>(row + 8 * c - (over > 0 ? over : 0));
-    if (over <= 0) return make_uint4(v.x, v.y, v.z, v.w);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool WIDE>
+__device__ __forceinline__ uint4 settle(uint4 v, int c, int cols) {
+    const int over = 8 * c + 8 - cols;
+    if (WIDE || over <= 0 || over >= 8) return v;
     uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
     const int k = 16 * over;  // bits, under 128
     lo = k >= 64 ? hi >> (k - 64) : lo >> k | hi << (64 - k);
@@ -127,12 +134,15 @@ __device__ __forceinline__ void load_floats(const float* row, int c, int cols, f
     const float* p = row + 8 * c - (over > 0 ? over : 0);
     const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    if (over > 0) {
+}
+template <bool WIDE>
+__device__ __forceinline__ void settle(float (&f)[8], int c, int cols) {
+    const int over = 8 * c + 8 - cols;
+    if (WIDE || over <= 0 || over >= 8) return;
 #pragma unroll
-        for (int k = 4; k > 0; k >>= 1)
+    for (int k = 4; k > 0; k >>= 1)
 #pragma unroll
-            for (int i = 0; i < 8; i++) f[i] = over & k ? (i + k < 8 ? f[i + k] : 0.0f) : f[i];
-    }
+        for (int i = 0; i < 8; i++) f[i] = over & k ? (i + k < 8 ? f[i + k] : 0.0f) : f[i];
 }
 template <bool WIDE>
 __device__ __forceinline__ void store_floats(float* row, int c, int cols, const float (&f)[8]) {
@@ -147,8 +157,12 @@ __device__ __forceinline__ void store_floats(float* row, int c, int cols, const 
 }
 template <bool WIDE>
 __device__ __forceinline__ void load_weight(const void* w, bool w32, int c, int cols, float (&f)[8]) {
-    if (w32) load_floats<WIDE>(static_cast<const float*>(w), c, cols, f);
-    else unpack(load_chunk<WIDE>(static_cast<const uint16_t*>(w), c, cols), f);
+    if (w32) {
+        load_floats<WIDE>(static_cast<const float*>(w), c, cols, f);
+        settle<WIDE>(f, c, cols);
+    } else {
+        unpack(settle<WIDE>(load_chunk<WIDE>(static_cast<const uint16_t*>(w), c, cols), c, cols), f);
+    }
 }
 
 // Block b of n in an order that gives each XCD (blocks go to the 8 of them in turn) one run of rows: what
@@ -206,10 +220,11 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
     for (int j = 0; j < NV; j++) {
         const int c = t + j * TPR;
         float f[8];
+        h[j] = settle<WIDE>(h[j], c, cols);
         unpack(h[j], f);
         if (p.residual) {
             float g[8];
-            unpack(res[j], g);
+            unpack(settle<WIDE>(res[j], c, cols), g);
 #pragma unroll
             for (int i = 0; i < 8; i++) f[i] += g[i];
             h[j] = pack(f);
@@ -411,7 +426,7 @@ __device__ __forceinline__ float grad_at(const void* g, int64_t i) {
 }
 
 template <bool G32, bool WIDE>
-struct Grads {  // eight gradients
+struct Eight {  // eight gradients or weights
     uint4 v[G32 ? 2 : 1];
     __device__ __forceinline__ void load(const void* g, int64_t at, int c, int cols) {
         if (G32) {
@@ -423,6 +438,10 @@ struct Grads {  // eight gradients
             v[0] = load_chunk<WIDE>(static_cast<const uint16_t*>(g) + at, c, cols);
         }
     }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < (G32 ? 2 : 1); i++) v[i] = make_uint4(0, 0, 0, 0);
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         if (G32) {
             const uint4 a = v[0], b = v[G32 ? 1 : 0];
@@ -432,13 +451,24 @@ struct Grads {  // eight gradients
             unpack(v[0], f);
         }
     }
+    __device__ __forceinline__ void settle_all(int c, int cols) {
+        if (G32) {
+            float f[8];
+            get(f);
+            settle<WIDE>(f, c, cols);
+            v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            v[G32 ? 1 : 0] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+        } else {
+            v[0] = settle<WIDE>(v[0], c, cols);
+        }
+    }
 };
 
 // What a lane has of a row.
 template <bool G32, int NV, bool WIDE>
 struct BackRow {
     uint4 h[NV];
-    Grads<G32, WIDE> dy[NV], dh[NV];
+    Eight<G32, WIDE> dy[NV];
     float rstd;
     __device__ __forceinline__ void load(const NormBackArgs& p, int64_t row, int t, int tpr) {
         const bool ok = row < p.rows;
@@ -448,12 +478,10 @@ struct BackRow {
         for (int j = 0; j < NV; j++) {
             const int c = t + j * tpr;
             h[j] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < (G32 ? 2 : 1); i++) dy[j].v[i] = dh[j].v[i] = make_uint4(0, 0, 0, 0);
+            dy[j].clear();
             if (8 * c < cols) {
                 h[j] = load_chunk<WIDE>(p.h + row * p.ld_h, c, cols);
                 dy[j].load(p.dy, row * p.ld_dy, c, cols);
-                if (p.dh) dh[j].load(p.dh, row * p.ld_dh, c, cols);
             }
         }
     }
@@ -462,7 +490,7 @@ struct BackRow {
 // Rows held in registers: p.waves waves a row, NV chunks of 8 columns a lane, the same ones of each of its
 // rows, whose sums for dw it keeps; a row's loads go out while the one before it is worked on.  The rows of a
 // block's waves are added at the end.
-template <bool G32, int NV, bool WIDE>
+template <bool G32, bool W32, int NV, bool WIDE>
 __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
     __shared__ float red[2][16];
     extern __shared__ float sums[];  // [rows of a block less one][8][threads of a row]
@@ -473,28 +501,43 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
     for (int j = 0; j < NV; j++)
 #pragma unroll
         for (int i = 0; i < 8; i++) acc[j][i] = 0.0f;
+    Eight<W32, WIDE> weight[NV];
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        const int c = t + j * tpr;
+        weight[j].clear();
+        if (8 * c < p.cols) weight[j].load(p.w, 0, c, (int)p.cols);
+        weight[j].settle_all(c, (int)p.cols);
+    }
     BackRow<G32, NV, WIDE> cur, next;
     int64_t r0 = (int64_t)blockIdx.x * rpb;
     cur.load(p, r0 + mine, t, tpr);
     const float inv_cols = 1.0f / (float)p.cols;
     for (int turn = 0; r0 < p.rows; turn ^= 1) {  // the rows of a block stay together, for its barriers
         const int64_t row = r0 + mine;
+        const int cols = row < p.rows ? (int)p.cols : 0;
+        Eight<G32, WIDE> dh[NV];  // used after the row's sum, so not a row ahead
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            dh[j].clear();
+            if (p.dh && 8 * (t + j * tpr) < cols) dh[j].load(p.dh, row * p.ld_dh, t + j * tpr, cols);
+        }
         r0 += (int64_t)gridDim.x * rpb;
         next.load(p, r0 + mine, t, tpr);
-        float w[NV][8], sum = 0.0f;
+        float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             const int c = t + j * tpr;
-            float x[8], g[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) w[j][i] = 0.0f;
-            if (8 * c < p.cols) load_weight<WIDE>(p.w, p.w32, c, (int)p.cols, w[j]);
+            float x[8], g[8], w[8];
+            weight[j].get(w);
+            cur.h[j] = settle<WIDE>(cur.h[j], c, (int)p.cols);
+            cur.dy[j].settle_all(c, (int)p.cols);
             unpack(cur.h[j], x);
             cur.dy[j].get(g);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const float xh = x[i] * cur.rstd;
-                sum += g[i] * w[j][i] * xh;
+                sum += g[i] * w[i] * xh;
                 acc[j][i] += g[i] * xh;
             }
         }
@@ -507,17 +550,18 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
             for (int i = 0; i < waves; i++) sum += red[turn][mine * waves + i];
         }
         const float mean = sum * inv_cols;
-        const int cols = row < p.rows ? (int)p.cols : 0;
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             const int c = t + j * tpr;
             if (8 * c >= cols) continue;
-            float x[8], g[8], e[8];
+            float x[8], g[8], e[8], w[8];
+            weight[j].get(w);
             unpack(cur.h[j], x);
             cur.dy[j].get(g);
-            cur.dh[j].get(e);
+            dh[j].settle_all(c, cols);
+            dh[j].get(e);
 #pragma unroll
-            for (int i = 0; i < 8; i++) e[i] += cur.rstd * (g[i] * w[j][i] - (x[i] * cur.rstd) * mean);
+            for (int i = 0; i < 8; i++) e[i] += cur.rstd * (g[i] * w[i] - (x[i] * cur.rstd) * mean);
             if (G32) store_floats<WIDE>(static_cast<float*>(p.dx) + row * p.ld_dx, c, cols, e);
             else store_chunk<WIDE>(static_cast<uint16_t*>(p.dx) + row * p.ld_dx, c, cols, pack(e));
         }
@@ -605,17 +649,17 @@ static inline NormBackPlan norm_back_plan(int64_t rows, int64_t cols) {
     return p;
 }
 
-template <bool G32>
+template <bool G32, bool W32>
 static void launch_norm_back(const NormBackArgs& p, const NormBackPlan& n, hipStream_t stream) {
     const bool wide = p.cols % 8 == 0 && fp8q_rows_wide(p.h, p.ld_h, 16) && fp8q_rows_wide(p.dy, p.ld_dy, 16) &&
                       fp8q_rows_wide(p.dh, p.ld_dh, 16) && fp8q_rows_wide(p.dx, p.ld_dx, 16) && fp8q_aligned(p.w, 16);
     const dim3 grid((unsigned)n.blocks), block(64 * n.waves * n.rows);
     const size_t lds = (size_t)(n.rows - 1) * 8 * 64 * n.waves * 4;
     if (n.chunks == 0) norm_back_generic_kernel<G32><<<grid, dim3(256), 0, stream>>>(p);
-    else if (n.chunks == 1 && wide) norm_back_kernel<G32, 1, true><<<grid, block, lds, stream>>>(p);
-    else if (n.chunks == 1) norm_back_kernel<G32, 1, false><<<grid, block, lds, stream>>>(p);
-    else if (wide) norm_back_kernel<G32, 2, true><<<grid, block, lds, stream>>>(p);
-    else norm_back_kernel<G32, 2, false><<<grid, block, lds, stream>>>(p);
+    else if (n.chunks == 1 && wide) norm_back_kernel<G32, W32, 1, true><<<grid, block, lds, stream>>>(p);
+    else if (n.chunks == 1) norm_back_kernel<G32, W32, 1, false><<<grid, block, lds, stream>>>(p);
+    else if (wide) norm_back_kernel<G32, W32, 2, true><<<grid, block, lds, stream>>>(p);
+    else norm_back_kernel<G32, W32, 2, false><<<grid, block, lds, stream>>>(p);
 }
 
 static inline bool dtype_ok(int d) { return d == FP8Q_OUT_BF16 || d == FP8Q_OUT_FP32; }
@@ -679,8 +723,11 @@ extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, co
     const NormBackPlan n = norm_back_plan(rows, cols);
     p.waves = n.waves;
     if (rows > 0) {
-        if (grad_dtype == FP8Q_OUT_FP32) launch_norm_back<true>(p, n, stream);
-        else launch_norm_back<false>(p, n, stream);
+        const bool g32 = grad_dtype == FP8Q_OUT_FP32;
+        if (g32 && p.w32) launch_norm_back<true, true>(p, n, stream);
+        else if (g32) launch_norm_back<true, false>(p, n, stream);
+        else if (p.w32) launch_norm_back<false, true>(p, n, stream);
+        else launch_norm_back<false, false>(p, n, stream);
         FP8Q_CHECK_LAUNCH();
     }
     norm_back_join_kernel<<<dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream>>>(p.part, (int)n.blocks, cols, dweight);
