@@ -33,24 +33,42 @@ struct RouteGradArgs {
 };
 
 __device__ __forceinline__ float rg_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ uint16_t rg_to_bf16(float f) {
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);  // NaN stays NaN
-    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+typedef __bf16 rg_bf16x2 __attribute__((ext_vector_type(2)));
+typedef float rg_f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t rg_pack(float a, float b) {  // to the nearest, ties to even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((rg_f32x2{a, b}), rg_bf16x2));
 }
 
-// Sums and maxima over the L lanes that share a row.
-template <int L>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+// The value of another lane of the 16 that a DPP operation reaches: 1 and 2 away, then mirrored in 8 and 16
+// (whose halves hold one value each by then).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+// Sum (SUM) or maximum over the L lanes that share a row, the same in all of them.
+template <int L, bool SUM>
+__device__ __forceinline__ float over_row(float v) {
+    const auto join = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+    if (L > 1) v = join(v, dpp<0xB1>(v));    // quad_perm 1 0 3 2
+    if (L > 2) v = join(v, dpp<0x4E>(v));    // quad_perm 2 3 0 1
+    if (L > 4) v = join(v, dpp<0x141>(v));   // row_half_mirror
+    if (L > 8) v = join(v, dpp<0x140>(v));   // row_mirror
+    if (L > 16) v = join(v, __shfl_xor(v, 16, 64));
+    if (L > 32) v = join(v, __shfl_xor(v, 32, 64));
     return v;
 }
 template <int L>
-__device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-    return v;
+__device__ __forceinline__ float row_sum(float v) { return over_row<L, true>(v); }
+template <int L>
+__device__ __forceinline__ float row_max(float v) { return over_row<L, false>(v); }
+
+// exp(x) for x <= 0 within two units: 2^(x log2(e)), the product's rounding made good to first order.
+// Results under 2^-126 are zero.
+__device__ __forceinline__ float exp_neg(float x) {
+    x = x < -200.0f ? -200.0f : x;  // a NaN stays
+    const float t = x * 1.44269504f, r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269504f, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, r * 0.693147181f, e);
 }
 
 // End of sequence s, inside [0, T] whatever is stored.
@@ -116,7 +134,7 @@ __device__ __forceinline__ void softmax_of(const float (&l)[N], float (&out)[N])
     m = m == -INFINITY ? 0.0f : m;  // every logit at minus infinity: no probabilities
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        out[i] = expf(l[i] - m);
+        out[i] = exp_neg(l[i] - m);
         sum += out[i];
     }
     sum = row_sum<L>(sum);
@@ -140,7 +158,7 @@ __device__ __forceinline__ void scores_of(bool sigmoid, const float (&l)[N], flo
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        const float u = expf(-fabsf(l[i])), one = 1.0f / (1.0f + u), rest = u * one;  // neither end overflows or cancels
+        const float u = exp_neg(-fabsf(l[i])), one = __builtin_amdgcn_rcpf(1.0f + u), rest = u * one;  // neither end overflows or cancels
         s[i] = l[i] > 0.0f ? one : rest;
         slope[i] = l[i] > 0.0f ? rest : one;
         sum += s[i];
@@ -207,138 +225,187 @@ __global__ __launch_bounds__(256) void balance_kernel(const RouteGradArgs p) {
     }
 }
 
-// A sequence's loss and counts from its chunks: a block per sequence, a thread an expert at a time.
-__global__ __launch_bounds__(256) void balance_join_kernel(const RouteGradArgs p) {
-    __shared__ float red[4];
-    const int s = blockIdx.x;
+// A sequence's loss and counts from its chunks: a block per sequence; C threads take an expert each, the
+// block's 1024 / C rows of them the chunks in turn.
+__global__ __launch_bounds__(1024) void balance_join_kernel(const RouteGradArgs p, int C) {
+    __shared__ float mass[1024], red[16];
+    __shared__ int32_t count[1024];
+    const int s = blockIdx.x, e = threadIdx.x & (C - 1), row = threadIdx.x / C, rows = 1024 / C;
     const int64_t a = s == 0 ? 0 : seq_end(p, s - 1), b = seq_end(p, s), n = b - a;
+    float m = 0.0f;
+    int32_t k = 0;
+    if (n > 0 && e < p.E) {
+        const int64_t last = (b - 1) / p.rows;
+#pragma unroll 8
+        for (int64_t c = a / p.rows + row; c <= last; c += rows) {
+            m += p.mass[(c + s) * p.E + e];
+            k += p.part[(c + s) * p.E + e];
+        }
+    }
+    mass[threadIdx.x] = m;
+    count[threadIdx.x] = k;
+    __syncthreads();
     float sum = 0.0f;
-    for (int e = threadIdx.x; e < p.E; e += 256) {
-        float mass = 0.0f;
-        int32_t count = 0;
-        if (n > 0)
-            for (int64_t c = a / p.rows; c <= (b - 1) / p.rows; c++) {
-                mass += p.mass[(c + s) * p.E + e];
-                count += p.part[(c + s) * p.E + e];
-            }
-        p.counts[(int64_t)s * p.E + e] = count;
-        sum += (float)count * mass;
+    if (row == 0 && e < p.E) {
+        for (int i = 1; i < rows; i++) {
+            m += mass[i * C + e];
+            k += count[i * C + e];
+        }
+        p.counts[(int64_t)s * p.E + e] = k;
+        sum = (float)k * m;
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        sum = (red[0] + red[1]) + (red[2] + red[3]);
+        for (int i = 1; i < 16; i++) sum += red[i];
         p.loss[s] = n > 0 ? sum * ((float)p.E / ((float)p.k * (float)n * (float)n)) : 0.0f;
     }
 }
 
+// Lanes of a wave see what others of it have written to LDS.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// p.rows rows of a block.  What the chosen experts add goes through a row of E numbers in LDS: their scores
+// are read from it, then each choice is added to its expert's place by the lane that holds the expert, in
+// the order of the choices.  (Comparing each choice with each expert in registers: 68 against XXX us for
+// 65536 x 256, 8 of them.)
 template <int L, int NV, bool WIDE32>
 __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) {
     constexpr int R = 64 / L, ROWS = 4 * R, N = 4 * NV;
+    __shared__ float4 lds[4][R][NV][L];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane % L;
-    const int64_t r = (int64_t)blockIdx.x * ROWS + wave * R + lane / L;
-    const int64_t row = r < p.T ? r : p.T - 1;  // the lanes of a wave stay together
-    float l[N], q[N], sc[N], sl[N], dl[N];
-    load_logits<L, NV, WIDE32>(p, row, j, l);
-    scores_of<L>(p.sigmoid, l, q, sc, sl);
-#pragma unroll
-    for (int i = 0; i < N; i++) dl[i] = 0.0f;
-    const int s = seq_of(p, row);
-    if (p.dloss && s < p.S) {
-        const float n = (float)(seq_end(p, s) - (s == 0 ? 0 : seq_end(p, s - 1)));
-        const float over = p.dloss[s] * ((float)p.E / ((float)p.k * n * n));
-        float dp[N], dot = 0.0f;
-#pragma unroll
-        for (int v = 0; v < NV; v++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int e = 4 * (j + L * v) + i;
-                dp[4 * v + i] = e < p.E ? over * (float)p.counts[(int64_t)s * p.E + e] : 0.0f;
-                dot += q[4 * v + i] * dp[4 * v + i];
-            }
-        dot = row_sum<L>(dot);
-#pragma unroll
-        for (int i = 0; i < N; i++) dl[i] = q[i] * sl[i] * (dp[i] - dot);
-    }
-    if (p.dweights) {
-        float times[N], dw[N];  // how often an expert is chosen, and its weights' gradients
-#pragma unroll
-        for (int i = 0; i < N; i++) times[i] = dw[i] = 0.0f;
-        for (int c = 0; c < p.k; c++) {
-            const int id = p.ids[row * p.k + c];
-            const float g = p.dweights[row * p.k + c];
+    float4(*mine)[L] = lds[wave][lane / L];
+    float* place = reinterpret_cast<float*>(mine);  // expert e at place[e]
+    const int64_t begin = (int64_t)blockIdx.x * p.rows;
+    const int64_t end = begin + p.rows < p.T ? begin + p.rows : p.T;
+    int s = p.dloss ? seq_of(p, begin + wave * R + lane / L) - 1 : p.S;
+    int64_t seq_last = -1;  // end of sequence s
+    float dp[N];
+    for (int64_t r0 = begin; r0 < end; r0 += ROWS) {
+        const int64_t r = r0 + wave * R + lane / L;
+        const int64_t row = r < p.T ? r : p.T - 1;  // the lanes of a wave stay together
+        float l[N], q[N], sc[N], sl[N], dl[N];
+        load_logits<L, NV, WIDE32>(p, row, j, l);
+        while (s < p.S && row >= seq_last) {  // the row's sequence, and what its loss gives each expert
+            if (++s >= p.S) break;
+            const int64_t first = s == 0 ? 0 : seq_end(p, s - 1);
+            seq_last = seq_end(p, s);
+            if (row >= seq_last) continue;
+            const float n = (float)(seq_last - first);
+            const float over = p.dloss[s] * ((float)p.E / ((float)p.k * n * n));
 #pragma unroll
             for (int v = 0; v < NV; v++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const bool hit = id == 4 * (j + L * v) + i;
-                    times[4 * v + i] += hit ? 1.0f : 0.0f;
-                    dw[4 * v + i] += hit ? g : 0.0f;
+                    const int e = 4 * (j + L * v) + i;
+                    dp[4 * v + i] = e < p.E ? over * (float)p.counts[(int64_t)s * p.E + e] : 0.0f;
                 }
         }
-        if (p.renorm) {
-            float total = 0.0f, dot = 0.0f;
+        scores_of<L>(p.sigmoid, l, q, sc, sl);
 #pragma unroll
-            for (int i = 0; i < N; i++) total += times[i] * sc[i];
-            total = row_sum<L>(total);
-            if (total < kTinyScores) {  // the weights are a softmax of the chosen logits alone
-                float m = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < N; i++) m = times[i] > 0.0f ? fmaxf(m, l[i]) : m;
-                m = row_max<L>(m);
-                total = 0.0f;
-#pragma unroll
-                for (int i = 0; i < N; i++) {
-                    sc[i] = times[i] > 0.0f && m > -INFINITY ? expf(l[i] - m) : 0.0f;
-                    total += times[i] * sc[i];
-                }
-                total = row_sum<L>(total);
-            }
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-            for (int i = 0; i < N; i++) dot += dw[i] * (sc[i] * inv);
-            dot = row_sum<L>(dot);
-#pragma unroll
-            for (int i = 0; i < N; i++)
-                if (times[i] > 0.0f) dl[i] += p.scale * (sc[i] * inv) * sl[i] * (dw[i] - times[i] * dot);
-        } else if (p.sigmoid) {
-#pragma unroll
-            for (int i = 0; i < N; i++) dl[i] += p.scale * sc[i] * sl[i] * dw[i];
-        } else {
+        for (int i = 0; i < N; i++) dl[i] = 0.0f;
+        if (s < p.S) {
             float dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < N; i++) dot += q[i] * dw[i];
+            for (int i = 0; i < N; i++) dot += q[i] * dp[i];
             dot = row_sum<L>(dot);
 #pragma unroll
-            for (int i = 0; i < N; i++) dl[i] += p.scale * q[i] * (dw[i] - dot);
+            for (int i = 0; i < N; i++) dl[i] = q[i] * sl[i] * (dp[i] - dot);
         }
-    }
-    if (r >= p.T) return;
+        if (p.dweights) {
+            const int32_t* ids = p.ids + row * p.k;
+            const float* dw = p.dweights + row * p.k;
 #pragma unroll
-    for (int v = 0; v < NV; v++) {
-        const int e = 4 * (j + L * v);
-        if (e >= p.E) continue;
-        const float* d = &dl[4 * v];
-        if (WIDE32) {
-            float* dst = static_cast<float*>(p.dlogits) + r * p.ld_d + e;
-            if (p.wide) {
-                *reinterpret_cast<float4*>(dst) = make_float4(d[0], d[1], d[2], d[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (e + i < p.E) dst[i] = d[i];
+            for (int v = 0; v < NV; v++) mine[v][j] = make_float4(sc[4 * v], sc[4 * v + 1], sc[4 * v + 2], sc[4 * v + 3]);
+            wave_sync();
+            float total = 0.0f, dot = 0.0f;
+            for (int c = j; c < p.k; c += L) {
+                const int id = ids[c];
+                const float v = id >= 0 && id < p.E ? place[id] : 0.0f;
+                total += v;
+                dot += v * dw[c];
             }
-        } else {
-            uint16_t* dst = static_cast<uint16_t*>(p.dlogits) + r * p.ld_d + e;
-            if (p.wide) {
-                *reinterpret_cast<uint2*>(dst) = make_uint2(rg_to_bf16(d[0]) | (uint32_t)rg_to_bf16(d[1]) << 16,
-                                                            rg_to_bf16(d[2]) | (uint32_t)rg_to_bf16(d[3]) << 16);
-            } else {
+            total = row_sum<L>(total);
+            dot = row_sum<L>(dot);
+            if (p.renorm && total < kTinyScores) {  // the weights are a softmax of the chosen logits alone
+                float m = -INFINITY;
+                wave_sync();
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (e + i < p.E) dst[i] = rg_to_bf16(d[i]);
+                for (int v = 0; v < NV; v++) mine[v][j] = make_float4(l[4 * v], l[4 * v + 1], l[4 * v + 2], l[4 * v + 3]);
+                wave_sync();
+                for (int c = j; c < p.k; c += L) {
+                    const int id = ids[c];
+                    if (id >= 0 && id < p.E) m = fmaxf(m, place[id]);
+                }
+                m = row_max<L>(m);
+                m = m == -INFINITY ? 0.0f : m;
+                total = dot = 0.0f;
+                for (int c = j; c < p.k; c += L) {
+                    const int id = ids[c];
+                    const float v = id >= 0 && id < p.E ? exp_neg(place[id] - m) : 0.0f;
+                    total += v;
+                    dot += v * dw[c];
+                }
+                total = row_sum<L>(total);
+                dot = row_sum<L>(dot);
+#pragma unroll
+                for (int i = 0; i < N; i++) sc[i] = exp_neg(fminf(l[i] - m, 0.0f));  // counts for chosen ones alone
+            }
+            const float inv = p.renorm ? (total == 0.0f ? 0.0f : 1.0f / total) : 1.0f;
+            dot = p.renorm ? dot * inv : 0.0f;
+            wave_sync();
+#pragma unroll
+            for (int v = 0; v < NV; v++) mine[v][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            wave_sync();
+            for (int c = 0; c < p.k; c++) {
+                const int id = ids[c];
+                if (id >= 0 && id < p.E && (id >> 2) % L == j) place[id] += dw[c] - dot;
+            }
+            wave_sync();
+            float x[N], all = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; v++) {
+                const float4 w = mine[v][j];
+                x[4 * v] = w.x; x[4 * v + 1] = w.y; x[4 * v + 2] = w.z; x[4 * v + 3] = w.w;
+            }
+            if (!p.renorm && !p.sigmoid) {  // a softmax's scores hang together
+#pragma unroll
+                for (int i = 0; i < N; i++) all += q[i] * x[i];
+                all = row_sum<L>(all);
+            }
+#pragma unroll
+            for (int i = 0; i < N; i++) dl[i] += p.scale * (sc[i] * inv) * sl[i] * (x[i] - all);
+        }
+        if (r >= end) continue;
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int e = 4 * (j + L * v);
+            if (e >= p.E) continue;
+            const float* d = &dl[4 * v];
+            if (WIDE32) {
+                float* dst = static_cast<float*>(p.dlogits) + r * p.ld_d + e;
+                if (p.wide) {
+                    *reinterpret_cast<float4*>(dst) = make_float4(d[0], d[1], d[2], d[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (e + i < p.E) dst[i] = d[i];
+                }
+            } else {
+                uint16_t* dst = static_cast<uint16_t*>(p.dlogits) + r * p.ld_d + e;
+                if (p.wide) {
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(rg_pack(d[0], d[1]), rg_pack(d[2], d[3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (e + i < p.E) dst[i] = (uint16_t)rg_pack(d[i], 0.0f);
+                }
             }
         }
     }
@@ -352,27 +419,26 @@ static inline int64_t balance_rows(int64_t T) {
 static inline int64_t balance_slots(int64_t T, int64_t S) { return (T + balance_rows(T) - 1) / balance_rows(T) + S; }
 
 template <int L, int NV, bool WIDE32>
-static void launch_route_grad(const RouteGradArgs& p, bool back, hipStream_t stream) {
+static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     constexpr int ROWS = 4 * (64 / L);
-    if (back) {
-        route_back_kernel<L, NV, WIDE32><<<dim3((unsigned)((p.T + ROWS - 1) / ROWS)), dim3(256), 0, stream>>>(p);
-    } else {
-        const unsigned blocks = (unsigned)((p.T + p.rows - 1) / p.rows);
-        balance_kernel<L, NV, WIDE32><<<dim3(blocks), dim3(256), (size_t)(ROWS + 1) * p.E * 4, stream>>>(p);
-    }
+    if (back) p.rows = p.T <= 2048 * ROWS ? ROWS : (p.T + 2048 * ROWS - 1) / (2048 * ROWS) * ROWS;
+    const unsigned blocks = (unsigned)((p.T + p.rows - 1) / p.rows);
+    if (back) route_back_kernel<L, NV, WIDE32><<<dim3(blocks), dim3(256), 0, stream>>>(p);
+    else balance_kernel<L, NV, WIDE32><<<dim3(blocks), dim3(256), (size_t)(ROWS + 1) * p.E * 4, stream>>>(p);
 }
 
-// Lanes of a row by the number of experts, 4 to a lane.
+// Lanes of a row by the number of experts, 16 of them to a lane: what a row's lanes do together counts for
+// as many experts as it can.
 template <bool WIDE32>
-static void pick_route_grad(const RouteGradArgs& p, bool back, hipStream_t stream) {
+static void pick_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     if (p.E <= 4) launch_route_grad<1, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 8) launch_route_grad<2, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 16) launch_route_grad<4, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 32) launch_route_grad<8, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 64) launch_route_grad<16, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 128) launch_route_grad<32, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 256) launch_route_grad<64, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 512) launch_route_grad<64, 2, WIDE32>(p, back, stream);
+    else if (p.E <= 8) launch_route_grad<1, 2, WIDE32>(p, back, stream);
+    else if (p.E <= 16) launch_route_grad<1, 4, WIDE32>(p, back, stream);
+    else if (p.E <= 32) launch_route_grad<2, 4, WIDE32>(p, back, stream);
+    else if (p.E <= 64) launch_route_grad<4, 4, WIDE32>(p, back, stream);
+    else if (p.E <= 128) launch_route_grad<8, 4, WIDE32>(p, back, stream);
+    else if (p.E <= 256) launch_route_grad<16, 4, WIDE32>(p, back, stream);
+    else if (p.E <= 512) launch_route_grad<32, 4, WIDE32>(p, back, stream);
     else launch_route_grad<64, 4, WIDE32>(p, back, stream);
 }
 
@@ -410,7 +476,9 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
         else pick_route_grad<false>(p, false, stream);
         FP8Q_CHECK_LAUNCH();
     }
-    balance_join_kernel<<<dim3((unsigned)S), dim3(256), 0, stream>>>(p);
+    int C = 1;
+    while (C < E) C *= 2;
+    balance_join_kernel<<<dim3((unsigned)S), dim3(1024), 0, stream>>>(p, C);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
