@@ -62,11 +62,11 @@ __device__ __forceinline__ float row_sum(float v) { return over_row<L, true>(v);
 template <int L>
 __device__ __forceinline__ float row_max(float v) { return over_row<L, false>(v); }
 
-// exp(x) for x <= 0 within two units: 2^(x log2(e)), the product's rounding made good to first order.
-// Results under 2^-126 are zero.
+// exp(x) for x <= 0 within two units and |x| / 4 of the last place: 2^(x log2(e)), the product's rounding made
+// good to first order.  Results under 2^-126 are zero.
 __device__ __forceinline__ float exp_neg(float x) {
     x = x < -200.0f ? -200.0f : x;  // a NaN stays
-    const float t = x * 1.44269504f, r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269504f, -t));
+    const float t = x * 1.44269504f, r = fmaf(x, 1.44269504f, -t);
     const float e = __builtin_amdgcn_exp2f(t);
     return fmaf(e, r * 0.693147181f, e);
 }
@@ -89,94 +89,105 @@ __device__ __forceinline__ int seq_of(const RouteGradArgs& p, int64_t r) {
 }
 
 // A row's logits: L lanes with 4 * NV experts each, lane j's at 4 (j + L v) .. + 3; minus infinity past E.
-template <int L, int NV, bool WIDE32>
-__device__ __forceinline__ void load_logits(const RouteGradArgs& p, int64_t r, int j, float (&l)[4 * NV]) {
+// They are held as they are read until get.
+template <int L, int NV, bool F32>
+struct Logits {
+    uint32_t w[NV][F32 ? 4 : 2];
+    __device__ __forceinline__ void load(const RouteGradArgs& p, int64_t r, int j) {
 #pragma unroll
-    for (int v = 0; v < NV; v++) {
-        const int e = 4 * (j + L * v);
+        for (int v = 0; v < NV; v++) {
+            const int e = 4 * (j + L * v);
+            if (F32) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) l[4 * v + i] = -INFINITY;
-        if (e >= p.E) continue;
-        if (WIDE32) {
-            const float* src = static_cast<const float*>(p.logits) + r * p.ld_l + e;
-            if (p.wide) {
-                const float4 w = *reinterpret_cast<const float4*>(src);
-                l[4 * v] = w.x; l[4 * v + 1] = w.y; l[4 * v + 2] = w.z; l[4 * v + 3] = w.w;
+                for (int i = 0; i < 4; i++) w[v][F32 ? i : 0] = 0xFF800000u;
+                if (e >= p.E) continue;
+                const uint32_t* src = static_cast<const uint32_t*>(p.logits) + r * p.ld_l + e;
+                if (p.wide) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(src);
+                    w[v][0] = a.x; w[v][1] = a.y; w[v][F32 ? 2 : 0] = a.z; w[v][F32 ? 3 : 0] = a.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (e + i < p.E) w[v][F32 ? i : 0] = src[i];
+                }
             } else {
+                w[v][0] = w[v][1] = 0xFF80FF80u;
+                if (e >= p.E) continue;
+                const uint16_t* src = static_cast<const uint16_t*>(p.logits) + r * p.ld_l + e;
+                if (p.wide) {
+                    const uint2 a = *reinterpret_cast<const uint2*>(src);
+                    w[v][0] = a.x; w[v][1] = a.y;
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (e + i < p.E) l[4 * v + i] = src[i];
-            }
-        } else {
-            const uint16_t* src = static_cast<const uint16_t*>(p.logits) + r * p.ld_l + e;
-            if (p.wide) {
-                const uint2 w = *reinterpret_cast<const uint2*>(src);
-                l[4 * v] = bf16_lo(w.x); l[4 * v + 1] = bf16_hi(w.x); l[4 * v + 2] = bf16_lo(w.y); l[4 * v + 3] = bf16_hi(w.y);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (e + i < p.E) l[4 * v + i] = rg_bf16(src[i]);
+                    for (int i = 0; i < 4; i++)
+                        if (e + i < p.E) w[v][i >> 1] = i & 1 ? (w[v][i >> 1] & 0xFFFFu) | (uint32_t)src[i] << 16 : (w[v][i >> 1] & 0xFFFF0000u) | src[i];
+                }
             }
         }
     }
-}
+    __device__ __forceinline__ void get(float (&l)[4 * NV]) const {
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                l[4 * v + i] = F32 ? __uint_as_float(w[v][F32 ? i : 0]) : i & 1 ? bf16_hi(w[v][i >> 1]) : bf16_lo(w[v][i >> 1]);
+    }
+};
 
 // Scores under this sum are formed from the logits less their maximum: sigmoids of logits so far below
 // zero are their exponentials, and a softmax's scores have the exponentials' ratios.
 constexpr float kTinyScores = 5.421010862427522e-20f;  // 2^-64
 
+// exp(l - m) and its row's 1 / sum.
 template <int L, int N>
-__device__ __forceinline__ void softmax_of(const float (&l)[N], float (&out)[N]) {
-    float m = -INFINITY, sum = 0.0f;
+__device__ __forceinline__ void exponentials(const float (&l)[N], float (&t)[N], float& m, float& inv) {
+    m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; i++) m = fmaxf(m, l[i]);
     m = row_max<L>(m);
     m = m == -INFINITY ? 0.0f : m;  // every logit at minus infinity: no probabilities
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        out[i] = exp_neg(l[i] - m);
-        sum += out[i];
+        t[i] = exp_neg(l[i] - m);
+        sum += t[i];
     }
     sum = row_sum<L>(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < N; i++) out[i] *= inv;
+    inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 }
 
-// Probabilities p, and the scores s and slopes of log(s) that the chosen weights are made of.
-template <int L, int N>
-__device__ __forceinline__ void scores_of(bool sigmoid, const float (&l)[N], float (&p)[N], float (&s)[N], float (&slope)[N]) {
-    if (!sigmoid) {
-        softmax_of<L>(l, p);
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            s[i] = p[i];
-            slope[i] = 1.0f;
-        }
+// A row's scores: probabilities are t a, the scores that weights are made of t b, and slope (sigmoids alone;
+// 1 else) is the derivative of a score's logarithm by its logit.
+template <int L, bool SIG, int N>
+__device__ __forceinline__ void scores_of(const float (&l)[N], float (&t)[N], float (&slope)[N], float& a, float& b) {
+    if (!SIG) {
+        float m;
+        exponentials<L>(l, t, m, a);
+        b = a;
         return;
     }
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const float u = exp_neg(-fabsf(l[i])), one = __builtin_amdgcn_rcpf(1.0f + u), rest = u * one;  // neither end overflows or cancels
-        s[i] = l[i] > 0.0f ? one : rest;
+        t[i] = l[i] > 0.0f ? one : rest;
         slope[i] = l[i] > 0.0f ? rest : one;
-        sum += s[i];
+        sum += t[i];
     }
     sum = row_sum<L>(sum);
+    a = 1.0f / sum;
+    b = 1.0f;
     if (sum < kTinyScores) {
-        softmax_of<L>(l, p);
-    } else {
-        const float inv = 1.0f / sum;
-#pragma unroll
-        for (int i = 0; i < N; i++) p[i] = s[i] * inv;
+        float m;
+        exponentials<L>(l, t, m, a);
+        b = expf(m);  // sigmoids so small are exponentials
     }
 }
 
 // One chunk of rows: for each sequence in it, the probabilities' sums and the counts go to slot chunk +
 // sequence of the workspace: both only grow along the rows, so no two pairs share one.  A thread keeps
 // the sums of its experts; rows of the block's waves are added in a fixed order.
-template <int L, int NV, bool WIDE32>
+template <int L, int NV, bool F32, bool SIG>
 __global__ __launch_bounds__(256) void balance_kernel(const RouteGradArgs p) {
     constexpr int R = 64 / L, ROWS = 4 * R, N = 4 * NV;  // rows of a wave and of the block at a time
     extern __shared__ float lds[];
@@ -194,12 +205,16 @@ __global__ __launch_bounds__(256) void balance_kernel(const RouteGradArgs p) {
         float acc[N];
 #pragma unroll
         for (int i = 0; i < N; i++) acc[i] = 0.0f;
+        Logits<L, NV, F32> cur, next;  // a row's loads go out while the one before it is worked on
+        if (r0 + mine < r1) cur.load(p, r0 + mine, j);
         for (int64_t r = r0 + mine; r < r1; r += ROWS) {
-            float l[N], q[N], sc[N], sl[N];
-            load_logits<L, NV, WIDE32>(p, r, j, l);
-            scores_of<L>(p.sigmoid, l, q, sc, sl);
+            next.load(p, r + ROWS < r1 ? r + ROWS : r, j);
+            float l[N], t[N], slope[N], a, b;
+            cur.get(l);
+            scores_of<L, SIG>(l, t, slope, a, b);
 #pragma unroll
-            for (int i = 0; i < N; i++) acc[i] += q[i];
+            for (int i = 0; i < N; i++) acc[i] += t[i] * a;
+            cur = next;
         }
         for (int64_t i = r0 * p.k + threadIdx.x; i < r1 * p.k; i += 256) {
             const int e = p.ids[i];
@@ -225,12 +240,12 @@ __global__ __launch_bounds__(256) void balance_kernel(const RouteGradArgs p) {
     }
 }
 
-// A sequence's loss and counts from its chunks: a block per sequence; C threads take an expert each, the
-// block's 1024 / C rows of them the chunks in turn.
+// A sequence's loss and counts from its chunks: a block per sequence; C threads take an expert each, up to
+// 16 rows of them the chunks in turn.
 __global__ __launch_bounds__(1024) void balance_join_kernel(const RouteGradArgs p, int C) {
     __shared__ float mass[1024], red[16];
     __shared__ int32_t count[1024];
-    const int s = blockIdx.x, e = threadIdx.x & (C - 1), row = threadIdx.x / C, rows = 1024 / C;
+    const int s = blockIdx.x, e = threadIdx.x & (C - 1), row = threadIdx.x / C, rows = blockDim.x / C;
     const int64_t a = s == 0 ? 0 : seq_end(p, s - 1), b = seq_end(p, s), n = b - a;
     float m = 0.0f;
     int32_t k = 0;
@@ -259,7 +274,7 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const RouteGradArgs 
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < 16; i++) sum += red[i];
+        for (int i = 1; i < (int)blockDim.x / 64; i++) sum += red[i];
         p.loss[s] = n > 0 ? sum * ((float)p.E / ((float)p.k * (float)n * (float)n)) : 0.0f;
     }
 }
@@ -271,33 +286,62 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// p.rows rows of a block.  What the chosen experts add goes through a row of E numbers in LDS: their scores
-// are read from it, then each choice is added to its expert's place by the lane that holds the expert, in
-// the order of the choices.  (Comparing each choice with each expert in registers: 68 against XXX us for
-// 65536 x 256, 8 of them.)
-template <int L, int NV, bool WIDE32>
+// p.rows rows of a block.  What the chosen experts' weights add goes through LDS: a row's scores are read
+// there by its choices, and each choice leaves its part at its expert's place.  (Comparing each choice with
+// each expert in registers: 68 us where this takes 30, 65536 x 256, 8 of them.)  Where an expert is named
+// twice for a token, which a choice learns by not finding its own number at the place, the lane that holds
+// the expert adds its parts in the order of the choices.
+template <int L, int NV, bool F32, bool SIG>
 __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) {
     constexpr int R = 64 / L, ROWS = 4 * R, N = 4 * NV;
-    __shared__ float4 lds[4][R][NV][L];
+    __shared__ float4 lds[2][4][R][NV][L];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane % L;
-    float4(*mine)[L] = lds[wave][lane / L];
-    float* place = reinterpret_cast<float*>(mine);  // expert e at place[e]
+    float4(*scores)[L] = lds[0][wave][lane / L];
+    float4(*parts)[L] = lds[1][wave][lane / L];
+    float* score = reinterpret_cast<float*>(scores);  // expert e's at score[e]
+    float* part = reinterpret_cast<float*>(parts);
+    int32_t* tag = reinterpret_cast<int32_t*>(parts);
     const int64_t begin = (int64_t)blockIdx.x * p.rows;
     const int64_t end = begin + p.rows < p.T ? begin + p.rows : p.T;
     int s = p.dloss ? seq_of(p, begin + wave * R + lane / L) - 1 : p.S;
     int64_t seq_last = -1;  // end of sequence s
     float dp[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) dp[i] = 0.0f;
     for (int64_t r0 = begin; r0 < end; r0 += ROWS) {
         const int64_t r = r0 + wave * R + lane / L;
         const int64_t row = r < p.T ? r : p.T - 1;  // the lanes of a wave stay together
-        float l[N], q[N], sc[N], sl[N], dl[N];
-        load_logits<L, NV, WIDE32>(p, row, j, l);
+        Logits<L, NV, F32> raw;
+        raw.load(p, row, j);
+        const int32_t* ids = p.ids + row * p.k;
+        const float* dw = p.dweights + row * p.k;
+        const auto expert = [&](int c) {  // of choice c, E for none
+            const int id = ids[c];
+            return id >= 0 && id < p.E ? id : p.E;
+        };
+        int first = p.E;  // the lane's first choice and its weight's gradient
+        float first_dw = 0.0f;
+        if (p.dweights && j < p.k) {
+            first = expert(j);
+            first_dw = dw[j];
+        }
+        const auto choices = [&](auto&& f) {  // the lane's: number, expert, gradient
+            if (first < p.E) f(j, first, first_dw);
+            for (int c = j + L; c < p.k; c += L) {
+                const int e = expert(c);
+                if (e < p.E) f(c, e, dw[c]);
+            }
+        };
         while (s < p.S && row >= seq_last) {  // the row's sequence, and what its loss gives each expert
-            if (++s >= p.S) break;
-            const int64_t first = s == 0 ? 0 : seq_end(p, s - 1);
+            if (++s >= p.S) {
+#pragma unroll
+                for (int i = 0; i < N; i++) dp[i] = 0.0f;
+                break;
+            }
+            const int64_t from = s == 0 ? 0 : seq_end(p, s - 1);
             seq_last = seq_end(p, s);
             if (row >= seq_last) continue;
-            const float n = (float)(seq_last - first);
+            const float n = (float)(seq_last - from);
             const float over = p.dloss[s] * ((float)p.E / ((float)p.k * n * n));
 #pragma unroll
             for (int v = 0; v < NV; v++)
@@ -307,88 +351,102 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
                     dp[4 * v + i] = e < p.E ? over * (float)p.counts[(int64_t)s * p.E + e] : 0.0f;
                 }
         }
-        scores_of<L>(p.sigmoid, l, q, sc, sl);
-#pragma unroll
-        for (int i = 0; i < N; i++) dl[i] = 0.0f;
-        if (s < p.S) {
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < N; i++) dot += q[i] * dp[i];
-            dot = row_sum<L>(dot);
-#pragma unroll
-            for (int i = 0; i < N; i++) dl[i] = q[i] * sl[i] * (dp[i] - dot);
+        float t[N], slope[N], a, b;
+        {
+            float l[N];
+            raw.get(l);
+            scores_of<L, SIG>(l, t, slope, a, b);
         }
-        if (p.dweights) {
-            const int32_t* ids = p.ids + row * p.k;
-            const float* dw = p.dweights + row * p.k;
+        float mean = 0.0f;  // of dp over p
+        if (p.dloss) {
 #pragma unroll
-            for (int v = 0; v < NV; v++) mine[v][j] = make_float4(sc[4 * v], sc[4 * v + 1], sc[4 * v + 2], sc[4 * v + 3]);
+            for (int i = 0; i < N; i++) mean += t[i] * dp[i];
+            mean = row_sum<L>(mean) * a;
+        }
+        float x[N], all = 0.0f;  // what the weights add: slope (x - t all)
+        if (p.dweights) {
+            wave_sync();
+#pragma unroll
+            for (int v = 0; v < NV; v++) {
+                scores[v][j] = make_float4(t[4 * v], t[4 * v + 1], t[4 * v + 2], t[4 * v + 3]);
+                parts[v][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
             wave_sync();
             float total = 0.0f, dot = 0.0f;
-            for (int c = j; c < p.k; c += L) {
-                const int id = ids[c];
-                const float v = id >= 0 && id < p.E ? place[id] : 0.0f;
+            choices([&](int c, int e, float g) {
+                const float v = score[e];
                 total += v;
-                dot += v * dw[c];
-            }
+                dot += v * g;
+                tag[e] = c;
+            });
             total = row_sum<L>(total);
             dot = row_sum<L>(dot);
-            if (p.renorm && total < kTinyScores) {  // the weights are a softmax of the chosen logits alone
+            float by = p.scale * b;
+            if (!p.renorm) {
+                if (!SIG) all = by * b * dot;  // a softmax's scores hang together
+                dot = 0.0f;
+            } else if (total >= kTinyScores || total != total) {
+                by = p.scale / total;
+                dot /= total;
+            } else {  // the weights are a softmax of the chosen logits alone
+                const auto logit = [&](int e) {
+                    const int64_t at = row * p.ld_l + e;
+                    return F32 ? static_cast<const float*>(p.logits)[at] : rg_bf16(static_cast<const uint16_t*>(p.logits)[at]);
+                };
                 float m = -INFINITY;
-                wave_sync();
-#pragma unroll
-                for (int v = 0; v < NV; v++) mine[v][j] = make_float4(l[4 * v], l[4 * v + 1], l[4 * v + 2], l[4 * v + 3]);
-                wave_sync();
-                for (int c = j; c < p.k; c += L) {
-                    const int id = ids[c];
-                    if (id >= 0 && id < p.E) m = fmaxf(m, place[id]);
-                }
+                choices([&](int, int e, float) { m = fmaxf(m, logit(e)); });
                 m = row_max<L>(m);
                 m = m == -INFINITY ? 0.0f : m;
                 total = dot = 0.0f;
-                for (int c = j; c < p.k; c += L) {
-                    const int id = ids[c];
-                    const float v = id >= 0 && id < p.E ? exp_neg(place[id] - m) : 0.0f;
+                choices([&](int, int e, float g) {
+                    const float v = exp_neg(logit(e) - m);
+                    score[e] = v;
                     total += v;
-                    dot += v * dw[c];
-                }
+                    dot += v * g;
+                });
                 total = row_sum<L>(total);
                 dot = row_sum<L>(dot);
-#pragma unroll
-                for (int i = 0; i < N; i++) sc[i] = exp_neg(fminf(l[i] - m, 0.0f));  // counts for chosen ones alone
-            }
-            const float inv = p.renorm ? (total == 0.0f ? 0.0f : 1.0f / total) : 1.0f;
-            dot = p.renorm ? dot * inv : 0.0f;
-            wave_sync();
-#pragma unroll
-            for (int v = 0; v < NV; v++) mine[v][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            wave_sync();
-            for (int c = 0; c < p.k; c++) {
-                const int id = ids[c];
-                if (id >= 0 && id < p.E && (id >> 2) % L == j) place[id] += dw[c] - dot;
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                by = p.scale * inv;
+                dot *= inv;
             }
             wave_sync();
-            float x[N], all = 0.0f;
+            bool twice = false;
+            choices([&](int c, int e, float) { twice = twice || tag[e] != c; });
+            twice = __any(twice);
+            wave_sync();
+            if (!twice) {
+                choices([&](int, int e, float g) { part[e] = score[e] * by * (g - dot); });
+            } else {
 #pragma unroll
-            for (int v = 0; v < NV; v++) {
-                const float4 w = mine[v][j];
-                x[4 * v] = w.x; x[4 * v + 1] = w.y; x[4 * v + 2] = w.z; x[4 * v + 3] = w.w;
+                for (int v = 0; v < NV; v++) parts[v][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                wave_sync();
+                for (int c = 0; c < p.k; c++) {
+                    const int e = expert(c);
+                    if (e < p.E && (e >> 2) % L == j) part[e] += score[e] * by * (dw[c] - dot);
+                }
             }
-            if (!p.renorm && !p.sigmoid) {  // a softmax's scores hang together
+            wave_sync();
+        }
 #pragma unroll
-                for (int i = 0; i < N; i++) all += q[i] * x[i];
-                all = row_sum<L>(all);
-            }
-#pragma unroll
-            for (int i = 0; i < N; i++) dl[i] += p.scale * (sc[i] * inv) * sl[i] * (x[i] - all);
+        for (int v = 0; v < NV; v++) {
+            float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p.dweights) w = parts[v][j];
+            x[4 * v] = w.x; x[4 * v + 1] = w.y; x[4 * v + 2] = w.z; x[4 * v + 3] = w.w;
         }
         if (r >= end) continue;
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             const int e = 4 * (j + L * v);
             if (e >= p.E) continue;
-            const float* d = &dl[4 * v];
-            if (WIDE32) {
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int k = 4 * v + i;
+                d[i] = t[k] * (a * (dp[k] - mean) - all) + x[k];
+                if (SIG) d[i] *= slope[k];
+            }
+            if (F32) {
                 float* dst = static_cast<float*>(p.dlogits) + r * p.ld_d + e;
                 if (p.wide) {
                     *reinterpret_cast<float4*>(dst) = make_float4(d[0], d[1], d[2], d[3]);
@@ -418,28 +476,35 @@ static inline int64_t balance_rows(int64_t T) {
 }
 static inline int64_t balance_slots(int64_t T, int64_t S) { return (T + balance_rows(T) - 1) / balance_rows(T) + S; }
 
-template <int L, int NV, bool WIDE32>
+template <int L, int NV, bool F32, bool SIG>
 static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     constexpr int ROWS = 4 * (64 / L);
     if (back) p.rows = p.T <= 2048 * ROWS ? ROWS : (p.T + 2048 * ROWS - 1) / (2048 * ROWS) * ROWS;
     const unsigned blocks = (unsigned)((p.T + p.rows - 1) / p.rows);
-    if (back) route_back_kernel<L, NV, WIDE32><<<dim3(blocks), dim3(256), 0, stream>>>(p);
-    else balance_kernel<L, NV, WIDE32><<<dim3(blocks), dim3(256), (size_t)(ROWS + 1) * p.E * 4, stream>>>(p);
+    if (back) route_back_kernel<L, NV, F32, SIG><<<dim3(blocks), dim3(256), 0, stream>>>(p);
+    else balance_kernel<L, NV, F32, SIG><<<dim3(blocks), dim3(256), (size_t)(ROWS + 1) * p.E * 4, stream>>>(p);
 }
 
 // Lanes of a row by the number of experts, 16 of them to a lane: what a row's lanes do together counts for
 // as many experts as it can.
-template <bool WIDE32>
+template <bool F32, bool SIG>
 static void pick_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
-    if (p.E <= 4) launch_route_grad<1, 1, WIDE32>(p, back, stream);
-    else if (p.E <= 8) launch_route_grad<1, 2, WIDE32>(p, back, stream);
-    else if (p.E <= 16) launch_route_grad<1, 4, WIDE32>(p, back, stream);
-    else if (p.E <= 32) launch_route_grad<2, 4, WIDE32>(p, back, stream);
-    else if (p.E <= 64) launch_route_grad<4, 4, WIDE32>(p, back, stream);
-    else if (p.E <= 128) launch_route_grad<8, 4, WIDE32>(p, back, stream);
-    else if (p.E <= 256) launch_route_grad<16, 4, WIDE32>(p, back, stream);
-    else if (p.E <= 512) launch_route_grad<32, 4, WIDE32>(p, back, stream);
-    else launch_route_grad<64, 4, WIDE32>(p, back, stream);
+    if (p.E <= 4) launch_route_grad<1, 1, F32, SIG>(p, back, stream);
+    else if (p.E <= 8) launch_route_grad<1, 2, F32, SIG>(p, back, stream);
+    else if (p.E <= 16) launch_route_grad<1, 4, F32, SIG>(p, back, stream);
+    else if (p.E <= 32) launch_route_grad<2, 4, F32, SIG>(p, back, stream);
+    else if (p.E <= 64) launch_route_grad<4, 4, F32, SIG>(p, back, stream);
+    else if (p.E <= 128) launch_route_grad<8, 4, F32, SIG>(p, back, stream);
+    else if (p.E <= 256) launch_route_grad<16, 4, F32, SIG>(p, back, stream);
+    else if (p.E <= 512) launch_route_grad<32, 4, F32, SIG>(p, back, stream);
+    else launch_route_grad<64, 4, F32, SIG>(p, back, stream);
+}
+
+static void start_route_grad(RouteGradArgs& p, bool f32, bool back, hipStream_t stream) {
+    if (f32 && p.sigmoid) pick_route_grad<true, true>(p, back, stream);
+    else if (f32) pick_route_grad<true, false>(p, back, stream);
+    else if (p.sigmoid) pick_route_grad<false, true>(p, back, stream);
+    else pick_route_grad<false, false>(p, back, stream);
 }
 
 static inline bool rg_wide(const void* p, int64_t ld, int64_t E, bool f32) {
@@ -472,13 +537,12 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
     p.part = reinterpret_cast<int32_t*>(p.mass + balance_slots(T, S) * E);
     p.E = (int)E; p.k = top_k; p.S = S; p.sigmoid = scoring == FP8Q_SCORE_SIGMOID; p.wide = rg_wide(logits, ld_l, E, f32);
     if (T > 0) {
-        if (f32) pick_route_grad<true>(p, false, stream);
-        else pick_route_grad<false>(p, false, stream);
+        start_route_grad(p, f32, false, stream);
         FP8Q_CHECK_LAUNCH();
     }
-    int C = 1;
+    int C = 4;
     while (C < E) C *= 2;
-    balance_join_kernel<<<dim3((unsigned)S), dim3(1024), 0, stream>>>(p, C);
+    balance_join_kernel<<<dim3((unsigned)S), dim3(C < 64 ? 16 * C : 1024), 0, stream>>>(p, C);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
@@ -502,8 +566,7 @@ extern "C" fp8q_status_t moe_route_backward(const void* logits, fp8q_out_t logit
     p.dloss = dloss; p.counts = const_cast<int32_t*>(counts); p.sequences = sequences; p.S = S; p.dlogits = dlogits; p.ld_d = ld_d;
     p.E = (int)E; p.k = top_k; p.sigmoid = scoring == FP8Q_SCORE_SIGMOID;
     p.wide = rg_wide(logits, ld_l, E, f32) && rg_wide(dlogits, ld_d, E, f32);
-    if (f32) pick_route_grad<true>(p, true, stream);
-    else pick_route_grad<false>(p, true, stream);
+    start_route_grad(p, f32, true, stream);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
