@@ -24,7 +24,9 @@ namespace fp8q {
 
 constexpr int AB = 128;            // elements of a block with one factor
 constexpr int ADAMW_TENSORS = 40;  // of one launch: its arguments fit the 4 KB that a launch takes
-constexpr int CHUNK = 2048;        // elements that a block of threads takes at a time
+// Elements that a block of 256 threads takes: 8 of a thread, with 8-bit states twice 8, half a chunk apart,
+// so that what a block's factors cost is shared by more of them.
+constexpr int chunk_of(bool eight) { return eight ? 4096 : 2048; }
 
 struct AdamTensor {
     void* param;
@@ -52,10 +54,10 @@ struct AdamArgs {
 };
 
 __device__ __forceinline__ float ad_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ uint16_t ad_to_bf16(float f) {
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);  // NaN stays NaN
-    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+typedef __bf16 ad_bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t ad_pack(float a, float b) {  // to the nearest, ties to even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2_t{a, b}), ad_bf16x2));
 }
 
 // An access that is always one to global memory, also where the compiler would choose between this
@@ -110,22 +112,17 @@ __device__ __forceinline__ void store8(void* dst, int64_t at, int n, bool wide, 
     } else {
         uint16_t* p = static_cast<uint16_t*>(dst) + at;
         if (wide && n == 8) {
-            *reinterpret_cast<uint4*>(p) = make_uint4(ad_to_bf16(v[0]) | (uint32_t)ad_to_bf16(v[1]) << 16,
-                                                      ad_to_bf16(v[2]) | (uint32_t)ad_to_bf16(v[3]) << 16,
-                                                      ad_to_bf16(v[4]) | (uint32_t)ad_to_bf16(v[5]) << 16,
-                                                      ad_to_bf16(v[6]) | (uint32_t)ad_to_bf16(v[7]) << 16);
+            *reinterpret_cast<uint4*>(p) = make_uint4(ad_pack(v[0], v[1]), ad_pack(v[2], v[3]), ad_pack(v[4], v[5]), ad_pack(v[6], v[7]));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                if (i < n) p[i] = ad_to_bf16(v[i]);
+                if (i < n) p[i] = (uint16_t)ad_pack(v[i], 0.0f);
         }
     }
 }
 
-typedef float f2_t __attribute__((ext_vector_type(2)));
-
-// Eight e4m3fn bytes times their block's factor.
-__device__ __forceinline__ void load8_fp8(const void* src, int64_t at, int n, bool wide, float d, float (&out)[8]) {
+// Eight e4m3fn values.
+__device__ __forceinline__ void load8_fp8(const void* src, int64_t at, int n, bool wide, float (&out)[8]) {
     const uint8_t* p = static_cast<const uint8_t*>(src) + at;
     uint32_t w[2] = {0, 0};
     if (wide && n == 8) {
@@ -139,29 +136,36 @@ __device__ __forceinline__ void load8_fp8(const void* src, int64_t at, int n, bo
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], true);
-        out[4 * i] = lo.x * d; out[4 * i + 1] = lo.y * d; out[4 * i + 2] = hi.x * d; out[4 * i + 3] = hi.y * d;
+        out[4 * i] = lo.x; out[4 * i + 1] = lo.y; out[4 * i + 2] = hi.x; out[4 * i + 3] = hi.y;
     }
 }
 
-// Keeps eight values of a block that 16 lanes share: factor and bytes.  ROOT: nonzero values, all of one
-// sign, do not become zero.
+// Largest magnitude of eight values each of 16 lanes, in all of them: by DPP 1 and 2 lanes away, then mirrored
+// in 8 and in 16.
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v) {
+    return fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false)));
+}
+__device__ __forceinline__ float block_amax(const float (&x)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(x[i]));
+    return dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(m))));
+}
+
+// Eight values as bytes, by their block's multiplier and random bits.  ROOT: values of which none is negative
+// and a nonzero one does not become zero: what lies under the grid's first value is taken for it.
 template <bool ROOT>
-__device__ __forceinline__ void keep8(void* dst, float* scales, int64_t at, int n, bool wide, const float (&x)[8], const uint32_t (&bits)[8]) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-    const float s = scale_from_amax<FP8Q_E4M3FN>(amax);
-    if ((threadIdx.x & 15) == 0 && n > 0) scales[at / AB] = 1.0f / s;
+__device__ __forceinline__ void keep8(void* dst, int64_t at, int n, bool wide, float s, const float (&x)[8], const uint32_t (&bits)[8]) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const float y = __builtin_amdgcn_fmed3f(x[i] * s, -kFmaxFn, kFmaxFn);
+        const float y = __builtin_amdgcn_fmed3f(x[i] * s, ROOT ? (x[i] > 0.0f ? 0.001953125f : 0.0f) : -kFmaxFn, kFmaxFn);
         const uint32_t r = ROOT ? bits[i] << 16 | bits[i] >> 16 : bits[i];
-        uint32_t b = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, 0, 0) & 0xFFu;
-        if (ROOT) b = x[i] > 0.0f && b == 0 ? 1u : b;
-        w[i >> 2] |= b << (8 * (i & 3));
+        if ((i & 3) == 0) w[i >> 2] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, 0, 0);
+        if ((i & 3) == 1) w[i >> 2] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, (int)w[i >> 2], 1);
+        if ((i & 3) == 2) w[i >> 2] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, (int)w[i >> 2], 2);
+        if ((i & 3) == 3) w[i >> 2] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, (int)w[i >> 2], 3);
     }
     uint8_t* p = static_cast<uint8_t*>(dst) + at;
     if (wide && n == 8) {
@@ -183,6 +187,7 @@ __device__ __forceinline__ void moments(const AdamArgs& a, float g, float& m, fl
 
 template <bool EIGHT>
 __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
+    constexpr int H = EIGHT ? 2 : 1, CHUNK = chunk_of(EIGHT);
     int lo = 0, hi = a.count - 1;  // the tensor of this chunk
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -190,8 +195,29 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
     }
     const AdamTensor& t = a.t[lo];
     const int64_t first = lo ? a.chunk_end[lo - 1] : 0;
-    const int64_t at = ((int64_t)blockIdx.x - first) * CHUNK + 8 * threadIdx.x;
-    const int n = t.n - at >= 8 ? 8 : t.n > at ? (int)(t.n - at) : 0;
+    const int64_t at0 = ((int64_t)blockIdx.x - first) * CHUNK + 8 * threadIdx.x;
+    const bool wide = t.wide;
+    float p[H][8], g[H][8], m[H][8], v[H][8], dm[H], dv[H];
+    int n[H];
+#pragma unroll
+    for (int h = 0; h < H; h++) {
+        const int64_t at = at0 + h * 2048;
+        n[h] = t.n - at >= 8 ? 8 : t.n > at ? (int)(t.n - at) : 0;
+        if (t.master) load8<true>(t.master, at, n[h], wide, p[h]);
+        else if (t.param32) load8<true>(t.param, at, n[h], wide, p[h]);
+        else load8<false>(t.param, at, n[h], wide, p[h]);
+        if (t.grad32) load8<true>(t.grad, at, n[h], wide, g[h]);
+        else load8<false>(t.grad, at, n[h], wide, g[h]);
+        if (EIGHT) {
+            dm[h] = n[h] > 0 ? t.m_scales[at / AB] : 0.0f;
+            dv[h] = n[h] > 0 ? t.v_scales[at / AB] : 0.0f;
+            load8_fp8(t.m, at, n[h], wide, m[h]);
+            load8_fp8(t.v, at, n[h], wide, v[h]);
+        } else {
+            load8<true>(t.m, at, n[h], wide, m[h]);
+            load8<true>(t.v, at, n[h], wide, v[h]);
+        }
+    }
     const float lr = a.lr_device ? global_at(a.lr_device, 0) : a.lr;
     float inv_bc1 = a.inv_bc1, inv_bc2 = a.inv_bc2;
     uint32_t seed = a.seed;
@@ -201,49 +227,53 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
         inv_bc2 = -1.0f / expm1f((float)step * a.log_b2);
         seed += (uint32_t)step;
     }
-    const bool wide = t.wide;
-    float p[8], g[8], m[8], v[8], r[8];
-    if (t.master) load8<true>(t.master, at, n, wide, p);
-    else if (t.param32) load8<true>(t.param, at, n, wide, p);
-    else load8<false>(t.param, at, n, wide, p);
-    if (t.grad32) load8<true>(t.grad, at, n, wide, g);
-    else load8<false>(t.grad, at, n, wide, g);
-    if (a.grad_scale) {
-        const float gs = global_at(a.grad_scale, 0);
+    const float scale = a.grad_scale ? global_at(a.grad_scale, 0) : 1.0f, root_bc2 = sqrtf(inv_bc2);
+    float r[H][8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) g[i] *= gs;
-    }
-    if (EIGHT) {
-        const bool any = n > 0;
-        load8_fp8(t.m, at, n, wide, any ? t.m_scales[at / AB] : 0.0f, m);
-        load8_fp8(t.v, at, n, wide, any ? t.v_scales[at / AB] : 0.0f, v);
+    for (int h = 0; h < H; h++) {
+        if (EIGHT) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] *= v[i];
-    } else {
-        load8<true>(t.m, at, n, wide, m);
-        load8<true>(t.v, at, n, wide, v);
-    }
-    const float root_bc2 = sqrtf(inv_bc2);
+            for (int i = 0; i < 8; i++) {
+                m[h][i] *= dm[h];
+                v[h][i] *= dv[h];
+                v[h][i] *= v[h][i];
+            }
+        }
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        moments(a, g[i], m[i], v[i]);
-        r[i] = sqrtf(v[i]);
-        const float d = (m[i] * inv_bc1) / (r[i] * root_bc2 + a.eps);
-        p[i] = p[i] - lr * (d + a.decay * p[i]);
+        for (int i = 0; i < 8; i++) {
+            moments(a, a.grad_scale ? g[h][i] * scale : g[h][i], m[h][i], v[h][i]);
+            r[h][i] = sqrtf(v[h][i]);
+            const float d = m[h][i] * inv_bc1 * __builtin_amdgcn_rcpf(r[h][i] * root_bc2 + a.eps);
+            p[h][i] = p[h][i] - lr * (d + a.decay * p[h][i]);
+        }
+        const int64_t at = at0 + h * 2048;
+        if (t.master) store8<true>(t.master, at, n[h], wide, p[h]);
+        if (t.param32) store8<true>(t.param, at, n[h], wide, p[h]);
+        else store8<false>(t.param, at, n[h], wide, p[h]);
+        if (!EIGHT) {
+            store8<true>(t.m, at, n[h], wide, m[h]);
+            store8<true>(t.v, at, n[h], wide, v[h]);
+        }
     }
-    if (t.master) store8<true>(t.master, at, n, wide, p);
-    if (t.param32) store8<true>(t.param, at, n, wide, p);
-    else store8<false>(t.param, at, n, wide, p);
-    if (EIGHT) {
-        const uint32_t key = mix(seed * 0x9E3779B1u + t.index) + (uint32_t)at + (uint32_t)(at >> 32) * 0x632BE5A7u;
+    if (!EIGHT) return;
+    // 16 lanes share two blocks and so four factors: four lanes form each of them
+    const int which = (threadIdx.x >> 2) & 3;
+    const float m0 = block_amax(m[0]), m1 = block_amax(m[H - 1]), r0 = block_amax(r[0]), r1 = block_amax(r[H - 1]);
+    const float mine = scale_from_amax<FP8Q_E4M3FN>(which & 2 ? (which & 1 ? r1 : m1) : which & 1 ? r0 : m0);
+    const int64_t at1 = at0 + (which & 2 ? 2048 : 0);
+    if ((threadIdx.x & 3) == 0 && t.n > (at1 & ~(int64_t)(AB - 1))) (which & 1 ? t.v_scales : t.m_scales)[at1 / AB] = 1.0f / mine;
+    const uint32_t key = mix(seed * 0x9E3779B1u + t.index);
+#pragma unroll
+    for (int h = 0; h < H; h++) {
+        const int64_t at = at0 + h * 2048;
+        const int from = (threadIdx.x & 48) + 8 * h;
+        const float sm = __shfl(mine, from, 64), sr = __shfl(mine, from + 4, 64);
+        const uint32_t base = key + (uint32_t)at + (uint32_t)(at >> 32) * 0x632BE5A7u;
         uint32_t bits[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) bits[i] = mix(key + i);
-        keep8<false>(t.m, t.m_scales, at, n, wide, m, bits);
-        keep8<true>(t.v, t.v_scales, at, n, wide, r, bits);
-    } else {
-        store8<true>(t.m, at, n, wide, m);
-        store8<true>(t.v, at, n, wide, v);
+        for (int i = 0; i < 8; i++) bits[i] = mix(base + i);
+        keep8<false>(t.m, at, n[h], wide, sm, m[h], bits);
+        keep8<true>(t.v, at, n[h], wide, sr, r[h], bits);
     }
 }
 
@@ -257,6 +287,7 @@ extern "C" fp8q_status_t adamw_step(const fp8q_adamw_tensor_t* tensors, int32_t 
         !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps > 0.0f) || (!h->step_device && h->step < 1))
         return FP8Q_ERR_INVALID_ARG;
     const bool eight = h->state_bits == 8;
+    const int64_t chunk = chunk_of(eight);
     for (int32_t i = 0; i < count; i++) {  // all of them before the first launch
         const fp8q_adamw_tensor_t& t = tensors[i];
         if (t.n < 0 || (t.param_dtype != FP8Q_OUT_BF16 && t.param_dtype != FP8Q_OUT_FP32) ||
@@ -264,7 +295,7 @@ extern "C" fp8q_status_t adamw_step(const fp8q_adamw_tensor_t* tensors, int32_t 
             return FP8Q_ERR_INVALID_ARG;
         if (!ad_real(t)) continue;
         if (!t.param || !t.exp_avg || !t.exp_avg_sq || (eight && (!t.exp_avg_scales || !t.exp_avg_sq_scales))) return FP8Q_ERR_INVALID_ARG;
-        if (t.n > (int64_t)CHUNK << 23) return FP8Q_ERR_UNSUPPORTED;  // a launch takes fewer than 2^32 threads
+        if (t.n > 1LL << 34) return FP8Q_ERR_UNSUPPORTED;  // a launch takes fewer than 2^32 threads
     }
     AdamArgs a{};
     a.b1 = (float)h->beta1; a.b2 = (float)h->beta2; a.one_b1 = (float)(1.0 - h->beta1); a.one_b2 = (float)(1.0 - h->beta2);
@@ -284,7 +315,7 @@ extern "C" fp8q_status_t adamw_step(const fp8q_adamw_tensor_t* tensors, int32_t 
         for (; i < count && a.count < ADAMW_TENSORS; i++) {
             const fp8q_adamw_tensor_t& t = tensors[i];
             if (!ad_real(t)) continue;
-            const int64_t more = (t.n + CHUNK - 1) / CHUNK;
+            const int64_t more = (t.n + chunk - 1) / chunk;
             if (chunks + more >= 1LL << 24) break;
             AdamTensor& to = a.t[a.count];
             to.param = t.param; to.master = t.master; to.grad = t.grad; to.m = t.exp_avg; to.m_scales = t.exp_avg_scales;
