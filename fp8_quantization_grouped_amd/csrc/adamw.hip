@@ -17,7 +17,9 @@
 // xor-shift and odd product (as in the finalizers of published hash functions, with constants of its
 // own); m takes the word, r the word with its halves exchanged, the conversion the upper 20 bits of each.
 //
-// Bound: HBM.
+// Bound: HBM.  Measured (MI355X, bytes of every tensor read and written once): 277M bf16 elements with 8-bit
+// states 524 us (5.35 TB/s), 58M with masters, fp32 gradients and 32-bit states 321 us (5.4 TB/s), where a
+// copy of large buffers reaches 5.2; 1.6M elements 8.3 us, mostly a launch's and the host's time.
 #include "common.hpp"
 
 namespace fp8q {
@@ -73,14 +75,25 @@ __device__ __forceinline__ uint32_t mix(uint32_t z) {
     return z ^ z >> 16;
 }
 
+// 16 bytes, with the non-temporal hint or without.
+template <bool NT>
+__device__ __forceinline__ uint4 get16(const void* p) { return NT ? ld_nt16(p) : *static_cast<const uint4*>(p); }
+template <bool NT>
+__device__ __forceinline__ void put16(void* p, uint4 v) {
+    if (NT) st_nt16(p, v);
+    else *static_cast<uint4*>(p) = v;
+}
+__device__ __forceinline__ uint32_t bits_of(float f) { return __float_as_uint(f); }
+
 // Eight consecutive elements as 32-bit values; n of them exist.
-template <bool F32>
+template <bool F32, bool NT>
 __device__ __forceinline__ void load8(const void* src, int64_t at, int n, bool wide, float (&out)[8]) {
     if (F32) {
         const float* p = static_cast<const float*>(src) + at;
         if (wide && n == 8) {
-            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-            out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w; out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+            const uint4 a = get16<NT>(p), b = get16<NT>(p + 4);
+            out[0] = __uint_as_float(a.x); out[1] = __uint_as_float(a.y); out[2] = __uint_as_float(a.z); out[3] = __uint_as_float(a.w);
+            out[4] = __uint_as_float(b.x); out[5] = __uint_as_float(b.y); out[6] = __uint_as_float(b.z); out[7] = __uint_as_float(b.w);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++) out[i] = i < n ? p[i] : 0.0f;
@@ -88,7 +101,7 @@ __device__ __forceinline__ void load8(const void* src, int64_t at, int n, bool w
     } else {
         const uint16_t* p = static_cast<const uint16_t*>(src) + at;
         if (wide && n == 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const uint4 a = get16<NT>(p);
             out[0] = bf16_lo(a.x); out[1] = bf16_hi(a.x); out[2] = bf16_lo(a.y); out[3] = bf16_hi(a.y);
             out[4] = bf16_lo(a.z); out[5] = bf16_hi(a.z); out[6] = bf16_lo(a.w); out[7] = bf16_hi(a.w);
         } else {
@@ -97,13 +110,13 @@ __device__ __forceinline__ void load8(const void* src, int64_t at, int n, bool w
         }
     }
 }
-template <bool F32>
+template <bool F32, bool NT>
 __device__ __forceinline__ void store8(void* dst, int64_t at, int n, bool wide, const float (&v)[8]) {
     if (F32) {
         float* p = static_cast<float*>(dst) + at;
         if (wide && n == 8) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            put16<NT>(p, make_uint4(bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])));
+            put16<NT>(p + 4, make_uint4(bits_of(v[4]), bits_of(v[5]), bits_of(v[6]), bits_of(v[7])));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -112,7 +125,7 @@ __device__ __forceinline__ void store8(void* dst, int64_t at, int n, bool wide, 
     } else {
         uint16_t* p = static_cast<uint16_t*>(dst) + at;
         if (wide && n == 8) {
-            *reinterpret_cast<uint4*>(p) = make_uint4(ad_pack(v[0], v[1]), ad_pack(v[2], v[3]), ad_pack(v[4], v[5]), ad_pack(v[6], v[7]));
+            put16<NT>(p, make_uint4(ad_pack(v[0], v[1]), ad_pack(v[2], v[3]), ad_pack(v[4], v[5]), ad_pack(v[6], v[7])));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -155,7 +168,7 @@ __device__ __forceinline__ float block_amax(const float (&x)[8]) {
 
 // Eight values as bytes, by their block's multiplier and random bits.  ROOT: values of which none is negative
 // and a nonzero one does not become zero: what lies under the grid's first value is taken for it.
-template <bool ROOT>
+template <bool ROOT, bool NT>
 __device__ __forceinline__ void keep8(void* dst, int64_t at, int n, bool wide, float s, const float (&x)[8], const uint32_t (&bits)[8]) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
@@ -169,7 +182,8 @@ __device__ __forceinline__ void keep8(void* dst, int64_t at, int n, bool wide, f
     }
     uint8_t* p = static_cast<uint8_t*>(dst) + at;
     if (wide && n == 8) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        if (NT) st_nt8(p, w[0], w[1]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++)
@@ -185,9 +199,13 @@ __device__ __forceinline__ void moments(const AdamArgs& a, float g, float& m, fl
     v = a.b2 * v + a.one_b2 * g * g;
 }
 
-template <bool EIGHT>
+// NT: stores, and with 8-bit states loads too, go past the caches, where a launch moves more than stays in the
+// last-level one.  277M bf16 elements, 8 bits: 545 us through the caches, 538 with the stores past them, 524
+// with both; 58M with masters, 32 bits: 345, 321 and 333 us.
+template <bool EIGHT, bool NT>
 __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
     constexpr int H = EIGHT ? 2 : 1, CHUNK = chunk_of(EIGHT);
+    constexpr bool NTL = NT && EIGHT;
     int lo = 0, hi = a.count - 1;  // the tensor of this chunk
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -203,19 +221,19 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
     for (int h = 0; h < H; h++) {
         const int64_t at = at0 + h * 2048;
         n[h] = t.n - at >= 8 ? 8 : t.n > at ? (int)(t.n - at) : 0;
-        if (t.master) load8<true>(t.master, at, n[h], wide, p[h]);
-        else if (t.param32) load8<true>(t.param, at, n[h], wide, p[h]);
-        else load8<false>(t.param, at, n[h], wide, p[h]);
-        if (t.grad32) load8<true>(t.grad, at, n[h], wide, g[h]);
-        else load8<false>(t.grad, at, n[h], wide, g[h]);
+        if (t.master) load8<true, NTL>(t.master, at, n[h], wide, p[h]);
+        else if (t.param32) load8<true, NTL>(t.param, at, n[h], wide, p[h]);
+        else load8<false, NTL>(t.param, at, n[h], wide, p[h]);
+        if (t.grad32) load8<true, NTL>(t.grad, at, n[h], wide, g[h]);
+        else load8<false, NTL>(t.grad, at, n[h], wide, g[h]);
         if (EIGHT) {
             dm[h] = n[h] > 0 ? t.m_scales[at / AB] : 0.0f;
             dv[h] = n[h] > 0 ? t.v_scales[at / AB] : 0.0f;
             load8_fp8(t.m, at, n[h], wide, m[h]);
             load8_fp8(t.v, at, n[h], wide, v[h]);
         } else {
-            load8<true>(t.m, at, n[h], wide, m[h]);
-            load8<true>(t.v, at, n[h], wide, v[h]);
+            load8<true, NTL>(t.m, at, n[h], wide, m[h]);
+            load8<true, NTL>(t.v, at, n[h], wide, v[h]);
         }
     }
     const float lr = a.lr_device ? global_at(a.lr_device, 0) : a.lr;
@@ -247,12 +265,12 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
             p[h][i] = p[h][i] - lr * (d + a.decay * p[h][i]);
         }
         const int64_t at = at0 + h * 2048;
-        if (t.master) store8<true>(t.master, at, n[h], wide, p[h]);
-        if (t.param32) store8<true>(t.param, at, n[h], wide, p[h]);
-        else store8<false>(t.param, at, n[h], wide, p[h]);
+        if (t.master) store8<true, NT>(t.master, at, n[h], wide, p[h]);
+        if (t.param32) store8<true, NT>(t.param, at, n[h], wide, p[h]);
+        else store8<false, NT>(t.param, at, n[h], wide, p[h]);
         if (!EIGHT) {
-            store8<true>(t.m, at, n[h], wide, m[h]);
-            store8<true>(t.v, at, n[h], wide, v[h]);
+            store8<true, NT>(t.m, at, n[h], wide, m[h]);
+            store8<true, NT>(t.v, at, n[h], wide, v[h]);
         }
     }
     if (!EIGHT) return;
@@ -272,8 +290,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
         uint32_t bits[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) bits[i] = mix(base + i);
-        keep8<false>(t.m, at, n[h], wide, sm, m[h], bits);
-        keep8<true>(t.v, at, n[h], wide, sr, r[h], bits);
+        keep8<false, NT>(t.m, at, n[h], wide, sm, m[h], bits);
+        keep8<true, NT>(t.v, at, n[h], wide, sr, r[h], bits);
     }
 }
 
@@ -311,6 +329,7 @@ extern "C" fp8q_status_t adamw_step(const fp8q_adamw_tensor_t* tensors, int32_t 
     }
     for (int32_t i = 0; i < count;) {
         int64_t chunks = 0;
+        double bytes = 0.0;  // that the launch reads and writes
         a.count = 0;
         for (; i < count && a.count < ADAMW_TENSORS; i++) {
             const fp8q_adamw_tensor_t& t = tensors[i];
@@ -324,11 +343,15 @@ extern "C" fp8q_status_t adamw_step(const fp8q_adamw_tensor_t* tensors, int32_t 
             to.wide = fp8q_aligned(t.param, 16) && fp8q_aligned(t.master, 16) && fp8q_aligned(t.grad, 16) &&
                       fp8q_aligned(t.exp_avg, eight ? 8 : 16) && fp8q_aligned(t.exp_avg_sq, eight ? 8 : 16);
             chunks += more;
+            bytes += (double)t.n * ((eight ? 4 : 16) + (to.param32 ? 8 : 4) + (to.grad32 ? 4 : 2) + (t.master ? 6 : 0));
             a.chunk_end[a.count++] = chunks;
         }
         if (a.count == 0) break;
-        if (eight) adamw_kernel<true><<<dim3((unsigned)chunks), dim3(256), 0, stream>>>(a);
-        else adamw_kernel<false><<<dim3((unsigned)chunks), dim3(256), 0, stream>>>(a);
+        const dim3 grid((unsigned)chunks), block(256);
+        if (eight && bytes > kStreamBytes) adamw_kernel<true, true><<<grid, block, 0, stream>>>(a);
+        else if (eight) adamw_kernel<true, false><<<grid, block, 0, stream>>>(a);
+        else if (bytes > kStreamBytes) adamw_kernel<false, true><<<grid, block, 0, stream>>>(a);
+        else adamw_kernel<false, false><<<grid, block, 0, stream>>>(a);
         FP8Q_CHECK_LAUNCH();
     }
     return FP8Q_OK;
