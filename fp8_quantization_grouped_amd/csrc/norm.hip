@@ -64,11 +64,12 @@ __device__ __forceinline__ float rstd_of(float sum, float cols, float eps) { ret
 // Where the sum of squares has overflowed: from the squares' sum of h * 2^-80; eps is far below them.
 __device__ __forceinline__ float rstd_of_shrunk(float sum, float cols) { return kShrink / sqrtf(sum / cols); }
 
-// Eight consecutive elements from 8 c on of a row of 8 or more, zeros past its end.  WIDE: rows are whole
+// Eight consecutive elements from 8 c on of a row of 8 or more, zeros past its end.  ACC & WIDE: rows are whole
 // chunks that start on 16 bytes; else a wide access need not be aligned, and a chunk that the row's end cuts
 // is read as the row's last eight, which stay inside it in one access, and moved down: reading it by elements
 // costs the loop 7 registers for every such load.  20000 x 5457 in the backward: 322 us where it was moved at
 // the load, 271 us where it is used.
+constexpr int WIDE = 1, PAST = 2;  // PAST: past the caches
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
@@ -76,29 +77,34 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 // load_chunk only reads; settle moves a cut chunk down, where it is used: the loads ahead of it stay in flight.
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int c, int cols) {
-    if (WIDE) return *reinterpret_cast<const uint4*>(row + 8 * c);
+    if (ACC & WIDE) return ACC & PAST ? ld_nt16(row + 8 * c) : *reinterpret_cast<const uint4*>(row + 8 * c);
     const int over = 8 * c + 8 - cols;
-    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(row + 8 * c - (over > 0 ? over : 0));
+    const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + 8 * c - (over > 0 ? over : 0));
+    const u32x4_any v = ACC & PAST ? __builtin_nontemporal_load(p) : *p;
     return make_uint4(v.x, v.y, v.z, v.w);
 }
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ uint4 settle(uint4 v, int c, int cols) {
     const int over = 8 * c + 8 - cols;
-    if (WIDE || over <= 0 || over >= 8) return v;
+    if ((ACC & WIDE) || over <= 0 || over >= 8) return v;
     uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
     const int k = 16 * over;  // bits, under 128
     lo = k >= 64 ? hi >> (k - 64) : lo >> k | hi << (64 - k);
     hi = k >= 64 ? 0 : hi >> k;
     return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
 }
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ void store_chunk(uint16_t* row, int c, int cols, uint4 v) {
-    if (WIDE) {
+    if ((ACC & WIDE) && (ACC & PAST)) {
+        st_nt16(row + 8 * c, v);
+    } else if (ACC & WIDE) {
         *reinterpret_cast<uint4*>(row + 8 * c) = v;
     } else if (8 * c + 8 <= cols) {
-        *reinterpret_cast<u32x4_any*>(row + 8 * c) = u32x4_any{v.x, v.y, v.z, v.w};
+        u32x4_any* p = reinterpret_cast<u32x4_any*>(row + 8 * c);
+        if (ACC & PAST) __builtin_nontemporal_store(u32x4_any{v.x, v.y, v.z, v.w}, p);
+        else *p = u32x4_any{v.x, v.y, v.z, v.w};
     } else {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -106,12 +112,16 @@ __device__ __forceinline__ void store_chunk(uint16_t* row, int c, int cols, uint
             if (8 * c + i < cols) row[8 * c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
 }
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ void store_bytes(uint8_t* row, int c, int cols, uint32_t a, uint32_t b) {
-    if (WIDE) {
+    if ((ACC & WIDE) && (ACC & PAST)) {
+        st_nt8(row + 8 * c, a, b);
+    } else if (ACC & WIDE) {
         *reinterpret_cast<uint2*>(row + 8 * c) = make_uint2(a, b);
     } else if (8 * c + 8 <= cols) {
-        *reinterpret_cast<u32x2_any*>(row + 8 * c) = u32x2_any{a, b};
+        u32x2_any* p = reinterpret_cast<u32x2_any*>(row + 8 * c);
+        if (ACC & PAST) __builtin_nontemporal_store(u32x2_any{a, b}, p);
+        else *p = u32x2_any{a, b};
     } else {
 #pragma unroll
         for (int i = 0; i < 7; i++)
@@ -128,40 +138,47 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {  // to the nearest
 __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ void load_floats(const float* row, int c, int cols, float (&f)[8]) {
-    const int over = WIDE ? 0 : 8 * c + 8 - cols;
-    const float* p = row + 8 * c - (over > 0 ? over : 0);
-    const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
+    const int over = ACC & WIDE ? 0 : 8 * c + 8 - cols;
+    const f32x4_any* p = reinterpret_cast<const f32x4_any*>(row + 8 * c - (over > 0 ? over : 0));
+    const f32x4_any a = ACC & PAST ? __builtin_nontemporal_load(p) : p[0], b = ACC & PAST ? __builtin_nontemporal_load(p + 1) : p[1];
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ void settle(float (&f)[8], int c, int cols) {
     const int over = 8 * c + 8 - cols;
-    if (WIDE || over <= 0 || over >= 8) return;
+    if ((ACC & WIDE) || over <= 0 || over >= 8) return;
 #pragma unroll
     for (int k = 4; k > 0; k >>= 1)
 #pragma unroll
         for (int i = 0; i < 8; i++) f[i] = over & k ? (i + k < 8 ? f[i + k] : 0.0f) : f[i];
 }
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ void store_floats(float* row, int c, int cols, const float (&f)[8]) {
-    if (WIDE || 8 * c + 8 <= cols) {
-        *reinterpret_cast<f32x4_any*>(row + 8 * c) = f32x4_any{f[0], f[1], f[2], f[3]};
-        *reinterpret_cast<f32x4_any*>(row + 8 * c + 4) = f32x4_any{f[4], f[5], f[6], f[7]};
+    if ((ACC & WIDE) || 8 * c + 8 <= cols) {
+        f32x4_any* p = reinterpret_cast<f32x4_any*>(row + 8 * c);
+        const f32x4_any a = {f[0], f[1], f[2], f[3]}, b = {f[4], f[5], f[6], f[7]};
+        if (ACC & PAST) {
+            __builtin_nontemporal_store(a, p);
+            __builtin_nontemporal_store(b, p + 1);
+        } else {
+            p[0] = a;
+            p[1] = b;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 7; i++)
             if (8 * c + i < cols) row[8 * c + i] = f[i];
     }
 }
-template <bool WIDE>
+template <int ACC>
 __device__ __forceinline__ void load_weight(const void* w, bool w32, int c, int cols, float (&f)[8]) {
     if (w32) {
-        load_floats<WIDE>(static_cast<const float*>(w), c, cols, f);
-        settle<WIDE>(f, c, cols);
+        load_floats<ACC & WIDE>(static_cast<const float*>(w), c, cols, f);
+        settle<ACC>(f, c, cols);
     } else {
-        unpack(settle<WIDE>(load_chunk<WIDE>(static_cast<const uint16_t*>(w), c, cols), c, cols), f);
+        unpack(settle<ACC>(load_chunk<ACC & WIDE>(static_cast<const uint16_t*>(w), c, cols), c, cols), f);
     }
 }
 
@@ -191,7 +208,7 @@ __device__ __forceinline__ float across(float v, float* red) {
 }
 
 // Rows held in registers: WPR waves a row, NV chunks of 8 elements a lane.
-template <int SC, int FMT, int WPR, int NV, bool WIDE>
+template <int SC, int FMT, int WPR, int NV, int ACC>
 __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const NormArgs p) {
     constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR, TPR = 64 * WPR;
     __shared__ float red[3][WAVES];
@@ -207,29 +224,29 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
     for (int j = 0; j < NV; j++) {
         const int c = t + j * TPR;
         h[j] = res[j] = make_uint4(0, 0, 0, 0);
-        if (8 * c < cols) h[j] = load_chunk<WIDE>(x, c, cols);
+        if (8 * c < cols) h[j] = load_chunk<ACC>(x, c, cols);
     }
     if (p.residual) {
         const uint16_t* from = p.residual + row * p.ld_res;
 #pragma unroll
         for (int j = 0; j < NV; j++)
-            if (8 * (t + j * TPR) < cols) res[j] = load_chunk<WIDE>(from, t + j * TPR, cols);
+            if (8 * (t + j * TPR) < cols) res[j] = load_chunk<ACC>(from, t + j * TPR, cols);
     }
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         const int c = t + j * TPR;
         float f[8];
-        h[j] = settle<WIDE>(h[j], c, cols);
+        h[j] = settle<ACC>(h[j], c, cols);
         unpack(h[j], f);
         if (p.residual) {
             float g[8];
-            unpack(settle<WIDE>(res[j], c, cols), g);
+            unpack(settle<ACC>(res[j], c, cols), g);
 #pragma unroll
             for (int i = 0; i < 8; i++) f[i] += g[i];
             h[j] = pack(f);
             unpack(h[j], f);
-            if (8 * c < cols) store_chunk<WIDE>(p.h + row * p.ld_h, c, cols, h[j]);
+            if (8 * c < cols) store_chunk<ACC>(p.h + row * p.ld_h, c, cols, h[j]);
         }
 #pragma unroll
         for (int i = 0; i < 8; i++) sum += f[i] * f[i];
@@ -258,11 +275,11 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
         float w[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = 0.0f;
-        if (8 * c < cols) load_weight<WIDE>(p.w, p.w32, c, cols, w);
+        if (8 * c < cols) load_weight<ACC>(p.w, p.w32, c, cols, w);
         unpack(h[j], y[j]);
 #pragma unroll
         for (int i = 0; i < 8; i++) y[j][i] = y[j][i] * rstd * w[i];
-        if (p.y && 8 * c < cols) store_chunk<WIDE>(p.y + row * p.ld_y, c, cols, pack(y[j]));
+        if (p.y && 8 * c < cols) store_chunk<ACC>(p.y + row * p.ld_y, c, cols, pack(y[j]));
         if (SC == FP8Q_NORM_NONE) continue;
         float m = 0.0f;
 #pragma unroll
@@ -276,7 +293,7 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
         const float s = scale_from_amax<FMT>(m), sm = s * Fmt<FMT>::mult;
         if (8 * c < cols) {
             if ((t & 15) == 0) p.scales[c / 16 * p.ld_s + row] = 1.0f / s;
-            store_bytes<WIDE>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
+            store_bytes<ACC>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
                               enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
         }
     }
@@ -287,18 +304,23 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
     for (int j = 0; j < NV; j++) {
         const int c = t + j * TPR;
         if (8 * c < cols)
-            store_bytes<WIDE>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
+            store_bytes<ACC>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
                               enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
     }
 }
 
 template <int SC, int FMT, int WPR, int NV>
-static void launch_norm(const NormArgs& p, bool wide, hipStream_t stream) {
+static void launch_norm(const NormArgs& p, int acc, hipStream_t stream) {
     constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR;
     const dim3 grid((unsigned)((p.rows + RPB - 1) / RPB)), block(64 * WAVES);
-    if (wide) norm_kernel<SC, FMT, WPR, NV, true><<<grid, block, 0, stream>>>(p);
-    else norm_kernel<SC, FMT, WPR, NV, false><<<grid, block, 0, stream>>>(p);
+    if (acc == (WIDE | PAST)) norm_kernel<SC, FMT, WPR, NV, WIDE | PAST><<<grid, block, 0, stream>>>(p);
+    else if (acc == WIDE) norm_kernel<SC, FMT, WPR, NV, WIDE><<<grid, block, 0, stream>>>(p);
+    else if (acc == PAST) norm_kernel<SC, FMT, WPR, NV, PAST><<<grid, block, 0, stream>>>(p);
+    else norm_kernel<SC, FMT, WPR, NV, 0><<<grid, block, 0, stream>>>(p);
 }
+
+// More than the last-level cache holds of what a call reads and writes: none of it will be found there.
+static inline bool past_caches(int64_t rows, int64_t cols, int bytes) { return (double)rows * cols * bytes > 2.0 * kStreamBytes; }
 
 // Rows that start on whole vectors of 8 elements; none where there is no matrix.
 static inline bool fp8q_rows_wide(const void* p, int64_t ld, uintptr_t align) { return !p || (ld % 8 == 0 && fp8q_aligned(p, align)); }
@@ -308,18 +330,20 @@ __global__ void norm_generic_kernel(const NormArgs p);
 
 template <int SC, int FMT>
 static void pick_norm(const NormArgs& p, hipStream_t stream) {
+    const int each = (p.residual ? 6 : 2) + (p.y ? 2 : 0) + (p.q ? 1 : 0);  // bytes of an element
     const bool wide = p.cols % 8 == 0 && fp8q_rows_wide(p.x, p.ld_x, 16) && fp8q_rows_wide(p.residual, p.ld_res, 16) &&
                       fp8q_rows_wide(p.h, p.ld_h, 16) && fp8q_rows_wide(p.y, p.ld_y, 16) && fp8q_rows_wide(p.q, p.ld_q, 8) &&
                       fp8q_aligned(p.w, 16);
+    const int acc = (wide ? WIDE : 0) | (past_caches(p.rows, p.cols, each) ? PAST : 0);
     if (p.cols < 8) norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
-    else if (p.rows <= 256 && p.cols > 1024 && p.cols <= 8192) launch_norm<SC, FMT, 16, 1>(p, wide, stream);
-    else if (p.cols <= 512) launch_norm<SC, FMT, 1, 1>(p, wide, stream);
-    else if (p.cols <= 1024) launch_norm<SC, FMT, 1, 2>(p, wide, stream);
-    else if (p.cols <= 2048) launch_norm<SC, FMT, 1, 4>(p, wide, stream);
-    else if (p.cols <= 4096) launch_norm<SC, FMT, 2, 4>(p, wide, stream);
-    else if (p.cols <= 8192) launch_norm<SC, FMT, 4, 4>(p, wide, stream);
-    else if (p.cols <= 16384) launch_norm<SC, FMT, 8, 4>(p, wide, stream);
-    else if (p.cols <= 32768) launch_norm<SC, FMT, 16, 4>(p, wide, stream);
+    else if (p.rows <= 256 && p.cols > 1024 && p.cols <= 8192) launch_norm<SC, FMT, 16, 1>(p, acc, stream);
+    else if (p.cols <= 512) launch_norm<SC, FMT, 1, 1>(p, acc, stream);
+    else if (p.cols <= 1024) launch_norm<SC, FMT, 1, 2>(p, acc, stream);
+    else if (p.cols <= 2048) launch_norm<SC, FMT, 1, 4>(p, acc, stream);
+    else if (p.cols <= 4096) launch_norm<SC, FMT, 2, 4>(p, acc, stream);
+    else if (p.cols <= 8192) launch_norm<SC, FMT, 4, 4>(p, acc, stream);
+    else if (p.cols <= 16384) launch_norm<SC, FMT, 8, 4>(p, acc, stream);
+    else if (p.cols <= 32768) launch_norm<SC, FMT, 16, 4>(p, acc, stream);
     else norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
 }
 
@@ -425,17 +449,17 @@ __device__ __forceinline__ float grad_at(const void* g, int64_t i) {
     return G32 ? static_cast<const float*>(g)[i] : bf16_f(static_cast<const uint16_t*>(g)[i]);
 }
 
-template <bool G32, bool WIDE>
+template <bool G32, int ACC>
 struct Eight {  // eight gradients or weights
     uint4 v[G32 ? 2 : 1];
     __device__ __forceinline__ void load(const void* g, int64_t at, int c, int cols) {
         if (G32) {
             float f[8];
-            load_floats<WIDE>(static_cast<const float*>(g) + at, c, cols, f);
+            load_floats<ACC>(static_cast<const float*>(g) + at, c, cols, f);
             v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
             v[G32 ? 1 : 0] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
         } else {
-            v[0] = load_chunk<WIDE>(static_cast<const uint16_t*>(g) + at, c, cols);
+            v[0] = load_chunk<ACC>(static_cast<const uint16_t*>(g) + at, c, cols);
         }
     }
     __device__ __forceinline__ void clear() {
@@ -455,20 +479,20 @@ struct Eight {  // eight gradients or weights
         if (G32) {
             float f[8];
             get(f);
-            settle<WIDE>(f, c, cols);
+            settle<ACC>(f, c, cols);
             v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
             v[G32 ? 1 : 0] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
         } else {
-            v[0] = settle<WIDE>(v[0], c, cols);
+            v[0] = settle<ACC>(v[0], c, cols);
         }
     }
 };
 
 // What a lane has of a row.
-template <bool G32, int NV, bool WIDE>
+template <bool G32, int NV, int ACC>
 struct BackRow {
     uint4 h[NV];
-    Eight<G32, WIDE> dy[NV];
+    Eight<G32, ACC> dy[NV];
     float rstd;
     __device__ __forceinline__ void load(const NormBackArgs& p, int64_t row, int t, int tpr) {
         const bool ok = row < p.rows;
@@ -480,7 +504,7 @@ struct BackRow {
             h[j] = make_uint4(0, 0, 0, 0);
             dy[j].clear();
             if (8 * c < cols) {
-                h[j] = load_chunk<WIDE>(p.h + row * p.ld_h, c, cols);
+                h[j] = load_chunk<ACC>(p.h + row * p.ld_h, c, cols);
                 dy[j].load(p.dy, row * p.ld_dy, c, cols);
             }
         }
@@ -490,7 +514,7 @@ struct BackRow {
 // Rows held in registers: p.waves waves a row, NV chunks of 8 columns a lane, the same ones of each of its
 // rows, whose sums for dw it keeps; a row's loads go out while the one before it is worked on.  The rows of a
 // block's waves are added at the end.
-template <bool G32, bool W32, int NV, bool WIDE>
+template <bool G32, bool W32, int NV, int ACC>
 __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
     __shared__ float red[2][16];
     extern __shared__ float sums[];  // [rows of a block less one][8][threads of a row]
@@ -501,7 +525,7 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
     for (int j = 0; j < NV; j++)
 #pragma unroll
         for (int i = 0; i < 8; i++) acc[j][i] = 0.0f;
-    Eight<W32, WIDE> weight[NV];
+    Eight<W32, ACC & WIDE> weight[NV];
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         const int c = t + j * tpr;
@@ -509,14 +533,14 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
         if (8 * c < p.cols) weight[j].load(p.w, 0, c, (int)p.cols);
         weight[j].settle_all(c, (int)p.cols);
     }
-    BackRow<G32, NV, WIDE> cur, next;
+    BackRow<G32, NV, ACC> cur, next;
     int64_t r0 = (int64_t)blockIdx.x * rpb;
     cur.load(p, r0 + mine, t, tpr);
     const float inv_cols = 1.0f / (float)p.cols;
     for (int turn = 0; r0 < p.rows; turn ^= 1) {  // the rows of a block stay together, for its barriers
         const int64_t row = r0 + mine;
         const int cols = row < p.rows ? (int)p.cols : 0;
-        Eight<G32, WIDE> dh[NV];  // used after the row's sum, so not a row ahead
+        Eight<G32, ACC> dh[NV];  // used after the row's sum, so not a row ahead
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             dh[j].clear();
@@ -530,7 +554,7 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
             const int c = t + j * tpr;
             float x[8], g[8], w[8];
             weight[j].get(w);
-            cur.h[j] = settle<WIDE>(cur.h[j], c, (int)p.cols);
+            cur.h[j] = settle<ACC>(cur.h[j], c, (int)p.cols);
             cur.dy[j].settle_all(c, (int)p.cols);
             unpack(cur.h[j], x);
             cur.dy[j].get(g);
@@ -562,8 +586,8 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
             dh[j].get(e);
 #pragma unroll
             for (int i = 0; i < 8; i++) e[i] += cur.rstd * (g[i] * w[i] - (x[i] * cur.rstd) * mean);
-            if (G32) store_floats<WIDE>(static_cast<float*>(p.dx) + row * p.ld_dx, c, cols, e);
-            else store_chunk<WIDE>(static_cast<uint16_t*>(p.dx) + row * p.ld_dx, c, cols, pack(e));
+            if (G32) store_floats<ACC>(static_cast<float*>(p.dx) + row * p.ld_dx, c, cols, e);
+            else store_chunk<ACC>(static_cast<uint16_t*>(p.dx) + row * p.ld_dx, c, cols, pack(e));
         }
         cur = next;
     }
@@ -582,7 +606,7 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
 #pragma unroll
                     for (int i = 0; i < 8; i++) acc[j][i] += sums[(k * 8 + i) * tpr + t];
         }
-        if (mine == 0 && 8 * c < p.cols) store_floats<WIDE>(part, c, (int)p.cols, acc[j]);
+        if (mine == 0 && 8 * c < p.cols) store_floats<ACC & WIDE>(part, c, (int)p.cols, acc[j]);
     }
 }
 
@@ -649,17 +673,24 @@ static inline NormBackPlan norm_back_plan(int64_t rows, int64_t cols) {
     return p;
 }
 
+template <bool G32, bool W32, int NV>
+static void launch_norm_back_rows(const NormBackArgs& p, int acc, dim3 grid, dim3 block, size_t lds, hipStream_t stream) {
+    if (acc == (WIDE | PAST)) norm_back_kernel<G32, W32, NV, WIDE | PAST><<<grid, block, lds, stream>>>(p);
+    else if (acc == WIDE) norm_back_kernel<G32, W32, NV, WIDE><<<grid, block, lds, stream>>>(p);
+    else if (acc == PAST) norm_back_kernel<G32, W32, NV, PAST><<<grid, block, lds, stream>>>(p);
+    else norm_back_kernel<G32, W32, NV, 0><<<grid, block, lds, stream>>>(p);
+}
+
 template <bool G32, bool W32>
 static void launch_norm_back(const NormBackArgs& p, const NormBackPlan& n, hipStream_t stream) {
     const bool wide = p.cols % 8 == 0 && fp8q_rows_wide(p.h, p.ld_h, 16) && fp8q_rows_wide(p.dy, p.ld_dy, 16) &&
                       fp8q_rows_wide(p.dh, p.ld_dh, 16) && fp8q_rows_wide(p.dx, p.ld_dx, 16) && fp8q_aligned(p.w, 16);
+    const int acc = (wide ? WIDE : 0) | (past_caches(p.rows, p.cols, 2 + (G32 ? 4 : 2) * (p.dh ? 3 : 2)) ? PAST : 0);
     const dim3 grid((unsigned)n.blocks), block(64 * n.waves * n.rows);
     const size_t lds = (size_t)(n.rows - 1) * 8 * 64 * n.waves * 4;
     if (n.chunks == 0) norm_back_generic_kernel<G32><<<grid, dim3(256), 0, stream>>>(p);
-    else if (n.chunks == 1 && wide) norm_back_kernel<G32, W32, 1, true><<<grid, block, lds, stream>>>(p);
-    else if (n.chunks == 1) norm_back_kernel<G32, W32, 1, false><<<grid, block, lds, stream>>>(p);
-    else if (wide) norm_back_kernel<G32, W32, 2, true><<<grid, block, lds, stream>>>(p);
-    else norm_back_kernel<G32, W32, 2, false><<<grid, block, lds, stream>>>(p);
+    else if (n.chunks == 1) launch_norm_back_rows<G32, W32, 1>(p, acc, grid, block, lds, stream);
+    else launch_norm_back_rows<G32, W32, 2>(p, acc, grid, block, lds, stream);
 }
 
 static inline bool dtype_ok(int d) { return d == FP8Q_OUT_BF16 || d == FP8Q_OUT_FP32; }
