@@ -189,21 +189,35 @@ __device__ __forceinline__ int64_t xcd_run(unsigned b, unsigned n) {
     return (int64_t)x * q + (x < r ? x : r) + b / 8;
 }
 
-// Sum (SUM) or maximum over the WPR waves of a row; red: a float for each of the block's waves.
+// Sums (SUM) and maxima over a wave, the same in all lanes: by DPP 1 and 2 lanes away, then mirrored in 8 and
+// in 16, then the four rows of 16.
+template <bool SUM>
+__device__ __forceinline__ float join(float a, float b) { return SUM ? a + b : fmaxf(a, b); }
+template <bool SUM, int CTRL>
+__device__ __forceinline__ float join_dpp(float v) {
+    return join<SUM>(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false)));
+}
+template <bool SUM>
+__device__ __forceinline__ float over16(float v) {
+    return join_dpp<SUM, 0x140>(join_dpp<SUM, 0x141>(join_dpp<SUM, 0x4E>(join_dpp<SUM, 0xB1>(v))));
+}
+template <bool SUM>
+__device__ __forceinline__ float over_wave(float v) {
+    v = over16<SUM>(v);
+    const auto lane = [&](int i) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), i)); };
+    return join<SUM>(join<SUM>(lane(0), lane(16)), join<SUM>(lane(32), lane(48)));
+}
+// Over the WPR waves of a row; red: a float for each of the block's waves.
 template <int WPR, bool SUM>
 __device__ __forceinline__ float across(float v, float* red) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const float o = __shfl_xor(v, off, 64);
-        v = SUM ? v + o : fmaxf(v, o);
-    }
+    v = over_wave<SUM>(v);
     if (WPR == 1) return v;
     const int wave = threadIdx.x >> 6, w0 = wave / WPR * WPR;
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
     v = red[w0];
 #pragma unroll
-    for (int w = 1; w < WPR; w++) v = SUM ? v + red[w0 + w] : fmaxf(v, red[w0 + w]);
+    for (int w = 1; w < WPR; w++) v = join<SUM>(v, red[w0 + w]);
     return v;
 }
 
@@ -268,7 +282,7 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
         if (WPR > 1) __syncthreads();  // as many barriers as in the other case
     }
     if (t == 0 && row_ok && p.rstd) p.rstd[row] = rstd;
-    float y[NV][8], amax = 0.0f;
+    float y[NV][8], amax = 0.0f, block_max[NV];
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         const int c = t + j * TPR;
@@ -284,17 +298,26 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(y[j][i]));
-        if (SC == FP8Q_NORM_ROW) {
-            amax = fmaxf(amax, m);
-            continue;
-        }
+        if (SC == FP8Q_NORM_ROW) amax = fmaxf(amax, m);
+        else block_max[j] = over16<false>(m);  // 16 lanes have a block
+    }
+    if (SC == FP8Q_NORM_BLOCK) {
+        // the 16 lanes have NV blocks: 16 / NV lanes form each one's factors
+        constexpr int EACH = 16 / NV;
+        const int which = (t & 15) / EACH;
+        float m = block_max[0];
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));  // 16 lanes have a block
-        const float s = scale_from_amax<FMT>(m), sm = s * Fmt<FMT>::mult;
-        if (8 * c < cols) {
-            if ((t & 15) == 0) p.scales[c / 16 * p.ld_s + row] = 1.0f / s;
-            store_bytes<ACC>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
-                              enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
+        for (int j = 1; j < NV; j++) m = which == j ? block_max[j] : m;
+        const float mine = scale_from_amax<FMT>(m);
+        const int first = t / 16 + which * (TPR / 16);  // the block
+        if (t % EACH == 0 && first * NB < cols) p.scales[first * p.ld_s + row] = 1.0f / mine;
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int c = t + j * TPR;
+            const float sm = (NV == 1 ? mine : __shfl(mine, (t & 48) + j * EACH, 64)) * Fmt<FMT>::mult;
+            if (8 * c < cols)
+                store_bytes<ACC>(p.q + row * p.ld_q, c, cols, enc4<FMT>(y[j][0] * sm, y[j][1] * sm, y[j][2] * sm, y[j][3] * sm),
+                                 enc4<FMT>(y[j][4] * sm, y[j][5] * sm, y[j][6] * sm, y[j][7] * sm));
         }
     }
     if (SC != FP8Q_NORM_ROW) return;
@@ -668,8 +691,10 @@ static inline NormBackPlan norm_back_plan(int64_t rows, int64_t cols) {
         p.waves = (int)((cols + 512 * p.chunks - 1) / (512 * p.chunks));
         p.rows = 16 / p.waves;
     }
-    p.blocks = (rows + p.rows - 1) / p.rows;
-    p.blocks = p.blocks < 512 ? p.blocks : 512;
+    // at most 512 blocks, each as often as the others: two for a CU at a time, and every block's sums of dw are
+    // written and read once more
+    const int64_t groups = (rows + p.rows - 1) / p.rows, turns = (groups + 511) / 512;
+    p.blocks = turns ? (groups + turns - 1) / turns : 0;
     return p;
 }
 
