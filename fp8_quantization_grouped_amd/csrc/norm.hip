@@ -691,9 +691,9 @@ static inline NormBackPlan norm_back_plan(int64_t rows, int64_t cols) {
         p.waves = (int)((cols + 512 * p.chunks - 1) / (512 * p.chunks));
         p.rows = 16 / p.waves;
     }
-    // at most 512 blocks, each as often as the others: two for a CU at a time, and every block's sums of dw are
+    // at most 256 blocks, each as often as the others: one for a CU at a time, and every block's sums of dw are
     // written and read once more
-    const int64_t groups = (rows + p.rows - 1) / p.rows, turns = (groups + 511) / 512;
+    const int64_t groups = (rows + p.rows - 1) / p.rows, turns = (groups + 255) / 256;
     p.blocks = turns ? (groups + turns - 1) / turns : 0;
     return p;
 }
