@@ -12,6 +12,7 @@
 namespace fp8q {
 
 constexpr int RG_MAX_E = 1024, RG_MAX_K = 32;
+constexpr int BAL_WAVES = 8;  // of a block that sums probabilities
 
 struct RouteGradArgs {
     const void* logits;
@@ -62,6 +63,18 @@ __device__ __forceinline__ float row_sum(float v) { return over_row<L, true>(v);
 template <int L>
 __device__ __forceinline__ float row_max(float v) { return over_row<L, false>(v); }
 
+// Sum over the 64 / L rows of a wave, in each of its lanes: by rotations of 16 lanes, then across these.
+template <int L>
+__device__ __forceinline__ float over_rows(float v) {
+    if (L <= 8) v += dpp<0x128>(v);  // row_ror 8
+    if (L <= 4) v += dpp<0x124>(v);
+    if (L <= 2) v += dpp<0x122>(v);
+    if (L <= 1) v += dpp<0x121>(v);
+    if (L <= 16) v += __shfl_xor(v, 16, 64);
+    if (L <= 32) v += __shfl_xor(v, 32, 64);
+    return v;
+}
+
 // exp(x) for x <= 0 within two units and |x| / 4 of the last place: 2^(x log2(e)), the product's rounding made
 // good to first order.  Results under 2^-126 are zero.
 __device__ __forceinline__ float exp_neg(float x) {
@@ -71,22 +84,40 @@ __device__ __forceinline__ float exp_neg(float x) {
     return fmaf(e, r * 0.693147181f, e);
 }
 
-// End of sequence s, inside [0, T] whatever is stored.
-__device__ __forceinline__ int64_t seq_end(const RouteGradArgs& p, int s) {
-    if (!p.sequences) return p.T;
-    const int64_t e = p.sequences[s];
-    return e < 0 ? 0 : e > p.T ? p.T : e;
-}
-// Sequence of row r: the first whose end lies behind it, S for rows behind the last.
-__device__ __forceinline__ int seq_of(const RouteGradArgs& p, int64_t r) {
-    if (!p.sequences) return 0;
-    int lo = 0, hi = p.S;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)p.sequences[mid] > r) hi = mid; else lo = mid + 1;
+// The sequences' ends, inside [0, T] whatever is stored.  Lane l of a wave reads the l-th at the kernel's start, so
+// that up to 64 of them are at hand without another load.  All lanes of a wave call these together.
+struct Ends {
+    const int32_t* all;
+    int64_t T;
+    int S, mine;
+    __device__ __forceinline__ explicit Ends(const RouteGradArgs& p) : all(p.sequences), T(p.T), S(p.S), mine(0) {
+        const int lane = threadIdx.x & 63;
+        if (all && lane < S) mine = all[lane];
     }
-    return lo;
-}
+    // Of sequence s, which may differ from lane to lane; 0 for s < 0.
+    __device__ __forceinline__ int64_t end(int s) const {
+        int64_t e = T;
+        if (all) e = S <= 64 ? __shfl(mine, s < 0 ? 0 : s, 64) : all[s < 0 ? 0 : s];
+        return s < 0 || e < 0 ? 0 : e > T ? T : e;
+    }
+    // The sequence of row r, the same in the whole wave: the first whose end lies behind it, S for rows behind
+    // the last; of more than 64, by looking at 64 places at a time.
+    __device__ __forceinline__ int of(int64_t r) const {
+        if (!all) return r < T ? 0 : 1;
+        const int lane = threadIdx.x & 63;
+        if (S <= 64) return __popcll(__ballot(lane < S && (int64_t)mine <= r));
+        int lo = 0, n = S;  // the answer lies in lo .. lo + n
+        while (n > 0) {
+            const int step = (n + 63) / 64, at = lane * step;
+            const int before = __popcll(__ballot(at < n && (int64_t)all[lo + (at < n ? at : 0)] <= r));
+            if (before == 0) return lo;
+            const int skip = (before - 1) * step + 1;
+            lo += skip;
+            n = n - skip < step - 1 ? n - skip : step - 1;
+        }
+        return lo;
+    }
+};
 
 // A row's logits: L lanes with 4 * NV experts each, lane j's at 4 (j + L v) .. + 3; minus infinity past E.
 // They are held as they are read until get.
@@ -188,25 +219,28 @@ __device__ __forceinline__ void scores_of(const float (&l)[N], float (&t)[N], fl
 // sequence of the workspace: both only grow along the rows, so no two pairs share one.  A thread keeps
 // the sums of its experts; rows of the block's waves are added in a fixed order.
 template <int L, int NV, bool F32, bool SIG>
-__global__ __launch_bounds__(256) void balance_kernel(const RouteGradArgs p) {
-    constexpr int R = 64 / L, ROWS = 4 * R, N = 4 * NV;  // rows of a wave and of the block at a time
-    extern __shared__ float lds[];
-    float* sums = lds;                                           // [ROWS][E]
-    int32_t* count = reinterpret_cast<int32_t*>(lds + ROWS * p.E);  // [E]
+__global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGradArgs p) {
+    constexpr int R = 64 / L, ROWS = BAL_WAVES * R, N = 4 * NV;  // rows of a wave and of the block at a time
+    __shared__ float sums[BAL_WAVES][4 * L * NV];
+    __shared__ int32_t count[4 * L * NV];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane % L, mine = wave * R + lane / L;
     const int64_t begin = (int64_t)blockIdx.x * p.rows;
     const int64_t end = begin + p.rows < p.T ? begin + p.rows : p.T;
     int64_t r0 = begin;
-    for (int s = seq_of(p, begin); s < p.S && r0 < end; s++) {
-        const int64_t e1 = seq_end(p, s), r1 = e1 < end ? e1 : end;
+    Logits<L, NV, F32> cur, next;  // a row's loads go out while the one before it is worked on
+    if (r0 + mine < end) cur.load(p, r0 + mine, j);
+    const int64_t id_at = begin * p.k + threadIdx.x;
+    const int first_id = id_at < end * p.k ? p.ids[id_at] : -1;
+    const Ends ends(p);
+    for (int s = ends.of(begin); s < p.S && r0 < end; s++) {
+        const int64_t e1 = ends.end(s), r1 = e1 < end ? e1 : end;
         if (r1 <= r0) continue;
-        for (int i = threadIdx.x; i < p.E; i += 256) count[i] = 0;
+        for (int i = threadIdx.x; i < p.E; i += 64 * BAL_WAVES) count[i] = 0;
         __syncthreads();
         float acc[N];
 #pragma unroll
         for (int i = 0; i < N; i++) acc[i] = 0.0f;
-        Logits<L, NV, F32> cur, next;  // a row's loads go out while the one before it is worked on
-        if (r0 + mine < r1) cur.load(p, r0 + mine, j);
+        if (r0 != begin && r0 + mine < r1) cur.load(p, r0 + mine, j);
         for (int64_t r = r0 + mine; r < r1; r += ROWS) {
             next.load(p, r + ROWS < r1 ? r + ROWS : r, j);
             float l[N], t[N], slope[N], a, b;
@@ -216,22 +250,22 @@ __global__ __launch_bounds__(256) void balance_kernel(const RouteGradArgs p) {
             for (int i = 0; i < N; i++) acc[i] += t[i] * a;
             cur = next;
         }
-        for (int64_t i = r0 * p.k + threadIdx.x; i < r1 * p.k; i += 256) {
-            const int e = p.ids[i];
+        for (int64_t i = id_at; i < r1 * p.k; i += 64 * BAL_WAVES) {
+            if (i < r0 * p.k) continue;
+            const int e = i == id_at ? first_id : p.ids[i];
             if (e >= 0 && e < p.E) atomicAdd(&count[e], 1);  // whole numbers: any order
         }
 #pragma unroll
-        for (int v = 0; v < NV; v++)
+        for (int i = 0; i < N; i++) acc[i] = over_rows<L>(acc[i]);
+        if (lane < L)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int e = 4 * (j + L * v) + i;
-                if (e < p.E) sums[mine * p.E + e] = acc[4 * v + i];
-            }
+            for (int i = 0; i < N; i++) sums[wave][4 * (j + L * (i / 4)) + i % 4] = acc[i];
         __syncthreads();
         const int64_t slot = (int64_t)blockIdx.x + s;
-        for (int e = threadIdx.x; e < p.E; e += 256) {
+        for (int e = threadIdx.x; e < p.E; e += 64 * BAL_WAVES) {
             float a = 0.0f;
-            for (int i = 0; i < ROWS; i++) a += sums[i * p.E + e];
+#pragma unroll
+            for (int i = 0; i < BAL_WAVES; i++) a += sums[i][e];
             p.mass[slot * p.E + e] = a;
             p.part[slot * p.E + e] = count[e];
         }
@@ -246,7 +280,8 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const RouteGradArgs 
     __shared__ float mass[1024], red[16];
     __shared__ int32_t count[1024];
     const int s = blockIdx.x, e = threadIdx.x & (C - 1), row = threadIdx.x / C, rows = blockDim.x / C;
-    const int64_t a = s == 0 ? 0 : seq_end(p, s - 1), b = seq_end(p, s), n = b - a;
+    const Ends ends(p);
+    const int64_t a = ends.end(s - 1), b = ends.end(s), n = b - a;
     float m = 0.0f;
     int32_t k = 0;
     if (n > 0 && e < p.E) {
@@ -303,7 +338,8 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
     int32_t* tag = reinterpret_cast<int32_t*>(parts);
     const int64_t begin = (int64_t)blockIdx.x * p.rows;
     const int64_t end = begin + p.rows < p.T ? begin + p.rows : p.T;
-    int s = p.dloss ? seq_of(p, begin + wave * R + lane / L) - 1 : p.S;
+    const Ends ends(p);
+    int s = p.dloss ? ends.of(begin + wave * R) - 1 : p.S;
     int64_t seq_last = -1;  // end of sequence s
     float dp[N];
 #pragma unroll
@@ -332,23 +368,28 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
                 if (e < p.E) f(c, e, dw[c]);
             }
         };
-        while (s < p.S && row >= seq_last) {  // the row's sequence, and what its loss gives each expert
-            if (++s >= p.S) {
-#pragma unroll
-                for (int i = 0; i < N; i++) dp[i] = 0.0f;
-                break;
+        // the row's sequence, and what its loss gives each expert
+        bool ahead = s < p.S && row >= seq_last, other = ahead;
+        int64_t seq_first = 0;
+        while (__any(ahead)) {
+            if (ahead) s++;
+            const int at = s < p.S ? s : p.S - 1;
+            const int64_t from = ends.end(at - 1), to = ends.end(at);
+            if (ahead) {
+                seq_first = from;
+                seq_last = to;
             }
-            const int64_t from = s == 0 ? 0 : seq_end(p, s - 1);
-            seq_last = seq_end(p, s);
-            if (row >= seq_last) continue;
-            const float n = (float)(seq_last - from);
-            const float over = p.dloss[s] * ((float)p.E / ((float)p.k * n * n));
+            ahead = ahead && s < p.S && row >= seq_last;
+        }
+        if (other) {
+            const float n = (float)(seq_last - seq_first);
+            const float over = s < p.S ? p.dloss[s] * ((float)p.E / ((float)p.k * n * n)) : 0.0f;
 #pragma unroll
             for (int v = 0; v < NV; v++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int e = 4 * (j + L * v) + i;
-                    dp[4 * v + i] = e < p.E ? over * (float)p.counts[(int64_t)s * p.E + e] : 0.0f;
+                    dp[4 * v + i] = s < p.S && e < p.E ? over * (float)p.counts[(int64_t)s * p.E + e] : 0.0f;
                 }
         }
         float t[N], slope[N], a, b;
@@ -469,12 +510,19 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
     }
 }
 
-// Rows of a chunk: enough for a block's waves several times over, at most 512 chunks.
-static inline int64_t balance_rows(int64_t T) {
-    const int64_t r = (T + 511) / 512;
-    return r < 16 ? 16 : r;
+// Lanes of a row by the number of experts, 16 of them to a lane: what a row's lanes do together counts for
+// as many experts as it can.
+static inline int route_lanes(int64_t E) {
+    int l = 1;
+    while (16 * l < E) l *= 2;
+    return l;
 }
-static inline int64_t balance_slots(int64_t T, int64_t S) { return (T + balance_rows(T) - 1) / balance_rows(T) + S; }
+// Rows of a chunk: as many as a block's waves take at a time, or so many that there are 512 chunks.
+static inline int64_t balance_rows(int64_t T, int64_t E) {
+    const int64_t once = BAL_WAVES * 64 / route_lanes(E), r = (T + 511) / 512;
+    return r < once ? once : r;
+}
+static inline int64_t balance_slots(int64_t T, int64_t E, int64_t S) { return (T + balance_rows(T, E) - 1) / balance_rows(T, E) + S; }
 
 template <int L, int NV, bool F32, bool SIG>
 static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
@@ -482,22 +530,24 @@ static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     if (back) p.rows = p.T <= 2048 * ROWS ? ROWS : (p.T + 2048 * ROWS - 1) / (2048 * ROWS) * ROWS;
     const unsigned blocks = (unsigned)((p.T + p.rows - 1) / p.rows);
     if (back) route_back_kernel<L, NV, F32, SIG><<<dim3(blocks), dim3(256), 0, stream>>>(p);
-    else balance_kernel<L, NV, F32, SIG><<<dim3(blocks), dim3(256), (size_t)(ROWS + 1) * p.E * 4, stream>>>(p);
+    else balance_kernel<L, NV, F32, SIG><<<dim3(blocks), dim3(64 * BAL_WAVES), 0, stream>>>(p);
 }
 
-// Lanes of a row by the number of experts, 16 of them to a lane: what a row's lanes do together counts for
-// as many experts as it can.
 template <bool F32, bool SIG>
 static void pick_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
-    if (p.E <= 4) launch_route_grad<1, 1, F32, SIG>(p, back, stream);
-    else if (p.E <= 8) launch_route_grad<1, 2, F32, SIG>(p, back, stream);
-    else if (p.E <= 16) launch_route_grad<1, 4, F32, SIG>(p, back, stream);
-    else if (p.E <= 32) launch_route_grad<2, 4, F32, SIG>(p, back, stream);
-    else if (p.E <= 64) launch_route_grad<4, 4, F32, SIG>(p, back, stream);
-    else if (p.E <= 128) launch_route_grad<8, 4, F32, SIG>(p, back, stream);
-    else if (p.E <= 256) launch_route_grad<16, 4, F32, SIG>(p, back, stream);
-    else if (p.E <= 512) launch_route_grad<32, 4, F32, SIG>(p, back, stream);
-    else launch_route_grad<64, 4, F32, SIG>(p, back, stream);
+    switch (route_lanes(p.E)) {
+        case 1:
+            if (p.E <= 4) launch_route_grad<1, 1, F32, SIG>(p, back, stream);
+            else if (p.E <= 8) launch_route_grad<1, 2, F32, SIG>(p, back, stream);
+            else launch_route_grad<1, 4, F32, SIG>(p, back, stream);
+            break;
+        case 2: launch_route_grad<2, 4, F32, SIG>(p, back, stream); break;
+        case 4: launch_route_grad<4, 4, F32, SIG>(p, back, stream); break;
+        case 8: launch_route_grad<8, 4, F32, SIG>(p, back, stream); break;
+        case 16: launch_route_grad<16, 4, F32, SIG>(p, back, stream); break;
+        case 32: launch_route_grad<32, 4, F32, SIG>(p, back, stream); break;
+        default: launch_route_grad<64, 4, F32, SIG>(p, back, stream); break;
+    }
 }
 
 static void start_route_grad(RouteGradArgs& p, bool f32, bool back, hipStream_t stream) {
@@ -515,7 +565,7 @@ static inline bool rg_wide(const void* p, int64_t ld, int64_t E, bool f32) {
 
 extern "C" size_t moe_balance_workspace_size(int64_t T, int64_t E, int32_t sequences) {
     if (T <= 0 || E <= 0 || sequences <= 0) return 256;
-    return (size_t)fp8q::balance_slots(T, sequences) * (size_t)E * 8;
+    return (size_t)fp8q::balance_slots(T, E, sequences) * (size_t)E * 8;
 }
 
 extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype, int64_t T, int64_t E, int64_t ld_l,
@@ -532,9 +582,9 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     RouteGradArgs p{};
     p.logits = logits; p.T = T; p.ld_l = ld_l; p.ids = ids; p.sequences = sequences; p.loss = loss; p.counts = counts;
-    p.rows = balance_rows(T);
+    p.rows = balance_rows(T, E);
     p.mass = static_cast<float*>(workspace);
-    p.part = reinterpret_cast<int32_t*>(p.mass + balance_slots(T, S) * E);
+    p.part = reinterpret_cast<int32_t*>(p.mass + balance_slots(T, E, S) * E);
     p.E = (int)E; p.k = top_k; p.S = S; p.sigmoid = scoring == FP8Q_SCORE_SIGMOID; p.wide = rg_wide(logits, ld_l, E, f32);
     if (T > 0) {
         start_route_grad(p, f32, false, stream);
