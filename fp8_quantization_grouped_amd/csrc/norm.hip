@@ -6,6 +6,7 @@
 //
 // Bound: HBM.
 #include "common.hpp"
+#include "plan.hpp"
 
 namespace fp8q {
 
@@ -223,8 +224,8 @@ __device__ __forceinline__ float across(float v, float* red) {
 
 // Rows held in registers: WPR waves a row, NV chunks of 8 elements a lane.
 template <int SC, int FMT, int WPR, int NV, int ACC>
-__global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const NormArgs p) {
-    constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR, TPR = 64 * WPR;
+__global__ __launch_bounds__(64 * norm_waves(WPR)) void norm_kernel(const NormArgs p) {
+    constexpr int WAVES = norm_waves(WPR), RPB = WAVES / WPR, TPR = 64 * WPR;
     __shared__ float red[3][WAVES];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), t = threadIdx.x % TPR;
     const int64_t group = SC == FP8Q_NORM_BLOCK ? xcd_run(blockIdx.x, gridDim.x) : (int64_t)blockIdx.x;
@@ -334,7 +335,7 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(const No
 
 template <int SC, int FMT, int WPR, int NV>
 static void launch_norm(const NormArgs& p, int acc, hipStream_t stream) {
-    constexpr int WAVES = WPR > 4 ? WPR : 4, RPB = WAVES / WPR;
+    constexpr int WAVES = norm_waves(WPR), RPB = WAVES / WPR;
     const dim3 grid((unsigned)((p.rows + RPB - 1) / RPB)), block(64 * WAVES);
     if (acc == (WIDE | PAST)) norm_kernel<SC, FMT, WPR, NV, WIDE | PAST><<<grid, block, 0, stream>>>(p);
     else if (acc == WIDE) norm_kernel<SC, FMT, WPR, NV, WIDE><<<grid, block, 0, stream>>>(p);
@@ -346,28 +347,30 @@ static void launch_norm(const NormArgs& p, int acc, hipStream_t stream) {
 static inline bool past_caches(int64_t rows, int64_t cols, int bytes) { return (double)rows * cols * bytes > 2.0 * kStreamBytes; }
 
 // Rows that start on whole vectors of 8 elements; none where there is no matrix.
-static inline bool fp8q_rows_wide(const void* p, int64_t ld, uintptr_t align) { return !p || (ld % 8 == 0 && fp8q_aligned(p, align)); }
+static inline bool rows_wide(const void* p, int64_t ld, uintptr_t align) { return !p || (ld % 8 == 0 && fp8q_aligned(p, align)); }
 
 template <int FMT>
 __global__ void norm_generic_kernel(const NormArgs p);
 
 template <int SC, int FMT>
-static void pick_norm(const NormArgs& p, hipStream_t stream) {
+static void start_norm(const NormArgs& p, hipStream_t stream) {
     const int each = (p.residual ? 6 : 2) + (p.y ? 2 : 0) + (p.q ? 1 : 0);  // bytes of an element
-    const bool wide = p.cols % 8 == 0 && fp8q_rows_wide(p.x, p.ld_x, 16) && fp8q_rows_wide(p.residual, p.ld_res, 16) &&
-                      fp8q_rows_wide(p.h, p.ld_h, 16) && fp8q_rows_wide(p.y, p.ld_y, 16) && fp8q_rows_wide(p.q, p.ld_q, 8) &&
+    const bool wide = p.cols % 8 == 0 && rows_wide(p.x, p.ld_x, 16) && rows_wide(p.residual, p.ld_res, 16) &&
+                      rows_wide(p.h, p.ld_h, 16) && rows_wide(p.y, p.ld_y, 16) && rows_wide(p.q, p.ld_q, 8) &&
                       fp8q_aligned(p.w, 16);
     const int acc = (wide ? WIDE : 0) | (past_caches(p.rows, p.cols, each) ? PAST : 0);
-    if (p.cols < 8) norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
-    else if (p.rows <= 256 && p.cols > 1024 && p.cols <= 8192) launch_norm<SC, FMT, 16, 1>(p, acc, stream);
-    else if (p.cols <= 512) launch_norm<SC, FMT, 1, 1>(p, acc, stream);
-    else if (p.cols <= 1024) launch_norm<SC, FMT, 1, 2>(p, acc, stream);
-    else if (p.cols <= 2048) launch_norm<SC, FMT, 1, 4>(p, acc, stream);
-    else if (p.cols <= 4096) launch_norm<SC, FMT, 2, 4>(p, acc, stream);
-    else if (p.cols <= 8192) launch_norm<SC, FMT, 4, 4>(p, acc, stream);
-    else if (p.cols <= 16384) launch_norm<SC, FMT, 8, 4>(p, acc, stream);
-    else if (p.cols <= 32768) launch_norm<SC, FMT, 16, 4>(p, acc, stream);
-    else norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
+    const NormShape n = pick_norm(p.rows, p.cols);
+    switch (n.chunks ? 10 * n.waves + n.chunks : 0) {
+        case 11: launch_norm<SC, FMT, 1, 1>(p, acc, stream); break;
+        case 12: launch_norm<SC, FMT, 1, 2>(p, acc, stream); break;
+        case 14: launch_norm<SC, FMT, 1, 4>(p, acc, stream); break;
+        case 24: launch_norm<SC, FMT, 2, 4>(p, acc, stream); break;
+        case 44: launch_norm<SC, FMT, 4, 4>(p, acc, stream); break;
+        case 84: launch_norm<SC, FMT, 8, 4>(p, acc, stream); break;
+        case 164: launch_norm<SC, FMT, 16, 4>(p, acc, stream); break;
+        case 161: launch_norm<SC, FMT, 16, 1>(p, acc, stream); break;
+        default: norm_generic_kernel<FMT><<<dim3((unsigned)p.rows), dim3(256), 0, stream>>>(p);
+    }
 }
 
 // Rows longer than registers hold, or shorter than a vector: a block of 4 waves per row, a wave takes blocks of 128 columns in turn, a lane
@@ -678,26 +681,6 @@ __global__ __launch_bounds__(1024) void norm_back_join_kernel(const float* part,
     }
 }
 
-// Waves of a row, chunks of a lane and rows of a block of at most 16 waves; chunks is 0 where registers do
-// not hold a row.
-struct NormBackPlan {
-    int waves, chunks, rows;
-    int64_t blocks;
-};
-static inline NormBackPlan norm_back_plan(int64_t rows, int64_t cols) {
-    NormBackPlan p{1, 0, 1, 0};
-    if (cols >= 8 && cols <= 16384) {
-        p.chunks = cols <= 8192 ? 1 : 2;
-        p.waves = (int)((cols + 512 * p.chunks - 1) / (512 * p.chunks));
-        p.rows = 16 / p.waves;
-    }
-    // at most 256 blocks, each as often as the others: one for a CU at a time, and every block's sums of dw are
-    // written and read once more
-    const int64_t groups = (rows + p.rows - 1) / p.rows, turns = (groups + 255) / 256;
-    p.blocks = turns ? (groups + turns - 1) / turns : 0;
-    return p;
-}
-
 template <bool G32, bool W32, int NV>
 static void launch_norm_back_rows(const NormBackArgs& p, int acc, dim3 grid, dim3 block, size_t lds, hipStream_t stream) {
     if (acc == (WIDE | PAST)) norm_back_kernel<G32, W32, NV, WIDE | PAST><<<grid, block, lds, stream>>>(p);
@@ -708,8 +691,8 @@ static void launch_norm_back_rows(const NormBackArgs& p, int acc, dim3 grid, dim
 
 template <bool G32, bool W32>
 static void launch_norm_back(const NormBackArgs& p, const NormBackPlan& n, hipStream_t stream) {
-    const bool wide = p.cols % 8 == 0 && fp8q_rows_wide(p.h, p.ld_h, 16) && fp8q_rows_wide(p.dy, p.ld_dy, 16) &&
-                      fp8q_rows_wide(p.dh, p.ld_dh, 16) && fp8q_rows_wide(p.dx, p.ld_dx, 16) && fp8q_aligned(p.w, 16);
+    const bool wide = p.cols % 8 == 0 && rows_wide(p.h, p.ld_h, 16) && rows_wide(p.dy, p.ld_dy, 16) &&
+                      rows_wide(p.dh, p.ld_dh, 16) && rows_wide(p.dx, p.ld_dx, 16) && fp8q_aligned(p.w, 16);
     const int acc = (wide ? WIDE : 0) | (past_caches(p.rows, p.cols, 2 + (G32 ? 4 : 2) * (p.dh ? 3 : 2)) ? PAST : 0);
     const dim3 grid((unsigned)n.blocks), block(64 * n.waves * n.rows);
     const size_t lds = (size_t)(n.rows - 1) * 8 * 64 * n.waves * 4;
@@ -739,22 +722,22 @@ extern "C" fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t c
         return FP8Q_ERR_INVALID_ARG;
     // in place: every element where it was
     if (h && ((h == x && ld_h != ld_x) || (h == residual && ld_h != ld_res))) return FP8Q_ERR_INVALID_ARG;
-    if (rows > 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
+    if (rows > 0x7FFFFFFFLL || !norm_fits(rows, cols)) return FP8Q_ERR_UNSUPPORTED;
     NormArgs p{};
     p.x = x; p.rows = rows; p.cols = cols; p.ld_x = ld_x; p.residual = residual; p.ld_res = ld_res; p.w = weight; p.h = h; p.ld_h = ld_h;
     p.y = y; p.ld_y = ld_y; p.q = q; p.ld_q = ld_q; p.scales = scales; p.ld_s = ld_s; p.rstd = rstd; p.eps = eps;
     p.w32 = weight_dtype == FP8Q_OUT_FP32; p.scaling = scaling;
-    if (scaling == FP8Q_NORM_NONE) pick_norm<FP8Q_NORM_NONE, FP8Q_E4M3FN>(p, stream);
-    else if (scaling == FP8Q_NORM_BLOCK) pick_norm<FP8Q_NORM_BLOCK, FP8Q_E4M3FN>(p, stream);
-    else if (fmt == FP8Q_E4M3FN) pick_norm<FP8Q_NORM_ROW, FP8Q_E4M3FN>(p, stream);
-    else pick_norm<FP8Q_NORM_ROW, FP8Q_E4M3FNUZ>(p, stream);
+    if (scaling == FP8Q_NORM_NONE) start_norm<FP8Q_NORM_NONE, FP8Q_E4M3FN>(p, stream);
+    else if (scaling == FP8Q_NORM_BLOCK) start_norm<FP8Q_NORM_BLOCK, FP8Q_E4M3FN>(p, stream);
+    else if (fmt == FP8Q_E4M3FN) start_norm<FP8Q_NORM_ROW, FP8Q_E4M3FN>(p, stream);
+    else start_norm<FP8Q_NORM_ROW, FP8Q_E4M3FNUZ>(p, stream);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }
 
 extern "C" size_t fp8_rms_norm_backward_workspace_size(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0) return 256;
-    return (size_t)fp8q::norm_back_plan(rows, cols).blocks * (size_t)cols * 4;
+    return (size_t)fp8q::pick_norm_back(rows, cols).blocks * (size_t)cols * 4;
 }
 
 extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,
@@ -769,14 +752,14 @@ extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, co
     if (cols == 0) return FP8Q_OK;
     if (!dweight || (rows > 0 && (!dy || !h || !rstd || !weight || !dx))) return FP8Q_ERR_INVALID_ARG;
     if (rows > 0 && ((dx == dy && ld_dx != ld_dy) || (dx == dh && ld_dx != ld_dh))) return FP8Q_ERR_INVALID_ARG;
-    if (rows > 0x7FFFFFFFLL || cols > 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
+    if (rows > 0x7FFFFFFFLL || cols >= 1LL << 27) return FP8Q_ERR_UNSUPPORTED;  // (a launch takes fewer than 2^32 threads)
     if (rows > 0 && (!workspace || workspace_bytes < fp8_rms_norm_backward_workspace_size(rows, cols))) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     NormBackArgs p{};
     p.dy = dy; p.ld_dy = ld_dy; p.dh = dh; p.ld_dh = ld_dh; p.h = h; p.rows = rows; p.cols = cols; p.ld_h = ld_h;
     p.rstd = rstd; p.w = weight; p.dx = dx; p.ld_dx = ld_dx; p.part = static_cast<float*>(workspace);
     p.w32 = weight_dtype == FP8Q_OUT_FP32;
-    const NormBackPlan n = norm_back_plan(rows, cols);
+    const NormBackPlan n = pick_norm_back(rows, cols);
     p.waves = n.waves;
     if (rows > 0) {
         const bool g32 = grad_dtype == FP8Q_OUT_FP32;

@@ -1,4 +1,4 @@
-// Which variant of the block-scaled kernels a call takes: rules on sizes and the chip's CUs alone, in
+// Which variant of the block-scaled kernels, the norm's and the router's a call takes: rules on sizes and the chip's CUs alone, in
 // plain C++ so that they can be checked without a GPU.  Times are of an MI355X (256 CUs), those of one
 // comparison taken together.
 #pragma once
@@ -102,5 +102,74 @@ static inline int route_splits(int64_t T, int64_t H, int64_t E) {
     s = s < most ? s : most;
     return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
+
+// ----------------------------------------------------------------------------------------- norm
+
+// Waves of a row and chunks of 8 elements a lane; chunks is 0 where rows are read again instead of being held
+// in registers: shorter than a chunk, or longer than 16 waves of 4.
+struct NormShape {
+    int waves, chunks;
+};
+static inline NormShape pick_norm(int64_t rows, int64_t cols) {
+    if (cols < 8 || cols > 32768) return {4, 0};
+    // A few rows, two a CU or less, by 16 waves each: 1 x 7168 3.1 us against 4.0 in 4 waves, 256 x 7168 5.4
+    // against 6.2, 64 x 2048 3.6 against 5.0; with 1024 rows it turns (13.6 against 12.5, 2048 wide 8.7
+    // against 6.4).
+    if (rows <= 512 && cols > 1024 && cols <= 8192) return {16, 1};
+    if (cols <= 512) return {1, 1};
+    if (cols <= 1024) return {1, 2};
+    if (cols <= 2048) return {1, 4};
+    if (cols <= 4096) return {2, 4};
+    if (cols <= 8192) return {4, 4};
+    if (cols <= 16384) return {8, 4};
+    return {16, 4};
+}
+constexpr int norm_waves(int waves) { return waves > 4 ? waves : 4; }  // of a block
+// A launch takes fewer than 2^32 threads.
+static inline bool norm_fits(int64_t rows, int64_t cols) {
+    const NormShape n = pick_norm(rows, cols);
+    const int64_t at_a_time = n.chunks ? norm_waves(n.waves) / n.waves : 1;
+    return plan_up(rows, at_a_time) * 64 * norm_waves(n.waves) < 1LL << 32;
+}
+
+// The backward: waves of a row, chunks of a lane (0 as above), rows of a block of up to 16 waves at a time, and
+// blocks.
+struct NormBackPlan {
+    int waves, chunks, rows;
+    int64_t blocks;
+};
+static inline NormBackPlan pick_norm_back(int64_t rows, int64_t cols) {
+    NormBackPlan p{1, 0, 1, 0};
+    if (cols >= 8 && cols <= 16384) {
+        p.chunks = cols <= 8192 ? 1 : 2;
+        p.waves = (int)plan_up(cols, 512 * p.chunks);
+        p.rows = 16 / p.waves;
+    }
+    // At most 256 blocks, each as often as the others: one for a CU at a time, and every block's sums of dw are
+    // written and read once more (16384 x 7168 152 us, with 512 blocks 159; 2048 x 2064 fp32 15 and 17).
+    const int64_t groups = plan_up(rows, p.rows), turns = plan_up(groups, 256);
+    p.blocks = turns ? plan_up(groups, turns) : 0;
+    return p;
+}
+
+// --------------------------------------------------------------------------- a router's training
+
+constexpr int BAL_WAVES = 8;  // of a block that sums probabilities
+
+// Lanes of a row by the number of experts, 16 of them to a lane: what a row's lanes do together counts for as
+// many experts as it can (with 4 to a lane 65536 x 256 took 38 us for the sums and 68 for the gradient, where
+// 16 take 24 and 52).
+static inline int route_lanes(int64_t E) {
+    int l = 1;
+    while (16 * l < E) l *= 2;
+    return l;
+}
+// Rows of a chunk: as many as a block's waves take at a time, or so many that there are 512 chunks.
+static inline int64_t balance_rows(int64_t T, int64_t E) {
+    const int64_t once = BAL_WAVES * 64 / route_lanes(E), r = plan_up(T, 512);
+    return r < once ? once : r;
+}
+// Places for the sums of a chunk's tokens of one sequence.
+static inline int64_t balance_slots(int64_t T, int64_t E, int64_t S) { return plan_up(T, balance_rows(T, E)) + S; }
 
 }  // namespace fp8q

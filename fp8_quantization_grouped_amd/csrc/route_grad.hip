@@ -8,11 +8,11 @@
 //
 // Bound: HBM for large T * E, launches below.
 #include "common.hpp"
+#include "plan.hpp"
 
 namespace fp8q {
 
 constexpr int RG_MAX_E = 1024, RG_MAX_K = 32;
-constexpr int BAL_WAVES = 8;  // of a block that sums probabilities
 
 struct RouteGradArgs {
     const void* logits;
@@ -510,20 +510,6 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
     }
 }
 
-// Lanes of a row by the number of experts, 16 of them to a lane: what a row's lanes do together counts for
-// as many experts as it can.
-static inline int route_lanes(int64_t E) {
-    int l = 1;
-    while (16 * l < E) l *= 2;
-    return l;
-}
-// Rows of a chunk: as many as a block's waves take at a time, or so many that there are 512 chunks.
-static inline int64_t balance_rows(int64_t T, int64_t E) {
-    const int64_t once = BAL_WAVES * 64 / route_lanes(E), r = (T + 511) / 512;
-    return r < once ? once : r;
-}
-static inline int64_t balance_slots(int64_t T, int64_t E, int64_t S) { return (T + balance_rows(T, E) - 1) / balance_rows(T, E) + S; }
-
 template <int L, int NV, bool F32, bool SIG>
 static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     constexpr int ROWS = 4 * (64 / L);
@@ -577,7 +563,7 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
     if (T < 0 || E < 1 || ld_l < E || top_k < 1 || S < 1 || (!sequences && S != 1) || (!f32 && logits_dtype != FP8Q_OUT_BF16) ||
         (scoring != FP8Q_SCORE_SOFTMAX && scoring != FP8Q_SCORE_SIGMOID) || !loss || !counts || (T > 0 && (!logits || !ids)))
         return FP8Q_ERR_INVALID_ARG;
-    if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
+    if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL || S >= 1 << 22) return FP8Q_ERR_UNSUPPORTED;
     if (T > 0 && (!workspace || workspace_bytes < moe_balance_workspace_size(T, E, S))) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     RouteGradArgs p{};
@@ -610,7 +596,7 @@ extern "C" fp8q_status_t moe_route_backward(const void* logits, fp8q_out_t logit
     if (dloss && (!counts || S < 1 || (!sequences && S != 1))) return FP8Q_ERR_INVALID_ARG;
     if (T == 0) return FP8Q_OK;
     if (!logits || !ids || !dlogits || (dlogits == logits && ld_d != ld_l)) return FP8Q_ERR_INVALID_ARG;
-    if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL) return FP8Q_ERR_UNSUPPORTED;
+    if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL || (dloss && S >= 1 << 22)) return FP8Q_ERR_UNSUPPORTED;
     RouteGradArgs p{};
     p.logits = logits; p.T = T; p.ld_l = ld_l; p.ids = ids; p.dweights = dweights; p.renorm = renormalize != 0; p.scale = scale;
     p.dloss = dloss; p.counts = const_cast<int32_t*>(counts); p.sequences = sequences; p.S = S; p.dlogits = dlogits; p.ld_d = ld_d;

@@ -480,8 +480,9 @@ fp8q_status_t fp8_moe_few_tokens(const uint16_t* x, int64_t T, int64_t H, int64_
  *   rstd  fp32 [rows] for the backward, or null
  * Rows of any finite h: where the squares' sum leaves fp32's range it is formed of h * 2^-80.
  * Any sizes and alignments; cols and leading dimensions that are multiples of 8 with x, residual, h,
- * y and weight 16-byte and q 8-byte aligned take the wide accesses.  rows < 2^31
- * (FP8Q_ERR_UNSUPPORTED beyond).  rows == 0 or cols == 0 is a no-op. */
+ * y and weight 16-byte and q 8-byte aligned take the wide accesses.  Rows under 2^24, for cols from 8193
+ * to 32768 under 2^22, are taken; more are refused (FP8Q_ERR_UNSUPPORTED) where one launch cannot hold
+ * them.  rows == 0 or cols == 0 is a no-op. */
 typedef enum { FP8Q_NORM_NONE = 0, FP8Q_NORM_ROW = 1, FP8Q_NORM_BLOCK = 2 } fp8q_norm_scaling_t;
 fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x,
                            const uint16_t* residual, int64_t ld_res, const void* weight,
@@ -497,7 +498,8 @@ fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t cols, int64_
  *   dy, dh, dx [rows][ld] of grad_dtype; dx may be dy or dh itself (the same pointer and leading
  *   dimension)
  *   workspace  fp8_rms_norm_backward_workspace_size bytes, any content, 16-byte aligned
- * Sums in fp32, every one in a fixed order.  rows == 0 gives a dweight of zeros. */
+ * Sums in fp32, every one in a fixed order.  rows < 2^31, cols < 2^27 (FP8Q_ERR_UNSUPPORTED beyond).
+ * rows == 0 gives a dweight of zeros. */
 size_t fp8_rms_norm_backward_workspace_size(int64_t rows, int64_t cols);
 fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,
                                     fp8q_out_t grad_dtype, const uint16_t* h, int64_t rows,
@@ -529,7 +531,7 @@ fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* d
  *   choice alone).
  * Without dloss, counts, sequences and S are ignored.  dlogits may be logits itself (the same pointer
  * and leading dimension).
- * Limits (FP8Q_ERR_UNSUPPORTED): E <= 1024, top_k <= 32, T < 2^31. */
+ * Limits (FP8Q_ERR_UNSUPPORTED): E <= 1024, top_k <= 32, T < 2^31, S < 2^22. */
 size_t moe_balance_workspace_size(int64_t T, int64_t E, int32_t sequences);
 fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype, int64_t T, int64_t E,
                           int64_t ld_l, fp8q_scoring_t scoring, const int32_t* ids, int32_t top_k,
