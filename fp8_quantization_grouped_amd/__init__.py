@@ -877,6 +877,7 @@ def fp8_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     h, rstd: what the forward returned.  Returns (dx [rows, cols] like dy, the gradient of x and of the
     residual alike, dweight float32 [cols]).  dx may be given as dy or dh to replace it."""
     rows, cols, dev = _matrix(dy, "dy", _WIDE)
+    _no_grad("fp8_rms_norm_backward", dy, dh)
     shape = (rows, cols)
     _rows_of(h, "h", _BF16, shape, dev)
     _rows_of(rstd, "rstd", _F32, (rows,), dev)
@@ -971,6 +972,7 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
     loss with its counts and sequences; either may be None.  dlogits may be given as logits to replace
     them."""
     T, E, dev, top_k, args = _choice(logits, ids, scoring)
+    _no_grad("moe_route_backward", dweights, dloss)
     if dweights is not None:
         _rows_of(dweights, "dweights", _F32, (T, top_k), dev)
         _want(dweights.is_contiguous(), "dweights must be contiguous")
@@ -1042,6 +1044,8 @@ class AdamWStates:
                 used = [[zeros(p.shape, torch.float32) for p in self.params] for _ in range(2)]
         self.exp_avg, self.exp_avg_sq = used[:2]
         self.exp_avg_scales, self.exp_avg_sq_scales = used[2:] if eight else ([None] * n, [None] * n)
+        # what torch has recorded of a parameter's value is no longer that after a step, and torch is told so
+        self._watched = [t for t in self.params + self.masters if t is not None and t.requires_grad]
         self._table = (_AdamTensor * n)()
         taken = set()
         for i, p in enumerate(self.params):
@@ -1112,3 +1116,5 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
     if not grads:
         return
     _call("adamw_step", dev, ctypes.addressof(table), len(grads), ctypes.addressof(h))
+    if states._watched:
+        torch.autograd.graph.increment_version(states._watched)

@@ -53,7 +53,7 @@ def test_states_refuse(calls):  # noqa: F811
 
 def test_step_binding_refuses(calls):  # noqa: F811
     s = fq.AdamWStates.__new__(fq.AdamWStates)
-    s.params, s.bits, s.device, s._table = [zeros(4, 8)], 8, zeros(1).device, (fq._AdamTensor * 1)()
+    s.params, s.bits, s.device, s._table, s._watched = [zeros(4, 8)], 8, zeros(1).device, (fq._AdamTensor * 1)(), []
     g = [zeros(4, 8)]
     for kw in (dict(grads=[]), dict(grads=[zeros(32)]), dict(grads=[zeros(4, 8, dtype=torch.float16)]), dict(grads=[torch.zeros(4, 8)]),
                dict(grads=[zeros(8, 4).t()]), dict(step=0), dict(step=zeros(1)), dict(step=zeros(2, dtype=torch.int32)),

@@ -232,3 +232,47 @@ def test_states_go_into_the_block_format(fq):
     fq.adamw_step(s, [x], 1, 1e-3, betas=(0.0, 0.5))
     q, d = fq.fp8_block_quant_rowwise(x.to(BF16)[None])
     assert torch.equal(s.exp_avg[0], q[0]) and torch.equal(s.exp_avg_scales[0], d[:, 0])
+
+
+@pytest.mark.parametrize("bits,n", [(32, 6_000_077), (8, 14_000_077)])
+def test_steps_past_the_caches(fq, bits, n):
+    """More than the last-level cache holds, where reads and writes go past the caches: against 64 bits at both
+    ends and in the middle."""
+    g = torch.Generator("cuda").manual_seed(bits)
+    flat = lambda scale: torch.randn(n, generator=g, device="cuda") * scale
+    p, grad, m = flat(1.0), flat(1e-3), flat(1e-3)
+    if bits == 32:
+        s = fq.AdamWStates([p], 32, None, [m], [(m * 3).square() + 1e-9])
+    else:
+        (q, d), (r, e) = (fq.fp8_block_quant_rowwise(v.to(BF16)[None]) for v in (m, m.abs() * 3 + 1e-4))
+        s = fq.AdamWStates([p], 8, None, [q[0].contiguous()], [r[0].contiguous()], [d[:, 0].contiguous()], [e[:, 0].contiguous()])
+    cuts = [(0, 5000), (n // 256 * 128, n // 256 * 128 + 5000), (n // 128 * 128 - 4992, n)]
+    part = lambda t, a, b: t[a:b].cpu().double()
+    blocks = lambda t, a, b: t[a // 128:-(-b // 128)].cpu()
+    before = [(part(p, a, b),) + ((part(s.exp_avg[0], a, b), part(s.exp_avg_sq[0], a, b)) if bits == 32 else
+              (al.decode(s.exp_avg[0][a:b], blocks(s.exp_avg_scales[0], a, b)),
+               al.decode(s.exp_avg_sq[0][a:b], blocks(s.exp_avg_sq_scales[0], a, b)).square())) for a, b in cuts]
+    fq.adamw_step(s, [grad], 7, 1e-2)
+    words = al.words(7, 0, n)
+    for (a, b), (p0, m0, v0) in zip(cuts, before):
+        p1, off_p, m1, off_m, v1, off_v = al.step64(p0, part(grad, a, b), m0, v0, 7, 1e-2, (0.9, 0.999), 1e-8, 0.01)
+        assert bool(((part(p, a, b) - p1).abs() <= off_p).all())
+        if bits == 32:
+            assert bool(((part(s.exp_avg[0], a, b) - m1).abs() <= off_m).all())
+            assert bool(((part(s.exp_avg_sq[0], a, b) - v1).abs() <= off_v).all())
+            continue
+        b -= (b - a) % 128 if b < n else 0  # whole blocks
+        k, r = b - a, torch.sqrt(v1)
+        off_r = torch.maximum(torch.sqrt(v1 + off_v) - r, r - torch.sqrt((v1 - off_v).clamp(min=0))) + 2 * al.U * r
+        al.check_kept(s.exp_avg[0][a:b], blocks(s.exp_avg_scales[0], a, b), m1[:k], off_m[:k], words[a:b], False)
+        al.check_kept(s.exp_avg_sq[0][a:b], blocks(s.exp_avg_sq_scales[0], a, b), r[:k], off_r[:k], words[a:b], True)
+
+
+def test_a_step_is_seen_by_what_torch_has_recorded(fq):
+    """A parameter that was saved for a backward pass and then stepped is a parameter that was changed."""
+    p = torch.nn.Parameter(normal(100, 1))
+    loss = (p * p).sum()
+    s = fq.AdamWStates([p], 32)
+    fq.adamw_step(s, [torch.ones(100, device="cuda")], 1, 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()

@@ -98,3 +98,17 @@ def test_one_row_of_any_stride(calls):  # noqa: F811
         fq.fp8_rms_norm_backward(x, x, zeros(1), zeros(256), dh=x, dx=x)
         args = calls[-1][1]
         assert args[1] == args[3] == args[8] == args[13] == 256
+
+
+def test_a_backward_that_torch_would_record_is_refused(calls):  # noqa: F811
+    x, w = zeros(4, 256, dtype=BF16), zeros(256).requires_grad_()
+    for which in range(2):
+        t = [zeros(4, 256), zeros(4, 256)]
+        t[which].requires_grad_()
+        with pytest.raises(ValueError, match="no gradient"):
+            fq.fp8_rms_norm_backward(t[0], x, zeros(4), w, dh=t[1])
+    fq.fp8_rms_norm_backward(zeros(4, 256), x, zeros(4), w)  # (a weight that is a parameter is no obstacle)
+    ids = zeros(6, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="no gradient"):
+        fq.moe_route_backward(zeros(6, 8), ids, zeros(6, 2).requires_grad_())
+    assert len(calls) == 1
