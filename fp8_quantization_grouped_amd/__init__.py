@@ -795,9 +795,12 @@ class Normed(NamedTuple):
 
 def _no_record(what: str, backward: str, *tensors) -> None:
     """Refuses operands whose gradient torch would record: it is another call's."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError(f"{what} is not recorded, its gradient is {backward}: detach its operands, or call "
-                         "it under torch.no_grad()")
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{what} is not recorded, its gradient is {backward}: detach its operands, or "
+                             "call it under torch.no_grad()")
 
 
 def fp8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -953,10 +956,12 @@ def moe_balance(logits: torch.Tensor, ids: torch.Tensor, scoring: str = "softmax
     else:
         _rows_of(counts, "counts", _I32T, (S, E), dev)
         _want(counts.is_contiguous(), "counts must be contiguous")
+    ws = None
     if workspace is None:
         need = lib().moe_balance_workspace_size(T, E, S)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws = workspace.data_ptr()
+        if need:  # few tokens take none
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
     else:
         ws, need = _workspace(workspace, dev)
     _call("moe_balance", dev, *args, seq, S, loss.data_ptr(), counts.data_ptr(), ws, need)

@@ -169,6 +169,8 @@ static inline int64_t balance_rows(int64_t T, int64_t E) {
     const int64_t once = BAL_WAVES * 64 / route_lanes(E), r = plan_up(T, 512);
     return r < once ? once : r;
 }
+// One block takes all tokens and needs no second launch to join them (96 x 4 10 -> XXX us, both as called).
+static inline bool balance_is_small(int64_t T, int64_t E) { return T <= BAL_WAVES * 64 / route_lanes(E); }
 // Places for the sums of a chunk's tokens of one sequence.
 static inline int64_t balance_slots(int64_t T, int64_t E, int64_t S) { return plan_up(T, balance_rows(T, E)) + S; }
 

@@ -215,14 +215,31 @@ __device__ __forceinline__ void scores_of(const float (&l)[N], float (&t)[N], fl
     }
 }
 
+// E / (k n^2), what a sequence of n tokens' sum of counts times probabilities is multiplied by.
+__device__ __forceinline__ float balance_over(const RouteGradArgs& p, int64_t n) {
+    return (float)p.E / ((float)p.k * (float)n * (float)n);
+}
+// Sum over a block of up to 16 waves, in thread 0.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int i = 1; i < (int)blockDim.x / 64; i++) v += red[i];
+    return v;
+}
+
 // One chunk of rows: for each sequence in it, the probabilities' sums and the counts go to slot chunk +
 // sequence of the workspace: both only grow along the rows, so no two pairs share one.  A thread keeps
-// the sums of its experts; rows of the block's waves are added in a fixed order.
+// the sums of its experts; rows of the block's waves are added in a fixed order.  Where one block takes all
+// rows (p.mass is null) it leaves the losses and counts, those of empty sequences among them.
 template <int L, int NV, bool F32, bool SIG>
 __global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGradArgs p) {
     constexpr int R = 64 / L, ROWS = BAL_WAVES * R, N = 4 * NV;  // rows of a wave and of the block at a time
     __shared__ float sums[BAL_WAVES][4 * L * NV];
     __shared__ int32_t count[4 * L * NV];
+    __shared__ float red[BAL_WAVES];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane % L, mine = wave * R + lane / L;
     const int64_t begin = (int64_t)blockIdx.x * p.rows;
     const int64_t end = begin + p.rows < p.T ? begin + p.rows : p.T;
@@ -232,9 +249,16 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGrad
     const int64_t id_at = begin * p.k + threadIdx.x;
     const int first_id = id_at < end * p.k ? p.ids[id_at] : -1;
     const Ends ends(p);
-    for (int s = ends.of(begin); s < p.S && r0 < end; s++) {
+    const bool small = p.mass == nullptr;
+    for (int s = small ? 0 : ends.of(begin); s < p.S && (small || r0 < end); s++) {
         const int64_t e1 = ends.end(s), r1 = e1 < end ? e1 : end;
-        if (r1 <= r0) continue;
+        if (r1 <= r0) {
+            if (small) {
+                for (int e = threadIdx.x; e < p.E; e += 64 * BAL_WAVES) p.counts[(int64_t)s * p.E + e] = 0;
+                if (threadIdx.x == 0) p.loss[s] = 0.0f;
+            }
+            continue;
+        }
         for (int i = threadIdx.x; i < p.E; i += 64 * BAL_WAVES) count[i] = 0;
         __syncthreads();
         float acc[N];
@@ -262,12 +286,22 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGrad
             for (int i = 0; i < N; i++) sums[wave][4 * (j + L * (i / 4)) + i % 4] = acc[i];
         __syncthreads();
         const int64_t slot = (int64_t)blockIdx.x + s;
+        float loss = 0.0f;
         for (int e = threadIdx.x; e < p.E; e += 64 * BAL_WAVES) {
             float a = 0.0f;
 #pragma unroll
             for (int i = 0; i < BAL_WAVES; i++) a += sums[i][e];
-            p.mass[slot * p.E + e] = a;
-            p.part[slot * p.E + e] = count[e];
+            if (small) {
+                p.counts[(int64_t)s * p.E + e] = count[e];
+                loss += (float)count[e] * a;
+            } else {
+                p.mass[slot * p.E + e] = a;
+                p.part[slot * p.E + e] = count[e];
+            }
+        }
+        if (small) {
+            loss = block_sum(loss, red);
+            if (threadIdx.x == 0) p.loss[s] = loss * balance_over(p, r1 - r0);
         }
         __syncthreads();
         r0 = r1;
@@ -304,14 +338,8 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const RouteGradArgs 
         p.counts[(int64_t)s * p.E + e] = k;
         sum = (float)k * m;
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < (int)blockDim.x / 64; i++) sum += red[i];
-        p.loss[s] = n > 0 ? sum * ((float)p.E / ((float)p.k * (float)n * (float)n)) : 0.0f;
-    }
+    sum = block_sum(sum, red);
+    if (threadIdx.x == 0) p.loss[s] = n > 0 ? sum * balance_over(p, n) : 0.0f;
 }
 
 // Lanes of a wave see what others of it have written to LDS.
@@ -382,8 +410,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
             ahead = ahead && s < p.S && row >= seq_last;
         }
         if (other) {
-            const float n = (float)(seq_last - seq_first);
-            const float over = s < p.S ? p.dloss[s] * ((float)p.E / ((float)p.k * n * n)) : 0.0f;
+            const float over = s < p.S ? p.dloss[s] * balance_over(p, seq_last - seq_first) : 0.0f;
 #pragma unroll
             for (int v = 0; v < NV; v++)
 #pragma unroll
@@ -550,7 +577,7 @@ static inline bool rg_wide(const void* p, int64_t ld, int64_t E, bool f32) {
 }  // namespace fp8q
 
 extern "C" size_t moe_balance_workspace_size(int64_t T, int64_t E, int32_t sequences) {
-    if (T <= 0 || E <= 0 || sequences <= 0) return 256;
+    if (T <= 0 || E <= 0 || sequences <= 0 || fp8q::balance_is_small(T, E)) return 0;
     return (size_t)fp8q::balance_slots(T, E, sequences) * (size_t)E * 8;
 }
 
@@ -564,17 +591,21 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
         (scoring != FP8Q_SCORE_SOFTMAX && scoring != FP8Q_SCORE_SIGMOID) || !loss || !counts || (T > 0 && (!logits || !ids)))
         return FP8Q_ERR_INVALID_ARG;
     if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL || S >= 1 << 22) return FP8Q_ERR_UNSUPPORTED;
-    if (T > 0 && (!workspace || workspace_bytes < moe_balance_workspace_size(T, E, S))) return FP8Q_ERR_WORKSPACE;
+    const bool small = balance_is_small(T, E);
+    if (!small && (!workspace || workspace_bytes < moe_balance_workspace_size(T, E, S))) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     RouteGradArgs p{};
     p.logits = logits; p.T = T; p.ld_l = ld_l; p.ids = ids; p.sequences = sequences; p.loss = loss; p.counts = counts;
     p.rows = balance_rows(T, E);
-    p.mass = static_cast<float*>(workspace);
-    p.part = reinterpret_cast<int32_t*>(p.mass + balance_slots(T, E, S) * E);
+    if (!small) {
+        p.mass = static_cast<float*>(workspace);
+        p.part = reinterpret_cast<int32_t*>(p.mass + balance_slots(T, E, S) * E);
+    }
     p.E = (int)E; p.k = top_k; p.S = S; p.sigmoid = scoring == FP8Q_SCORE_SIGMOID; p.wide = rg_wide(logits, ld_l, E, f32);
     if (T > 0) {
         start_route_grad(p, f32, false, stream);
         FP8Q_CHECK_LAUNCH();
+        if (small) return FP8Q_OK;
     }
     int C = 4;
     while (C < E) C *= 2;

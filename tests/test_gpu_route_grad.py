@@ -157,3 +157,18 @@ def test_logits_of_the_routing(fq, T, H, E, k, scoring):
     # scores, their sum and the quotient in 32 bits, exponents up to 20 away
     assert bool(((w.cpu().double() - got).abs() <= (2 * (20 + 8) + 64) * rl.U * got).all())
     run(fq, l, ids, torch.randn(T, k, generator=g).cuda(), scoring)
+
+
+@pytest.mark.parametrize("E,k", [(4, 2), (16, 3), (64, 6), (256, 8), (1000, 4)])
+def test_one_block_or_more(fq, E, k):
+    """As many tokens as one block takes by itself, and one more; with and without sequences, empty ones first, in
+    the middle and last."""
+    once = 512
+    while 16 * 512 // once < E:
+        once //= 2
+    assert fq.moe_balance_workspace_size(once, E, 1) == 0 < fq.moe_balance_workspace_size(once + 1, E, 1)
+    for T in (once - 1, once, once + 1):
+        l, ids, dw = case(T, E, k, T)
+        run(fq, l, ids, dw)
+        for ends in ([0, 0, 1, T // 2, T // 2, T - 1, T - 1], [T], [0] * 70 + [T]):
+            run(fq, l, ids, dw, sequences=torch.tensor(ends, dtype=I32).cuda())

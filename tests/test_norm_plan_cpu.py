@@ -81,3 +81,11 @@ def test_chunks_of_the_balance():
         assert lanes in (1, 2, 4, 8, 16, 32, 64) and 16 * lanes >= E and (lanes == 1 or 8 * lanes < E)
         chunks = -(-T // rows)
         assert chunks <= 512 and slots == chunks + S  # chunk c and sequence s share place c + s: c < chunks, s < S
+
+
+def test_few_tokens_need_no_workspace():
+    import fp8_quantization_grouped_amd as fq
+    for E in (1, 8, 16, 17, 64, 65, 300, 1024):
+        once = ask("route", 1, E, 1)[1]
+        assert fq.moe_balance_workspace_size(once, E, 5) == 0
+        assert fq.moe_balance_workspace_size(once + 1, E, 5) == (2 + 5) * E * 8

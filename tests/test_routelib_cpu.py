@@ -56,7 +56,7 @@ def back(**kw):
     (dict(T=-1), INVALID), (dict(E=0), INVALID), (dict(ld=7), INVALID), (dict(k=0), INVALID), (dict(S=0), INVALID), (dict(S=2), INVALID),
     (dict(dtype=2), INVALID), (dict(scoring=2), INVALID), (dict(loss=None), INVALID), (dict(counts=None), INVALID),
     (dict(logits=None), INVALID), (dict(ids=None), INVALID), (dict(ws=ctypes.c_void_p(4100)), INVALID), (dict(E=1025, ld=1025), UNSUPPORTED),
-    (dict(k=33), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(size=8), WORKSPACE)])
+    (dict(k=33), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED), (dict(T=1000, ws=None), WORKSPACE), (dict(T=1000, size=8), WORKSPACE)])
 def test_balance_refuses(kw, status):
     assert balance(**kw) == status
 
