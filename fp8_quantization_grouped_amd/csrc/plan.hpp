@@ -169,9 +169,15 @@ static inline int64_t balance_rows(int64_t T, int64_t E) {
     const int64_t once = BAL_WAVES * 64 / route_lanes(E), r = plan_up(T, 512);
     return r < once ? once : r;
 }
-// One block takes all tokens and needs no second launch to join them (96 x 4 10 -> XXX us, both as called).
+// One block takes all tokens and needs no second launch to join them (96 x 4, as called: 10 us in two, 7 in one).
 static inline bool balance_is_small(int64_t T, int64_t E) { return T <= BAL_WAVES * 64 / route_lanes(E); }
 // Places for the sums of a chunk's tokens of one sequence.
 static inline int64_t balance_slots(int64_t T, int64_t E, int64_t S) { return plan_up(T, balance_rows(T, E)) + S; }
+// Groups of experts that join a sequence's sums, in a block each, where one block a sequence would read more
+// than 512 KB (65536 x 256 in one sequence, 1 MB, 13.9 us, in groups 6.5; 65536 x 64, 256 KB, 6.0 and 6.6).
+constexpr int BAL_GROUP = 32;
+static inline int balance_groups(int64_t T, int64_t E, int64_t S) {
+    return E > BAL_GROUP && balance_slots(T, E, S) * E * 8 > S * (512 << 10) ? (int)plan_up(E, BAL_GROUP) : 1;
+}
 
 }  // namespace fp8q

@@ -27,6 +27,7 @@ struct RouteGradArgs {
     int64_t ld_d;
     float* mass;                 // [chunks + S][E] sums of p of a chunk's tokens of one sequence
     int32_t* part;               // [chunks + S][E] their counts
+    float* group_sums;               // [S][groups] what groups of experts give a sequence's loss, or null
     int64_t rows;                // of a chunk
     int E, k, S;
     bool sigmoid, renorm, wide;  // wide: rows start on whole vectors of 4, and E is a multiple of 4
@@ -41,7 +42,7 @@ __device__ __forceinline__ uint32_t rg_pack(float a, float b) {  // to the neare
 }
 
 // The value of another lane of the 16 that a DPP operation reaches: 1 and 2 away, then mirrored in 8 and 16
-// (whose halves hold one value each by then).
+// (whose group_sums hold one value each by then).
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
@@ -309,11 +310,12 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGrad
 }
 
 // A sequence's loss and counts from its chunks: a block per sequence; C threads take an expert each, up to
-// 16 rows of them the chunks in turn.
+// 16 rows of them the chunks in turn.  With p.group_sums a block per sequence and C experts, whose parts of the
+// loss are added by a third launch: one block alone reads 130 GB/s.
 __global__ __launch_bounds__(1024) void balance_join_kernel(const RouteGradArgs p, int C) {
     __shared__ float mass[1024], red[16];
     __shared__ int32_t count[1024];
-    const int s = blockIdx.x, e = threadIdx.x & (C - 1), row = threadIdx.x / C, rows = blockDim.x / C;
+    const int s = blockIdx.x, e = blockIdx.y * C + (threadIdx.x & (C - 1)), row = threadIdx.x / C, rows = blockDim.x / C;
     const Ends ends(p);
     const int64_t a = ends.end(s - 1), b = ends.end(s), n = b - a;
     float m = 0.0f;
@@ -332,13 +334,26 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const RouteGradArgs 
     float sum = 0.0f;
     if (row == 0 && e < p.E) {
         for (int i = 1; i < rows; i++) {
-            m += mass[i * C + e];
-            k += count[i * C + e];
+            m += mass[i * C + threadIdx.x];
+            k += count[i * C + threadIdx.x];
         }
         p.counts[(int64_t)s * p.E + e] = k;
         sum = (float)k * m;
     }
     sum = block_sum(sum, red);
+    if (threadIdx.x != 0) return;
+    if (p.group_sums) p.group_sums[(int64_t)s * gridDim.y + blockIdx.y] = sum;
+    else p.loss[s] = n > 0 ? sum * balance_over(p, n) : 0.0f;
+}
+
+// The losses from the groups' parts: a wave a sequence.
+__global__ __launch_bounds__(64) void balance_loss_kernel(const RouteGradArgs p, int groups) {
+    const int s = blockIdx.x;
+    const Ends ends(p);
+    const int64_t n = ends.end(s) - ends.end(s - 1);
+    float sum = (int)threadIdx.x < groups ? p.group_sums[(int64_t)s * groups + threadIdx.x] : 0.0f;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
     if (threadIdx.x == 0) p.loss[s] = n > 0 ? sum * balance_over(p, n) : 0.0f;
 }
 
@@ -578,7 +593,8 @@ static inline bool rg_wide(const void* p, int64_t ld, int64_t E, bool f32) {
 
 extern "C" size_t moe_balance_workspace_size(int64_t T, int64_t E, int32_t sequences) {
     if (T <= 0 || E <= 0 || sequences <= 0 || fp8q::balance_is_small(T, E)) return 0;
-    return (size_t)fp8q::balance_slots(T, E, sequences) * (size_t)E * 8;
+    const int groups = fp8q::balance_groups(T, E, sequences);
+    return (size_t)fp8q::balance_slots(T, E, sequences) * (size_t)E * 8 + (groups > 1 ? (size_t)groups * (size_t)sequences * 4 : 0);
 }
 
 extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype, int64_t T, int64_t E, int64_t ld_l,
@@ -607,9 +623,17 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
         FP8Q_CHECK_LAUNCH();
         if (small) return FP8Q_OK;
     }
-    int C = 4;
-    while (C < E) C *= 2;
-    balance_join_kernel<<<dim3((unsigned)S), dim3(C < 64 ? 16 * C : 1024), 0, stream>>>(p, C);
+    const int groups = balance_groups(T, E, S);
+    if (!small && groups > 1) {
+        p.group_sums = reinterpret_cast<float*>(p.part + balance_slots(T, E, S) * E);
+        balance_join_kernel<<<dim3((unsigned)S, (unsigned)groups), dim3(1024), 0, stream>>>(p, BAL_GROUP);
+        FP8Q_CHECK_LAUNCH();
+        balance_loss_kernel<<<dim3((unsigned)S), dim3(64), 0, stream>>>(p, groups);
+    } else {
+        int C = 4;
+        while (C < E) C *= 2;
+        balance_join_kernel<<<dim3((unsigned)S), dim3(C < 64 ? 16 * C : 1024), 0, stream>>>(p, C);
+    }
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }

@@ -172,3 +172,13 @@ def test_one_block_or_more(fq, E, k):
         run(fq, l, ids, dw)
         for ends in ([0, 0, 1, T // 2, T // 2, T - 1, T - 1], [T], [0] * 70 + [T]):
             run(fq, l, ids, dw, sequences=torch.tensor(ends, dtype=I32).cuda())
+
+
+@pytest.mark.parametrize("T,E,k,ends", [(30000, 512, 4, [10, 29000]), (20000, 1000, 2, None), (40000, 257, 8, [0, 39999, 39999, 40000]), (9000, 260, 3, [8999])])
+def test_joins_in_groups_of_experts(fq, T, E, k, ends):
+    """Sums of a sequence that several blocks join."""
+    l, ids, dw = case(T, E, k, T)
+    seq = None if ends is None else torch.tensor(ends, dtype=I32).cuda()
+    first = run(fq, l, ids, dw, sequences=seq)
+    for a, b in zip(first, run(fq, l, ids, dw, sequences=seq)):
+        assert torch.equal(a, b)

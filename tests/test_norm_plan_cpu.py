@@ -22,7 +22,7 @@ extern "C" void back(int64_t rows, int64_t cols, int64_t* out) {
     out[0] = p.waves; out[1] = p.chunks; out[2] = p.rows; out[3] = p.blocks;
 }
 extern "C" void route(int64_t T, int64_t E, int64_t S, int64_t* out) {
-    out[0] = route_lanes(E); out[1] = balance_rows(T, E); out[2] = balance_slots(T, E, S);
+    out[0] = route_lanes(E); out[1] = balance_rows(T, E); out[2] = balance_slots(T, E, S); out[3] = balance_groups(T, E, S);
 }
 """
 
@@ -77,7 +77,8 @@ def test_chunks_of_the_balance():
     rng = random.Random(2)
     for _ in range(20000):
         T, E, S = int(2 ** rng.uniform(0, 30)), rng.randint(1, 1024), int(2 ** rng.uniform(0, 20))
-        lanes, rows, slots, _ = ask("route", T, E, S)
+        lanes, rows, slots, groups = ask("route", T, E, S)
+        assert groups == 1 or (groups <= 64 and groups == -(-E // 32))  # (a wave adds them)
         assert lanes in (1, 2, 4, 8, 16, 32, 64) and 16 * lanes >= E and (lanes == 1 or 8 * lanes < E)
         chunks = -(-T // rows)
         assert chunks <= 512 and slots == chunks + S  # chunk c and sequence s share place c + s: c < chunks, s < S
