@@ -122,7 +122,7 @@ struct Ends {
 
 // A row's logits: L lanes with 4 * NV experts each, lane j's at 4 (j + L v) .. + 3; minus infinity past E.
 // They are held as they are read until get.
-template <int L, int NV, bool F32>
+template <int L, int NV, bool F32, bool WIDE>
 struct Logits {
     uint32_t w[NV][F32 ? 4 : 2];
     __device__ __forceinline__ void load(const RouteGradArgs& p, int64_t r, int j) {
@@ -134,7 +134,7 @@ struct Logits {
                 for (int i = 0; i < 4; i++) w[v][F32 ? i : 0] = 0xFF800000u;
                 if (e >= p.E) continue;
                 const uint32_t* src = static_cast<const uint32_t*>(p.logits) + r * p.ld_l + e;
-                if (p.wide) {
+                if (WIDE) {
                     const uint4 a = *reinterpret_cast<const uint4*>(src);
                     w[v][0] = a.x; w[v][1] = a.y; w[v][F32 ? 2 : 0] = a.z; w[v][F32 ? 3 : 0] = a.w;
                 } else {
@@ -146,7 +146,7 @@ struct Logits {
                 w[v][0] = w[v][1] = 0xFF80FF80u;
                 if (e >= p.E) continue;
                 const uint16_t* src = static_cast<const uint16_t*>(p.logits) + r * p.ld_l + e;
-                if (p.wide) {
+                if (WIDE) {
                     const uint2 a = *reinterpret_cast<const uint2*>(src);
                     w[v][0] = a.x; w[v][1] = a.y;
                 } else {
@@ -235,7 +235,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // sequence of the workspace: both only grow along the rows, so no two pairs share one.  A thread keeps
 // the sums of its experts; rows of the block's waves are added in a fixed order.  Where one block takes all
 // rows (p.mass is null) it leaves the losses and counts, those of empty sequences among them.
-template <int L, int NV, bool F32, bool SIG>
+template <int L, int NV, bool F32, bool SIG, bool WIDE>
 __global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGradArgs p) {
     constexpr int R = 64 / L, ROWS = BAL_WAVES * R, N = 4 * NV;  // rows of a wave and of the block at a time
     __shared__ float sums[BAL_WAVES][4 * L * NV];
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGrad
     const int64_t begin = (int64_t)blockIdx.x * p.rows;
     const int64_t end = begin + p.rows < p.T ? begin + p.rows : p.T;
     int64_t r0 = begin;
-    Logits<L, NV, F32> cur, next;  // a row's loads go out while the one before it is worked on
+    Logits<L, NV, F32, WIDE> cur, next;  // a row's loads go out while the one before it is worked on
     if (r0 + mine < end) cur.load(p, r0 + mine, j);
     const int64_t id_at = begin * p.k + threadIdx.x;
     const int first_id = id_at < end * p.k ? p.ids[id_at] : -1;
@@ -369,7 +369,7 @@ __device__ __forceinline__ void wave_sync() {
 // each expert in registers: 68 us where this takes 30, 65536 x 256, 8 of them.)  Where an expert is named
 // twice for a token, which a choice learns by not finding its own number at the place, the lane that holds
 // the expert adds its parts in the order of the choices.
-template <int L, int NV, bool F32, bool SIG>
+template <int L, int NV, bool F32, bool SIG, bool WIDE>
 __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) {
     constexpr int R = 64 / L, ROWS = 4 * R, N = 4 * NV;
     __shared__ float4 lds[2][4][R][NV][L];
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
     for (int64_t r0 = begin; r0 < end; r0 += ROWS) {
         const int64_t r = r0 + wave * R + lane / L;
         const int64_t row = r < p.T ? r : p.T - 1;  // the lanes of a wave stay together
-        Logits<L, NV, F32> raw;
+        Logits<L, NV, F32, WIDE> raw;
         raw.load(p, row, j);
         const int32_t* ids = p.ids + row * p.k;
         const float* dw = p.dweights + row * p.k;
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
             }
             if (F32) {
                 float* dst = static_cast<float*>(p.dlogits) + r * p.ld_d + e;
-                if (p.wide) {
+                if (WIDE) {
                     *reinterpret_cast<float4*>(dst) = make_float4(d[0], d[1], d[2], d[3]);
                 } else {
 #pragma unroll
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
                 }
             } else {
                 uint16_t* dst = static_cast<uint16_t*>(p.dlogits) + r * p.ld_d + e;
-                if (p.wide) {
+                if (WIDE) {
                     *reinterpret_cast<uint2*>(dst) = make_uint2(rg_pack(d[0], d[1]), rg_pack(d[2], d[3]));
                 } else {
 #pragma unroll
@@ -557,8 +557,10 @@ static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     constexpr int ROWS = 4 * (64 / L);
     if (back) p.rows = p.T <= 2048 * ROWS ? ROWS : (p.T + 2048 * ROWS - 1) / (2048 * ROWS) * ROWS;
     const unsigned blocks = (unsigned)((p.T + p.rows - 1) / p.rows);
-    if (back) route_back_kernel<L, NV, F32, SIG><<<dim3(blocks), dim3(256), 0, stream>>>(p);
-    else balance_kernel<L, NV, F32, SIG><<<dim3(blocks), dim3(64 * BAL_WAVES), 0, stream>>>(p);
+    if (back && p.wide) route_back_kernel<L, NV, F32, SIG, true><<<dim3(blocks), dim3(256), 0, stream>>>(p);
+    else if (back) route_back_kernel<L, NV, F32, SIG, false><<<dim3(blocks), dim3(256), 0, stream>>>(p);
+    else if (p.wide) balance_kernel<L, NV, F32, SIG, true><<<dim3(blocks), dim3(64 * BAL_WAVES), 0, stream>>>(p);
+    else balance_kernel<L, NV, F32, SIG, false><<<dim3(blocks), dim3(64 * BAL_WAVES), 0, stream>>>(p);
 }
 
 template <bool F32, bool SIG>
