@@ -4,7 +4,10 @@
 //   a scale for each row or for each block of 1 x 128
 //   dx = rstd (g - xh mean(g xh)) + dh,  dw = sum over rows of dy xh,  g = dy w, xh = h rstd
 //
-// Bound: HBM.
+// Bound: HBM.  Each byte is moved once: the row stays in registers between its sum, its maximum and its
+// bytes (a block that reads it again: 508 us where this takes 185).  16384 x 7168 with residual, bf16 and
+// block factors 185 us (5.7 TB/s), the backward with dh 152 us (6.2 TB/s).  Small calls are the host's: the
+// kernel takes 2.7 us for one row of 7168.
 #include "common.hpp"
 #include "plan.hpp"
 
@@ -183,13 +186,6 @@ __device__ __forceinline__ void load_weight(const void* w, bool w32, int c, int 
     }
 }
 
-// Block b of n in an order that gives each XCD (blocks go to the 8 of them in turn) one run of rows: what
-// neighbouring rows write side by side, the factors of a block column, then meets in one L2.
-__device__ __forceinline__ int64_t xcd_run(unsigned b, unsigned n) {
-    const unsigned x = b % 8, q = n / 8, r = n % 8;
-    return (int64_t)x * q + (x < r ? x : r) + b / 8;
-}
-
 // Sums (SUM) and maxima over a wave, the same in all lanes: by DPP 1 and 2 lanes away, then mirrored in 8 and
 // in 16, then the four rows of 16.
 template <bool SUM>
@@ -222,14 +218,16 @@ __device__ __forceinline__ float across(float v, float* red) {
     return v;
 }
 
-// Rows held in registers: WPR waves a row, NV chunks of 8 elements a lane.
+// Rows held in registers: WPR waves a row, NV chunks of 8 elements a lane.  Blocks take the rows in turn, so
+// neighbouring rows are at work at once all over the chip.  (A run of rows for each XCD, whose factors then
+// meet in one L2: 16384 x 7168 with residual, bf16 and block factors 198 us against 185, 32768 x 2048 124
+// against 105; block rows alone 68 against 69.)
 template <int SC, int FMT, int WPR, int NV, int ACC>
 __global__ __launch_bounds__(64 * norm_waves(WPR)) void norm_kernel(const NormArgs p) {
     constexpr int WAVES = norm_waves(WPR), RPB = WAVES / WPR, TPR = 64 * WPR;
     __shared__ float red[3][WAVES];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), t = threadIdx.x % TPR;
-    const int64_t group = SC == FP8Q_NORM_BLOCK ? xcd_run(blockIdx.x, gridDim.x) : (int64_t)blockIdx.x;
-    const int64_t r = group * RPB + wave / WPR;
+    const int64_t r = (int64_t)blockIdx.x * RPB + wave / WPR;
     const bool row_ok = r < p.rows;
     const int64_t row = row_ok ? r : p.rows - 1;
     const int cols = row_ok ? (int)p.cols : 0;  // no columns of a row past the last
@@ -344,6 +342,7 @@ static void launch_norm(const NormArgs& p, int acc, hipStream_t stream) {
 }
 
 // More than the last-level cache holds of what a call reads and writes: none of it will be found there.
+// Backward 16384 x 7168 161 us past the caches, 182 through them; with fp32 gradients 288 and 314.
 static inline bool past_caches(int64_t rows, int64_t cols, int bytes) { return (double)rows * cols * bytes > 2.0 * kStreamBytes; }
 
 // Rows that start on whole vectors of 8 elements; none where there is no matrix.
