@@ -6,7 +6,9 @@
 //   dl      = p slope (dp - sum_e p dp),  dp[e] = dloss[s] E / (k n^2) count[s,e]
 //           + the chosen weights' part;  slope = 1 (softmax) or 1 - sigmoid(l), of log(score) over l
 //
-// Bound: HBM for large T * E, launches below.
+// Bound: HBM for many tokens of few experts or of fp32 logits (65536 x 256: sums 23 us, gradient 29, 13 and 27
+// at a copy's rate); with bf16 logits of 256 experts waits and exponentials (65536 x 256 sigmoid: sums 16 us and
+// their join 6, gradient 31, of which a copy's rate would take 14); launches below (96 x 4: 3 us each).
 #include "common.hpp"
 #include "plan.hpp"
 
@@ -27,7 +29,7 @@ struct RouteGradArgs {
     int64_t ld_d;
     float* mass;                 // [chunks + S][E] sums of p of a chunk's tokens of one sequence
     int32_t* part;               // [chunks + S][E] their counts
-    float* group_sums;               // [S][groups] what groups of experts give a sequence's loss, or null
+    float* group_sums;           // [S][groups] what groups of experts give a sequence's loss, or null
     int64_t rows;                // of a chunk
     int E, k, S;
     bool sigmoid, renorm, wide;  // wide: rows start on whole vectors of 4, and E is a multiple of 4
@@ -42,7 +44,7 @@ __device__ __forceinline__ uint32_t rg_pack(float a, float b) {  // to the neare
 }
 
 // The value of another lane of the 16 that a DPP operation reaches: 1 and 2 away, then mirrored in 8 and 16
-// (whose group_sums hold one value each by then).
+// (whose lanes hold one value each by then).
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
@@ -366,7 +368,7 @@ __device__ __forceinline__ void wave_sync() {
 
 // p.rows rows of a block.  What the chosen experts' weights add goes through LDS: a row's scores are read
 // there by its choices, and each choice leaves its part at its expert's place.  (Comparing each choice with
-// each expert in registers: 68 us where this takes 30, 65536 x 256, 8 of them.)  Where an expert is named
+// each expert in registers: 52 us where this takes 30, 65536 x 256, 8 of them.)  Where an expert is named
 // twice for a token, which a choice learns by not finding its own number at the place, the lane that holds
 // the expert adds its parts in the order of the choices.
 template <int L, int NV, bool F32, bool SIG, bool WIDE>
