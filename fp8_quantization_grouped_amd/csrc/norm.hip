@@ -4,7 +4,7 @@
 //   a scale for each row or for each block of 1 x 128
 //   dx = rstd (g - xh mean(g xh)) + dh,  dw = sum over rows of dy xh,  g = dy w, xh = h rstd
 //
-// Bound: HBM.  Each byte is moved once: the row stays in registers between its sum, its maximum and its
+// Bound: HBM.  Each byte is moved once, but for partial lines of the block factors: the row stays in registers between its sum, its maximum and its
 // bytes (a block that reads it again: 508 us where this takes 185).  16384 x 7168 with residual, bf16 and
 // block factors 185 us (5.7 TB/s), the backward with dh 152 us (6.2 TB/s).  Small calls are the host's: the
 // kernel takes 2.7 us for one row of 7168.
