@@ -1022,7 +1022,8 @@ class AdamWStates:
     factors float32 [ceil(n/128)] in exp_avg_scales and exp_avg_sq_scales: of a flattened parameter the
     layout that fp8_block_quant_rowwise gives one row.  masters: float32 copies of bf16 parameters, where
     the steps add up; None for a parameter without one.  States given (those of an earlier run) are used
-    as they are, others begin with zeros."""
+    as they are, others begin with zeros.  Each tensor keeps its memory: a parameter or master that was
+    given another (p.data = ...) is refused, and needs states made anew."""
 
     def __init__(self, params, bits: int = 8, masters=None, exp_avg=None, exp_avg_sq=None,
                  exp_avg_scales=None, exp_avg_sq_scales=None):
@@ -1049,10 +1050,9 @@ class AdamWStates:
                 used = [[zeros(p.shape, torch.float32) for p in self.params] for _ in range(2)]
         self.exp_avg, self.exp_avg_sq = used[:2]
         self.exp_avg_scales, self.exp_avg_sq_scales = used[2:] if eight else ([None] * n, [None] * n)
-        # what torch has recorded of a parameter's value is no longer that after a step, and torch is told so
-        self._watched = [t for t in self.params + self.masters if t is not None and t.requires_grad]
         self._table = (_AdamTensor * n)()
-        taken = set()
+        self._held = []  # alive as long as the table has their addresses
+        taken = []
         for i, p in enumerate(self.params):
             m = p.numel()
             mine = [p, self.masters[i], self.exp_avg[i], self.exp_avg_sq[i]]
@@ -1066,15 +1066,19 @@ class AdamWStates:
                 for t in mine[4:]:
                     self._flat(t, "a state's scales", _F32, _blocks(m))
             for t in mine:
-                if t is not None and m:
-                    _want(t.data_ptr() not in taken, "no two parameters or states may share memory")
-                    taken.add(t.data_ptr())
+                if t is not None:
+                    self._held.append(t.detach())
+                    if m:
+                        taken.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
             row = self._table[i]
             row.param, row.n, row.param_dtype = p.data_ptr(), m, _OUT[p.dtype]
             row.master = None if mine[1] is None else mine[1].data_ptr()
             row.exp_avg, row.exp_avg_sq = mine[2].data_ptr(), mine[3].data_ptr()
             if eight:
                 row.exp_avg_scales, row.exp_avg_sq_scales = mine[4].data_ptr(), mine[5].data_ptr()
+        taken.sort()
+        _want(all(a[1] <= b[0] for a, b in zip(taken, taken[1:])), "no two parameters or states may share memory")
+        self._at = [(p.data_ptr(), p.numel(), None if m is None else m.data_ptr()) for p, m in zip(self.params, self.masters)]
 
     def _flat(self, t, what, dtypes, n):
         _want(t.is_cuda and t.device == self.device, f"{what} must be on the first parameter's GPU")
@@ -1096,13 +1100,21 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
     _want(eps > 0, "eps must be positive")
     h = _Adam(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay, state_bits=states.bits,
               seed=seed & 0xFFFFFFFF)
+    changed = []
     for i, g in enumerate(grads):
         row = table[i]
         if g is None:
             row.grad = None
             continue
+        p, master, at = states.params[i], states.masters[i], states._at[i]
+        if not (p.data_ptr() == at[0] and p.numel() == at[1] and p.is_contiguous()
+                and (master is None or master.data_ptr() == at[2])):
+            raise ValueError("a parameter or master has other memory than the states were made for")
+        changed.append(p)
+        if master is not None:
+            changed.append(master)
         if not (g.is_cuda and g.device == dev and g.dtype in _OUT and g.is_contiguous()
-                and g.shape == states.params[i].shape):
+                and g.shape == p.shape):
             raise ValueError("a gradient must be contiguous, bfloat16 or float32, of its parameter's shape and on "
                              "its GPU")
         row.grad, row.grad_dtype = g.data_ptr(), _OUT[g.dtype]
@@ -1121,5 +1133,7 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
     if not grads:
         return
     _call("adamw_step", dev, ctypes.addressof(table), len(grads), ctypes.addressof(h))
-    if states._watched:
-        torch.autograd.graph.increment_version(states._watched)
+    # what torch has saved of a parameter's value is no longer that, and torch is told so
+    changed = [t for t in changed if not t.is_inference()]
+    if changed:
+        torch.autograd.graph.increment_version(changed)

@@ -35,6 +35,48 @@ def test_step_limits_and_nothing_to_do():
     assert fq.lib().adamw_step(None, 1, None, None) == INVALID
 
 
+def states(params, masters=None):
+    """8-bit states on tensors of the host that the binding takes for a GPU's."""
+    many = lambda dtype, size: [zeros(size(p.numel()), dtype=dtype) for p in params]
+    whole, blocks = lambda n: n, lambda n: -(-n // 128)
+    return fq.AdamWStates(params, 8, masters, many(U8, whole), many(U8, whole), many(torch.float32, blocks), many(torch.float32, blocks))
+
+
+def test_states_of_memory_that_overlaps(calls):  # noqa: F811
+    all_ = zeros(300)
+    for params in ([all_[:200], all_[100:]], [all_, all_[299:]], [all_[10:20], all_[:300]]):
+        with pytest.raises(ValueError, match="share memory"):
+            states(params)
+    states([all_[:100], all_[100:300]])
+
+
+def test_step_refuses_parameters_of_other_memory(calls):  # noqa: F811
+    for other in (lambda p: zeros(4, 4), lambda p: p.data.t(), lambda p: p.data[:2]):
+        p = zeros(4, 4)
+        s = states([p])
+        fq.adamw_step(s, [zeros(4, 4)], 1, 1e-3)
+        p.data = other(p)
+        with pytest.raises(ValueError, match="other memory"):
+            fq.adamw_step(s, [zeros(*p.shape)], 2, 1e-3)
+        fq.adamw_step(s, [None], 2, 1e-3)
+    p, m = zeros(4, 4, dtype=BF16), zeros(4, 4)
+    s = states([p], [m])
+    m.data = zeros(4, 4)
+    with pytest.raises(ValueError, match="other memory"):
+        fq.adamw_step(s, [zeros(4, 4)], 1, 1e-3)
+    assert len(calls) == 6
+
+
+def test_step_tells_torch_of_what_it_changes_alone(calls):  # noqa: F811
+    p, m = [zeros(8, dtype=BF16), zeros(8)], [zeros(8), None]
+    s = states(p, m)
+    before = [t._version for t in (p[0], m[0], p[1])]
+    fq.adamw_step(s, [None, zeros(8)], 1, 1e-3)
+    assert [t._version for t in (p[0], m[0], p[1])] == [before[0], before[1], before[2] + 1]
+    fq.adamw_step(s, [zeros(8), None], 2, 1e-3)
+    assert [t._version for t in (p[0], m[0], p[1])] == [before[0] + 1, before[1] + 1, before[2] + 1]
+
+
 def test_states_refuse(calls):  # noqa: F811
     p = [zeros(4, 8), zeros(300, dtype=BF16)]
     same = zeros(32)
@@ -52,8 +94,7 @@ def test_states_refuse(calls):  # noqa: F811
 
 
 def test_step_binding_refuses(calls):  # noqa: F811
-    s = fq.AdamWStates.__new__(fq.AdamWStates)
-    s.params, s.bits, s.device, s._table, s._watched = [zeros(4, 8)], 8, zeros(1).device, (fq._AdamTensor * 1)(), []
+    s = states([zeros(4, 8)])
     g = [zeros(4, 8)]
     for kw in (dict(grads=[]), dict(grads=[zeros(32)]), dict(grads=[zeros(4, 8, dtype=torch.float16)]), dict(grads=[torch.zeros(4, 8)]),
                dict(grads=[zeros(8, 4).t()]), dict(step=0), dict(step=zeros(1)), dict(step=zeros(2, dtype=torch.int32)),
