@@ -169,8 +169,9 @@ static inline int64_t balance_rows(int64_t T, int64_t E) {
     const int64_t once = BAL_WAVES * 64 / route_lanes(E), r = plan_up(T, 512);
     return r < once ? once : r;
 }
-// One block takes all tokens and needs no second launch to join them (96 x 4, as called: 10 us in two, 7 in one).
-static inline bool balance_is_small(int64_t T, int64_t E) { return T <= BAL_WAVES * 64 / route_lanes(E); }
+// One block takes all tokens and needs no second launch to join them (96 x 4, as called: 10 us in two, 7 in one),
+// of at most 64 sequences: it takes one after the other, and leaves the empty ones' results too.
+static inline bool balance_is_small(int64_t T, int64_t E, int64_t S) { return S <= 64 && T <= BAL_WAVES * 64 / route_lanes(E); }
 // Places for the sums of a chunk's tokens of one sequence.
 static inline int64_t balance_slots(int64_t T, int64_t E, int64_t S) { return plan_up(T, balance_rows(T, E)) + S; }
 // Groups of experts that join a sequence's sums, in a block each, where one block a sequence would read more

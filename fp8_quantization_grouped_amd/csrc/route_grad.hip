@@ -103,6 +103,16 @@ struct Ends {
         if (all) e = S <= 64 ? __shfl(mine, s < 0 ? 0 : s, 64) : all[s < 0 ? 0 : s];
         return s < 0 || e < 0 ? 0 : e > T ? T : e;
     }
+    // The first sequence behind s whose end lies behind row r, S for none; each lane by itself.
+    __device__ __forceinline__ int after(int s, int64_t r) const {
+        int lo = s + 1, hi = S;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if ((int64_t)all[mid] > r) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    }
     // The sequence of row r, the same in the whole wave: the first whose end lies behind it, S for rows behind
     // the last; of more than 64, by looking at 64 places at a time.
     __device__ __forceinline__ int of(int64_t r) const {
@@ -259,6 +269,9 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_kernel(const RouteGrad
             if (small) {
                 for (int e = threadIdx.x; e < p.E; e += 64 * BAL_WAVES) p.counts[(int64_t)s * p.E + e] = 0;
                 if (threadIdx.x == 0) p.loss[s] = 0.0f;
+            } else {  // on past all that are empty, and never back, whatever the ends say
+                const int at = ends.of(r0) - 1;
+                s = at > s ? at : s;
             }
             continue;
         }
@@ -416,8 +429,8 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
         // the row's sequence, and what its loss gives each expert
         bool ahead = s < p.S && row >= seq_last, other = ahead;
         int64_t seq_first = 0;
-        while (__any(ahead)) {
-            if (ahead) s++;
+        for (int turn = 0; __any(ahead); turn++) {  // a few steps, then by halves
+            if (ahead) s = turn < 4 || p.S <= 64 ? s + 1 : ends.after(s, row);
             const int at = s < p.S ? s : p.S - 1;
             const int64_t from = ends.end(at - 1), to = ends.end(at);
             if (ahead) {
@@ -596,7 +609,7 @@ static inline bool rg_wide(const void* p, int64_t ld, int64_t E, bool f32) {
 }  // namespace fp8q
 
 extern "C" size_t moe_balance_workspace_size(int64_t T, int64_t E, int32_t sequences) {
-    if (T <= 0 || E <= 0 || sequences <= 0 || fp8q::balance_is_small(T, E)) return 0;
+    if (T <= 0 || E <= 0 || sequences <= 0 || fp8q::balance_is_small(T, E, sequences)) return 0;
     const int groups = fp8q::balance_groups(T, E, sequences);
     return (size_t)fp8q::balance_slots(T, E, sequences) * (size_t)E * 8 + (groups > 1 ? (size_t)groups * (size_t)sequences * 4 : 0);
 }
@@ -611,7 +624,7 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
         (scoring != FP8Q_SCORE_SOFTMAX && scoring != FP8Q_SCORE_SIGMOID) || !loss || !counts || (T > 0 && (!logits || !ids)))
         return FP8Q_ERR_INVALID_ARG;
     if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL || S >= 1 << 22) return FP8Q_ERR_UNSUPPORTED;
-    const bool small = balance_is_small(T, E);
+    const bool small = balance_is_small(T, E, S);
     if (!small && (!workspace || workspace_bytes < moe_balance_workspace_size(T, E, S))) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     RouteGradArgs p{};

@@ -182,3 +182,28 @@ def test_joins_in_groups_of_experts(fq, T, E, k, ends):
     first = run(fq, l, ids, dw, sequences=seq)
     for a, b in zip(first, run(fq, l, ids, dw, sequences=seq)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,E,k", [(300, 8, 2), (5000, 64, 6)])
+def test_many_empty_sequences(fq, T, E, k):
+    """Runs of empty sequences before, between and behind tokens' ones: the losses and counts of those with tokens
+    as without the empty ones, zeros for these, and the same gradient to the bit."""
+    l, ids, dw = case(T, E, k, T)
+    ends, few = [], [T // 3, T // 3 + 1, T - 7]
+    at = []
+    for before, e in zip([0] + few, few):
+        ends += [before] * 30011 + [e]
+        at.append(len(ends) - 1)
+    ends = torch.tensor(ends + [few[-1]] * 10007, dtype=I32).cuda()
+    few = torch.tensor(few, dtype=I32).cuda()
+    loss, counts = fq.moe_balance(l, ids, sequences=ends)
+    loss3, counts3 = fq.moe_balance(l, ids, sequences=few)
+    assert torch.equal(counts[at], counts3) and int(counts.sum()) == int(counts3.sum())
+    # sums of at most T and E positive terms in two orders
+    assert bool(((loss[at] - loss3).abs() <= 2 * (T + E) * rl.U * loss3).all())
+    rest = torch.ones(len(ends), dtype=torch.bool)
+    rest[at] = False
+    assert not loss[rest.cuda()].any()
+    dloss = torch.linspace(0.5, 1.5, len(ends)).cuda()
+    d = fq.moe_route_backward(l, ids, dw, dloss=dloss, counts=counts, sequences=ends)
+    assert torch.equal(d, fq.moe_route_backward(l, ids, dw, dloss=dloss[at].contiguous(), counts=counts3, sequences=few))
