@@ -1078,7 +1078,10 @@ class AdamWStates:
                 row.exp_avg_scales, row.exp_avg_sq_scales = mine[4].data_ptr(), mine[5].data_ptr()
         taken.sort()
         _want(all(a[1] <= b[0] for a, b in zip(taken, taken[1:])), "no two parameters or states may share memory")
-        self._at = [(p.data_ptr(), p.numel(), None if m is None else m.data_ptr()) for p, m in zip(self.params, self.masters)]
+        self._rows = [(row, p, row.param, p.shape, m, row.master) for row, p, m in zip(self._table, self.params, self.masters)]
+        # whose values torch may have saved (inference tensors' it never does)
+        self._seen = [[t for t in pair if t is not None and not t.is_inference()] for pair in zip(self.params, self.masters)]
+        self._all_seen = [t for pair in self._seen for t in pair]
 
     def _flat(self, t, what, dtypes, n):
         _want(t.is_cuda and t.device == self.device, f"{what} must be on the first parameter's GPU")
@@ -1093,28 +1096,21 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
     be device tensors of one element, which a replayed graph reads anew.  grad_scale: float32 device
     tensor of one element that the gradients are multiplied by.  The random bits that 8-bit states are
     rounded by are a function of seed + step."""
-    dev, table = states.device, states._table
+    dev = states.device
     grads = list(grads)
     _want(len(grads) == len(states.params), "grads must be as many as the parameters")
     _want(0 <= betas[0] < 1 and 0 <= betas[1] < 1, "betas must lie in [0, 1)")
     _want(eps > 0, "eps must be positive")
     h = _Adam(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay, state_bits=states.bits,
               seed=seed & 0xFFFFFFFF)
-    changed = []
-    for i, g in enumerate(grads):
-        row = table[i]
+    for g, (row, p, at, shape, master, master_at) in zip(grads, states._rows):
         if g is None:
             row.grad = None
             continue
-        p, master, at = states.params[i], states.masters[i], states._at[i]
-        if not (p.data_ptr() == at[0] and p.numel() == at[1] and p.is_contiguous()
-                and (master is None or master.data_ptr() == at[2])):
+        if not (p.data_ptr() == (at or 0) and p.shape == shape and p.is_contiguous()
+                and (master is None or master.data_ptr() == (master_at or 0))):
             raise ValueError("a parameter or master has other memory than the states were made for")
-        changed.append(p)
-        if master is not None:
-            changed.append(master)
-        if not (g.is_cuda and g.device == dev and g.dtype in _OUT and g.is_contiguous()
-                and g.shape == p.shape):
+        if not (g.is_cuda and g.device == dev and g.dtype in _OUT and g.is_contiguous() and g.shape == shape):
             raise ValueError("a gradient must be contiguous, bfloat16 or float32, of its parameter's shape and on "
                              "its GPU")
         row.grad, row.grad_dtype = g.data_ptr(), _OUT[g.dtype]
@@ -1132,8 +1128,10 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
             _want(t is None, "grad_scale must be a device tensor")
     if not grads:
         return
-    _call("adamw_step", dev, ctypes.addressof(table), len(grads), ctypes.addressof(h))
+    _call("adamw_step", dev, ctypes.addressof(states._table), len(grads), ctypes.addressof(h))
     # what torch has saved of a parameter's value is no longer that, and torch is told so
-    changed = [t for t in changed if not t.is_inference()]
+    changed = states._all_seen
+    if any(g is None for g in grads):
+        changed = [t for g, pair in zip(grads, states._seen) if g is not None for t in pair]
     if changed:
         torch.autograd.graph.increment_version(changed)
