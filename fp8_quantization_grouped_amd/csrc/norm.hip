@@ -4,10 +4,10 @@
 //   a scale for each row or for each block of 1 x 128
 //   dx = rstd (g - xh mean(g xh)) + dh,  dw = sum over rows of dy xh,  g = dy w, xh = h rstd
 //
-// Bound: HBM.  Each byte is moved once, but for partial lines of the block factors: the row stays in registers between its sum, its maximum and its
-// bytes (a block that reads it again: 508 us where this takes 185).  16384 x 7168 with residual, bf16 and
-// block factors 185 us (5.7 TB/s), the backward with dh 152 us (6.2 TB/s).  Small calls are the host's: the
-// kernel takes 2.7 us for one row of 7168.
+// Bound: HBM.  Each byte is moved once, but for partial lines of the block factors: the row stays in registers
+// between its sum, its maximum and its bytes (a block that reads it again: 508 us where this takes 185).
+// 16384 x 7168 with residual, bf16 and block factors 185 us (5.7 TB/s), the backward with dh 152 us (6.2 TB/s).
+// Small calls are the host's: the kernel takes 2.7 us for one row of 7168.
 #include "common.hpp"
 #include "plan.hpp"
 
@@ -372,8 +372,8 @@ static void start_norm(const NormArgs& p, hipStream_t stream) {
     }
 }
 
-// Rows longer than registers hold, or shorter than a vector: a block of 4 waves per row, a wave takes blocks of 128 columns in turn, a lane
-// two of each; the row is read again (from cache) for the maximum and for the bytes.  A thread reads
+// Rows longer than registers hold, or shorter than a vector: a block of 4 waves per row, a wave takes blocks
+// of 128 columns in turn, a lane two of each; the row is read again (from cache) for the maximum and for the bytes.  A thread reads
 // only what it wrote of h, so h may be x or the residual.
 template <int FMT>
 __global__ __launch_bounds__(256) void norm_generic_kernel(const NormArgs p) {
@@ -635,8 +635,8 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(const NormBackArgs p) {
     }
 }
 
-// Rows longer than registers hold, or shorter than a vector: blocks take rows in turn, a thread the same columns of each; its columns' sums
-// for dw are kept in the block's own piece of the workspace.
+// Rows longer than registers hold, or shorter than a vector: blocks take rows in turn, a thread the same
+// columns of each; its columns' sums for dw are kept in the block's own piece of the workspace.
 template <bool G32>
 __global__ __launch_bounds__(256) void norm_back_generic_kernel(const NormBackArgs p) {
     __shared__ float red[4];
