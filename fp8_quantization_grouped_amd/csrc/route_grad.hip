@@ -8,7 +8,7 @@
 //
 // Bound: HBM for many tokens of few experts or of fp32 logits (65536 x 256: sums 23 us, gradient 29, 13 and 27
 // at a copy's rate); with bf16 logits of 256 experts waits and exponentials (65536 x 256 sigmoid: sums 16 us and
-// their join 6, gradient 31, of which a copy's rate would take 14); launches below (96 x 4: 3 us each).
+// their join 7, gradient 30 or, on one input again and again, 25, of which a copy's rate would take 14); launches below (96 x 4: 3 us each).
 #include "common.hpp"
 #include "plan.hpp"
 
@@ -570,7 +570,10 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
 template <int L, int NV, bool F32, bool SIG>
 static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     constexpr int ROWS = 4 * (64 / L);
-    if (back) p.rows = p.T <= 2048 * ROWS ? ROWS : (p.T + 2048 * ROWS - 1) / (2048 * ROWS) * ROWS;
+    // as many blocks of the gradient as 256 CUs hold at once, 4 each with 16 experts a lane (65536 x 256 bf16
+    // sigmoid, on one input: 25.2 us; 512 blocks 28.4, 768 29.2, 2048 28.3)
+    constexpr int64_t AT_ONCE = 1024 * ROWS;
+    if (back) p.rows = p.T <= AT_ONCE ? ROWS : (p.T + AT_ONCE - 1) / AT_ONCE * ROWS;
     const unsigned blocks = (unsigned)((p.T + p.rows - 1) / p.rows);
     if (back && p.wide) route_back_kernel<L, NV, F32, SIG, true><<<dim3(blocks), dim3(256), 0, stream>>>(p);
     else if (back) route_back_kernel<L, NV, F32, SIG, false><<<dim3(blocks), dim3(256), 0, stream>>>(p);
