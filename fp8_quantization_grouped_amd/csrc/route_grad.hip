@@ -8,7 +8,8 @@
 //
 // Bound: HBM for many tokens of few experts or of fp32 logits (65536 x 256: sums 23 us, gradient 29, 13 and 27
 // at a copy's rate); with bf16 logits of 256 experts waits and exponentials (65536 x 256 sigmoid: sums 16 us and
-// their join 7, gradient 30 or, on one input again and again, 25, of which a copy's rate would take 14); launches below (96 x 4: 3 us each).
+// their join 7, gradient 30 or, on one input again and again, 25, of which a copy's rate would take 14); launches
+// below (96 x 4: 3 us each).
 #include "common.hpp"
 #include "plan.hpp"
 
