@@ -628,7 +628,7 @@ extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype
         (scoring != FP8Q_SCORE_SOFTMAX && scoring != FP8Q_SCORE_SIGMOID) || !loss || !counts || (T > 0 && (!logits || !ids)))
         return FP8Q_ERR_INVALID_ARG;
     if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL || S >= 1 << 22) return FP8Q_ERR_UNSUPPORTED;
-    const bool small = balance_is_small(T, E, S);
+    const bool small = T == 0 || balance_is_small(T, E, S);  // neither takes a workspace
     if (!small && (!workspace || workspace_bytes < moe_balance_workspace_size(T, E, S))) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     RouteGradArgs p{};

@@ -521,7 +521,7 @@ fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* d
  *   ids int32 [T][top_k]; an id outside [0, E) counts nowhere, one named twice counts twice
  *   loss fp32 [S], counts int32 [S][E]
  *   workspace  moe_balance_workspace_size bytes, any content, 16-byte aligned; it may be null where that
- *              is 0 (few tokens)
+ *              is 0 (no or few tokens)
  * Sums in fp32, every one in a fixed order; counts are whole numbers.
  *
  * moe_route_backward: dlogits [T][ld_d] of logits_dtype, of the sum of
