@@ -675,7 +675,10 @@ extern "C" fp8q_status_t moe_route_backward(const void* logits, fp8q_out_t logit
     if (E > RG_MAX_E || top_k > RG_MAX_K || T > 0x7FFFFFFFLL || (dloss && S >= 1 << 22)) return FP8Q_ERR_UNSUPPORTED;
     RouteGradArgs p{};
     p.logits = logits; p.T = T; p.ld_l = ld_l; p.ids = ids; p.dweights = dweights; p.renorm = renormalize != 0; p.scale = scale;
-    p.dloss = dloss; p.counts = const_cast<int32_t*>(counts); p.sequences = sequences; p.S = S; p.dlogits = dlogits; p.ld_d = ld_d;
+    p.dlogits = dlogits; p.ld_d = ld_d;
+    if (dloss) {  // else none of them is looked at
+        p.dloss = dloss; p.counts = const_cast<int32_t*>(counts); p.sequences = sequences; p.S = S;
+    }
     p.E = (int)E; p.k = top_k; p.sigmoid = scoring == FP8Q_SCORE_SIGMOID;
     p.wide = rg_wide(logits, ld_l, E, f32) && rg_wide(dlogits, ld_d, E, f32);
     start_route_grad(p, f32, true, stream);

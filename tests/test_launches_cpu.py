@@ -21,3 +21,20 @@ def test_balance_of_no_tokens_takes_no_workspace(E):
     assert [fq.moe_balance_workspace_size(0, E, s) for s in S] == [0] * len(S)
     for s, (status, made) in zip(S, launches(*(balance(0, E, s, None, 0) for s in S))):
         assert status == OK and len(made) == 1 and "balance_join" in made[0].kernel and made[0].grid == [s, 1, 1]
+
+
+def test_gradient_without_a_loss_hands_no_sequences_on():
+    """Without dloss the kernel has no ends to read, whatever stands in the arguments: of the losses' part nothing but
+    nulls and zeros reaches it, and the launch is the one of a call that was given nothing."""
+    T, E = 100, 8
+
+    def back(counts, sequences, S):
+        return "moe_route_backward", (P, 1, T, E, E, 0, P, 2, P, 1, 1.0, None, counts, sequences, S, 2 * P, E)
+
+    (status, bare), *others = launches(back(None, None, 0), back(3 * P, 5 * P, 50), back(None, 5 * P, -7), back(3 * P, None, 1 << 30))
+    assert status == OK and len(bare) == 1 and "route_back" in bare[0].kernel
+    size = 15 * 8 + 3 * 4  # the argument's pointers and sizes, the last of them the number of sequences
+    assert bare[0].arg[size - 4:size] == bytes(4)
+    for status, made in others:
+        assert status == OK and made[0]._replace(arg=b"") == bare[0]._replace(arg=b"")
+        assert made[0].arg[:size] == bare[0].arg[:size]
