@@ -663,9 +663,10 @@ __global__ __launch_bounds__(256) void norm_back_generic_kernel(const NormBackAr
 
 // dw from the blocks' sums: a block takes 32 columns, 32 threads a column's parts in turn.
 __global__ __launch_bounds__(1024) void norm_back_join_kernel(const float* part, int parts, int64_t cols, float* dw) {
+    static_assert(NORM_JOIN == 32, "a column for each of 32 threads");
     __shared__ float red[32][33];
     const int i = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + i;
+    const int64_t c = (int64_t)blockIdx.x * NORM_JOIN + i;
     float s = 0.0f;
     if (c < cols) {
 #pragma unroll 8
@@ -751,7 +752,7 @@ extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, co
     if (cols == 0) return FP8Q_OK;
     if (!dweight || (rows > 0 && (!dy || !h || !rstd || !weight || !dx))) return FP8Q_ERR_INVALID_ARG;
     if (rows > 0 && ((dx == dy && ld_dx != ld_dy) || (dx == dh && ld_dx != ld_dh))) return FP8Q_ERR_INVALID_ARG;
-    if (rows > 0x7FFFFFFFLL || cols >= 1LL << 27) return FP8Q_ERR_UNSUPPORTED;  // (a launch takes fewer than 2^32 threads)
+    if (!norm_back_fits(rows, cols)) return FP8Q_ERR_UNSUPPORTED;
     if (rows > 0 && (!workspace || workspace_bytes < fp8_rms_norm_backward_workspace_size(rows, cols))) return FP8Q_ERR_WORKSPACE;
     if (!fp8q_aligned(workspace, 16)) return FP8Q_ERR_INVALID_ARG;
     NormBackArgs p{};
@@ -768,7 +769,7 @@ extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, co
         else launch_norm_back<false, false>(p, n, stream);
         FP8Q_CHECK_LAUNCH();
     }
-    norm_back_join_kernel<<<dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream>>>(p.part, (int)n.blocks, cols, dweight);
+    norm_back_join_kernel<<<dim3((unsigned)plan_up(cols, NORM_JOIN)), dim3(1024), 0, stream>>>(p.part, (int)n.blocks, cols, dweight);
     FP8Q_CHECK_LAUNCH();
     return FP8Q_OK;
 }

@@ -151,6 +151,11 @@ static inline NormBackPlan pick_norm_back(int64_t rows, int64_t cols) {
     p.blocks = turns ? plan_up(groups, turns) : 0;
     return p;
 }
+// Columns of a block of 1024 threads that joins the blocks' sums; such a launch takes fewer than 2^32 threads too.
+constexpr int NORM_JOIN = 32;
+static inline bool norm_back_fits(int64_t rows, int64_t cols) {
+    return rows < 1LL << 31 && plan_up(cols, NORM_JOIN) * 1024 < 1LL << 32;
+}
 
 // --------------------------------------------------------------------------- a router's training
 

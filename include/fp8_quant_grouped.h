@@ -498,7 +498,8 @@ fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t cols, int64_
  *   dy, dh, dx [rows][ld] of grad_dtype; dx may be dy or dh itself (the same pointer and leading
  *   dimension)
  *   workspace  fp8_rms_norm_backward_workspace_size bytes, any content, 16-byte aligned
- * Sums in fp32, every one in a fixed order.  rows < 2^31, cols < 2^27 (FP8Q_ERR_UNSUPPORTED beyond).
+ * Sums in fp32, every one in a fixed order.  rows < 2^31, cols <= 2^27 - 32 (FP8Q_ERR_UNSUPPORTED
+ * beyond).
  * rows == 0 gives a dweight of zeros. */
 size_t fp8_rms_norm_backward_workspace_size(int64_t rows, int64_t cols);
 fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,

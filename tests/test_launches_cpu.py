@@ -38,3 +38,16 @@ def test_gradient_without_a_loss_hands_no_sequences_on():
     for status, made in others:
         assert status == OK and made[0]._replace(arg=b"") == bare[0]._replace(arg=b"")
         assert made[0].arg[:size] == bare[0].arg[:size]
+
+
+@pytest.mark.parametrize("rows,cols", [(1, (1 << 27) - 33), (1, (1 << 27) - 32), (3, (1 << 27) - 31), (0, (1 << 27) - 32), (0, (1 << 27) - 31),
+                                       (1, (1 << 27) - 1), (5, 1 << 27)])
+def test_norm_backward_starts_nothing_that_it_cannot_finish(rows, cols):
+    """A launch takes fewer than 2^32 threads, the join of dw too: columns past that are refused before the first."""
+    need = fq.fp8_rms_norm_backward_workspace_size(rows, cols)
+    (status, made), = launches(("fp8_rms_norm_backward", (P, cols, None, 0, 0, P, rows, cols, cols, P, P, 0, P, cols, P, P, need)))
+    if cols > (1 << 27) - 32:
+        assert status == UNSUPPORTED and not made
+    else:
+        assert status == OK and len(made) == (2 if rows else 1)
+        assert all(l.grid[0] * l.block[0] < 1 << 32 and l.grid[1:] == l.block[1:] == [1, 1] for l in made)
