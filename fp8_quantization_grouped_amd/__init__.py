@@ -1022,8 +1022,9 @@ class AdamWStates:
     factors float32 [ceil(n/128)] in exp_avg_scales and exp_avg_sq_scales: of a flattened parameter the
     layout that fp8_block_quant_rowwise gives one row.  masters: float32 copies of bf16 parameters, where
     the steps add up; None for a parameter without one.  States given (those of an earlier run) are used
-    as they are, others begin with zeros.  Each tensor keeps its memory: a parameter or master that was
-    given another (p.data = ...) is refused, and needs states made anew."""
+    as they are, others begin with zeros.  Each tensor keeps its memory: a step refuses a parameter, master
+    or state that was given another (p.data = ..., another tensor in its list), which needs states made
+    anew; what is loaded into one is copied there."""
 
     def __init__(self, params, bits: int = 8, masters=None, exp_avg=None, exp_avg_sq=None,
                  exp_avg_scales=None, exp_avg_sq_scales=None):
@@ -1078,10 +1079,25 @@ class AdamWStates:
                 row.exp_avg_scales, row.exp_avg_sq_scales = mine[4].data_ptr(), mine[5].data_ptr()
         taken.sort()
         _want(all(a[1] <= b[0] for a, b in zip(taken, taken[1:])), "no two parameters or states may share memory")
-        self._rows = [(row, p, row.param, p.shape, m, row.master) for row, p, m in zip(self._table, self.params, self.masters)]
+        self._rows = [(row, p, p.shape) for row, p in zip(self._table, self.params)]
+        self._made_for = self._places()
         # whose values torch may have saved (inference tensors' it never does)
         self._seen = [[t for t in pair if t is not None and not t.is_inference()] for pair in zip(self.params, self.masters)]
         self._all_seen = [t for pair in self._seen for t in pair]
+
+    def _places(self):
+        """Where all of them lie now."""
+        lists = [self.params, self.exp_avg, self.exp_avg_sq]
+        if self.bits == 8:
+            lists += [self.exp_avg_scales, self.exp_avg_sq_scales]
+        places = [[*map(torch.Tensor.data_ptr, tensors)] for tensors in lists]
+        places.append([None if m is None else m.data_ptr() for m in self.masters])
+        return places
+
+    def _stepped_moved(self, grads) -> bool:
+        """Whether a list has another length, or a tensor that is stepped lies elsewhere than in the table."""
+        return any(len(now) != len(made) or any(a != b and g is not None for a, b, g in zip(now, made, grads))
+                   for now, made in zip(self._places(), self._made_for))
 
     def _flat(self, t, what, dtypes, n):
         _want(t.is_cuda and t.device == self.device, f"{what} must be on the first parameter's GPU")
@@ -1103,13 +1119,14 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
     _want(eps > 0, "eps must be positive")
     h = _Adam(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay, state_bits=states.bits,
               seed=seed & 0xFFFFFFFF)
-    for g, (row, p, at, shape, master, master_at) in zip(grads, states._rows):
+    moved = "a parameter, master or state has other memory than the states were made for"
+    _want(states._places() == states._made_for or not states._stepped_moved(grads), moved)
+    for g, (row, p, shape) in zip(grads, states._rows):
         if g is None:
             row.grad = None
             continue
-        if not (p.data_ptr() == (at or 0) and p.shape == shape and p.is_contiguous()
-                and (master is None or master.data_ptr() == (master_at or 0))):
-            raise ValueError("a parameter or master has other memory than the states were made for")
+        if not (p.shape == shape and p.is_contiguous()):
+            raise ValueError(moved)
         if not (g.is_cuda and g.device == dev and g.dtype in _OUT and g.is_contiguous() and g.shape == shape):
             raise ValueError("a gradient must be contiguous, bfloat16 or float32, of its parameter's shape and on "
                              "its GPU")
