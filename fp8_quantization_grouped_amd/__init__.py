@@ -656,6 +656,14 @@ def fp8_block_grouped_gemm(mode: int, a: torch.Tensor, a_scales: torch.Tensor, b
     return c
 
 
+def _written(*given) -> None:
+    """Tells torch of tensors that a call was given to write, None among them: what it has saved of their values is
+    no longer that (inference tensors' it never saves)."""
+    changed = [t for t in given if t is not None and not t.is_inference()]
+    if changed:
+        torch.autograd.graph.increment_version(changed)
+
+
 # ------------------------------------------------- a mixture-of-experts layer for a few tokens
 
 def _no_grad(what: str, *tensors) -> None:
@@ -717,6 +725,7 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int,
     else:
         _rows_of(logits, "logits", _F32, (T, E), dev)
         _call("moe_route_with_logits", dev, *args, logits.data_ptr(), _ld(logits, T, E), ws, need)
+        _written(logits)
     return ids, weights
 
 
@@ -819,6 +828,7 @@ def fp8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     _rows_of(weight, "weight", _WIDE, (cols,), dev)
     _want(scaling in _NORM_SCALING, "scaling must be block, row or None")
     _want(eps > 0, "eps must be positive")
+    given = () if h is y is q is scales is rstd is None else (h, y, q, scales, rstd)
     shape = (rows, cols)
     res_args = (None, 0, weight.data_ptr(), _OUT[weight.dtype], eps, None, 0)
     if residual is not None:
@@ -865,6 +875,8 @@ def fp8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         _rows_of(rstd, "rstd", _F32, (rows,), dev)
     _call("fp8_rms_norm", dev, x.data_ptr(), rows, cols, _ld(x, rows, cols), *res_args, *y_args,
           _NORM_SCALING[scaling], fmt, *q_args, rstd.data_ptr())
+    if given:
+        _written(*given)
     return Normed(h, y, q, scales, rstd)
 
 
@@ -881,6 +893,7 @@ def fp8_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     residual alike, dweight float32 [cols]).  dx may be given as dy or dh to replace it."""
     rows, cols, dev = _matrix(dy, "dy", _WIDE)
     _no_grad("fp8_rms_norm_backward", dy, dh)
+    given = () if dx is dweight is None else (dx, dweight)
     shape = (rows, cols)
     _rows_of(h, "h", _BF16, shape, dev)
     _rows_of(rstd, "rstd", _F32, (rows,), dev)
@@ -906,6 +919,8 @@ def fp8_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     _call("fp8_rms_norm_backward", dev, dy.data_ptr(), _ld(dy, rows, cols), *dh_args, _OUT[dy.dtype],
           h.data_ptr(), rows, cols, _ld(h, rows, cols), rstd.data_ptr(), weight.data_ptr(),
           _OUT[weight.dtype], dx.data_ptr(), _ld(dx, rows, cols), dweight.data_ptr(), ws, need)
+    if given:
+        _written(*given)
     return dx, dweight
 
 
@@ -947,6 +962,7 @@ def moe_balance(logits: torch.Tensor, ids: torch.Tensor, scoring: str = "softmax
     T, E, dev, top_k, args = _choice(logits, ids, scoring)
     _no_record("moe_balance", "moe_route_backward", logits)
     seq, S = _sequences(sequences, dev)
+    given = () if loss is counts is None else (loss, counts)
     if loss is None:
         loss = torch.empty(S, dtype=torch.float32, device=dev)
     else:
@@ -965,6 +981,8 @@ def moe_balance(logits: torch.Tensor, ids: torch.Tensor, scoring: str = "softmax
     else:
         ws, need = _workspace(workspace, dev)
     _call("moe_balance", dev, *args, seq, S, loss.data_ptr(), counts.data_ptr(), ws, need)
+    if given:
+        _written(*given)
     return loss, counts
 
 
@@ -991,12 +1009,15 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
         _rows_of(counts, "counts", _I32T, (S, E), dev)
         _want(counts.is_contiguous(), "counts must be contiguous")
         loss_args = (dloss.data_ptr(), counts.data_ptr(), seq, S)
+    given = () if dlogits is None else (dlogits,)
     if dlogits is None:
         dlogits = torch.empty(T, E, dtype=logits.dtype, device=dev)
     else:
         _rows_of(dlogits, "dlogits", (logits.dtype,), logits.shape, dev)
     _call("moe_route_backward", dev, *args, None if dweights is None else dweights.data_ptr(),
           int(renormalize), scale, *loss_args, dlogits.data_ptr(), _ld(dlogits, T, E))
+    if given:
+        _written(*given)
     return dlogits
 
 
