@@ -1041,7 +1041,8 @@ class AdamWStates:
     bits=32: exp_avg and exp_avg_sq are lists of float32 tensors like the parameters.  bits=8: exp_avg
     holds the first moments and exp_avg_sq the roots of the second ones as e4m3fn bytes, with the block
     factors float32 [ceil(n/128)] in exp_avg_scales and exp_avg_sq_scales: of a flattened parameter the
-    layout that fp8_block_quant_rowwise gives one row.  masters: float32 copies of bf16 parameters, where
+    layout that fp8_block_quant_rowwise gives one row.  An element whose moments 32 bits cannot hold (an
+    infinite gradient) is kept as NaN and leaves its block as it is.  masters: float32 copies of bf16 parameters, where
     the steps add up; None for a parameter without one.  States given (those of an earlier run) are used
     as they are, others begin with zeros.  Each tensor keeps its memory: a step refuses a parameter, master
     or state that was given another (p.data = ..., another tensor in its list), which needs states made

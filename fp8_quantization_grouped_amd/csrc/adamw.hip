@@ -11,7 +11,9 @@
 // remaining m by eps.  What the step itself uses is m' and v' in 32 bits, before they are kept.  The kept r
 // of a stationary gradient spreads about its true value by a sixth of it (b2 = 0.999) to a ninth (0.95),
 // the mean being 1% above: a value on the grid that moves by a small e of itself is rounded with a variance
-// of e times the step, so slow averages take little noise a step.
+// of e times the step, so slow averages take little noise a step.  An element whose m' or v' is not finite in
+// 32 bits (its gradient is not, or the square overflows) is kept as NaN and stays out of the factor: an infinite
+// factor would cost the other 127 their states, and a finite byte would hide it.
 //
 // Random bits: word(tensor, element) = mix(mix(seed * 0x9E3779B1 + tensor) + element), mix two rounds of
 // xor-shift and odd product (as in the finalizers of published hash functions, with constants of its
@@ -153,23 +155,28 @@ __device__ __forceinline__ void load8_fp8(const void* src, int64_t at, int n, bo
     }
 }
 
-// Largest magnitude of eight values each of 16 lanes, in all of them: by DPP 1 and 2 lanes away, then mirrored
-// in 8 and in 16.
+// Largest magnitude of eight values each of 16 lanes, in all of them, as its bits, whose order is the magnitudes'
+// with the infinite behind the finite and NaN behind these: by DPP 1 and 2 lanes away, then mirrored in 8 and
+// in 16.
+constexpr uint32_t kInfBits = 0x7F800000u;
 template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v) {
-    return fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false)));
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+    return v > o ? v : o;
 }
-__device__ __forceinline__ float block_amax(const float (&x)[8]) {
+__device__ __forceinline__ uint32_t block_amax(const float (&x)[8]) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(x[i]));
-    return dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(m))));
+    for (int i = 0; i < 8; i++) m = __builtin_elementwise_maximum(m, fabsf(x[i]));  // a NaN stays
+    return dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(__float_as_uint(m)))));
 }
 
 // Eight values as bytes, by their block's multiplier and random bits.  ROOT: values of which none is negative
-// and a nonzero one does not become zero: what lies under the grid's first value is taken for it.
+// and a nonzero one does not become zero: what lies under the grid's first value is taken for it.  lost: a bit
+// for each of them that is zero here and kept as NaN.
 template <bool ROOT, bool NT>
-__device__ __forceinline__ void keep8(void* dst, int64_t at, int n, bool wide, float s, const float (&x)[8], const uint32_t (&bits)[8]) {
+__device__ __forceinline__ void keep8(void* dst, int64_t at, int n, bool wide, float s, const float (&x)[8], const uint32_t (&bits)[8],
+                                      uint32_t lost) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -179,6 +186,11 @@ __device__ __forceinline__ void keep8(void* dst, int64_t at, int n, bool wide, f
         if ((i & 3) == 1) w[i >> 2] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, (int)w[i >> 2], 1);
         if ((i & 3) == 2) w[i >> 2] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, (int)w[i >> 2], 2);
         if ((i & 3) == 3) w[i >> 2] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, r, (int)w[i >> 2], 3);
+    }
+    if (lost) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (lost >> i & 1) w[i >> 2] |= 0x7Fu << (8 * (i & 3));
     }
     uint8_t* p = static_cast<uint8_t*>(dst) + at;
     if (wide && n == 8) {
@@ -276,8 +288,22 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
     if (!EIGHT) return;
     // 16 lanes share two blocks and so four factors: four lanes form each of them
     const int which = (threadIdx.x >> 2) & 3;
-    const float m0 = block_amax(m[0]), m1 = block_amax(m[H - 1]), r0 = block_amax(r[0]), r1 = block_amax(r[H - 1]);
-    const float mine = scale_from_amax<FP8Q_E4M3FN>(which & 2 ? (which & 1 ? r1 : m1) : which & 1 ? r0 : m0);
+    uint32_t m0 = block_amax(m[0]), m1 = block_amax(m[H - 1]), r0 = block_amax(r[0]), r1 = block_amax(r[H - 1]);
+    uint32_t amax = which & 2 ? (which & 1 ? r1 : m1) : which & 1 ? r0 : m0;
+    uint32_t lost = 0;  // elements that 32 bits do not hold, which must not become their neighbours' factor
+    if (__any(amax >= kInfBits)) {
+#pragma unroll
+        for (int i = 0; i < 8 * H; i++) {
+            float &a = m[i / 8][i % 8], &b = r[i / 8][i % 8];
+            if (!(fabsf(a) < INFINITY && b < INFINITY)) {
+                lost |= 1u << i;
+                a = b = 0.0f;
+            }
+        }
+        m0 = block_amax(m[0]), m1 = block_amax(m[H - 1]), r0 = block_amax(r[0]), r1 = block_amax(r[H - 1]);
+        amax = which & 2 ? (which & 1 ? r1 : m1) : which & 1 ? r0 : m0;
+    }
+    const float mine = scale_from_amax<FP8Q_E4M3FN>(__uint_as_float(amax));
     const int64_t at1 = at0 + (which & 2 ? 2048 : 0);
     if ((threadIdx.x & 3) == 0 && t.n > (at1 & ~(int64_t)(AB - 1))) (which & 1 ? t.v_scales : t.m_scales)[at1 / AB] = 1.0f / mine;
     const uint32_t key = mix(seed * 0x9E3779B1u + t.index);
@@ -290,8 +316,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
         uint32_t bits[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) bits[i] = mix(base + i);
-        keep8<false, NT>(t.m, at, n[h], wide, sm, m[h], bits);
-        keep8<true, NT>(t.v, at, n[h], wide, sr, r[h], bits);
+        keep8<false, NT>(t.m, at, n[h], wide, sm, m[h], bits, lost >> 8 * h & 0xFF);
+        keep8<true, NT>(t.v, at, n[h], wide, sr, r[h], bits, lost >> 8 * h & 0xFF);
     }
 }
 

@@ -559,7 +559,8 @@ fp8q_status_t moe_route_backward(const void* logits, fp8q_out_t logits_dtype, in
  *   below or above at random, in proportion to the distance (the step itself takes them unrounded); a
  *   nonzero r' is kept as one.  The random bits are a function of (seed + step) mod 2^32, the tensor's place in
  *   the list and the element's place in the tensor, so a step repeats to the bit.  States of zeros
- *   (bytes and factors) begin.
+ *   (bytes and factors) begin.  Where m' or v' is not finite (a gradient that is not, or whose square leaves
+ *   32 bits' range) both are kept as NaN, which stays, and the block's factors are those of its other elements.
  * Where step_device (int32) or lr_device (fp32) is not null the value there takes the place of step or
  * lr, so that a captured step can be replayed: the device's value is read at each replay.
  * tensors, h: on the host, read before the call returns.  A tensor with n == 0 or a null gradient is left
