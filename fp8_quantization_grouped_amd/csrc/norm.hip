@@ -737,7 +737,7 @@ extern "C" fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t c
 
 extern "C" size_t fp8_rms_norm_backward_workspace_size(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0) return 256;
-    return (size_t)fp8q::pick_norm_back(rows, cols).blocks * (size_t)cols * 4;
+    return (size_t)fp8q::norm_back_space(rows, cols);
 }
 
 extern "C" fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,

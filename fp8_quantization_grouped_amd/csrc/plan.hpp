@@ -151,6 +151,12 @@ static inline NormBackPlan pick_norm_back(int64_t rows, int64_t cols) {
     p.blocks = turns ? plan_up(groups, turns) : 0;
     return p;
 }
+// Bytes of the workspace: as many blocks as any number of rows up to this one gives (even turns take fewer for 257
+// groups than for 256), so that a workspace serves fewer rows too.
+static inline int64_t norm_back_space(int64_t rows, int64_t cols) {
+    const int64_t groups = plan_up(rows, pick_norm_back(rows, cols).rows);
+    return (groups < 256 ? groups : 256) * cols * 4;
+}
 // Columns of a block of 1024 threads that joins the blocks' sums; such a launch takes fewer than 2^32 threads too.
 constexpr int NORM_JOIN = 32;
 static inline bool norm_back_fits(int64_t rows, int64_t cols) {
@@ -184,6 +190,13 @@ static inline int64_t balance_slots(int64_t T, int64_t E, int64_t S) { return pl
 constexpr int BAL_GROUP = 32;
 static inline int balance_groups(int64_t T, int64_t E, int64_t S) {
     return E > BAL_GROUP && balance_slots(T, E, S) * E * 8 > S * (512 << 10) ? (int)plan_up(E, BAL_GROUP) : 1;
+}
+// Bytes of the workspace: as many places, and the groups' parts, as any number of tokens up to this one takes (rounded
+// rows of a chunk can leave fewer chunks to more tokens), so that a workspace serves fewer tokens and sequences too.
+static inline int64_t balance_space(int64_t T, int64_t E, int64_t S) {
+    const int64_t chunks = plan_up(T, BAL_WAVES * 64 / route_lanes(E)), places = (chunks < 512 ? chunks : 512) + S;
+    const bool groups = E > BAL_GROUP && places * E * 8 > S * (512 << 10);
+    return places * E * 8 + (groups ? plan_up(E, BAL_GROUP) * S * 4 : 0);
 }
 
 }  // namespace fp8q

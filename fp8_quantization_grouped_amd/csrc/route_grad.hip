@@ -614,8 +614,7 @@ static inline bool rg_wide(const void* p, int64_t ld, int64_t E, bool f32) {
 
 extern "C" size_t moe_balance_workspace_size(int64_t T, int64_t E, int32_t sequences) {
     if (T <= 0 || E <= 0 || sequences <= 0 || fp8q::balance_is_small(T, E, sequences)) return 0;
-    const int groups = fp8q::balance_groups(T, E, sequences);
-    return (size_t)fp8q::balance_slots(T, E, sequences) * (size_t)E * 8 + (groups > 1 ? (size_t)groups * (size_t)sequences * 4 : 0);
+    return (size_t)fp8q::balance_space(T, E, sequences);
 }
 
 extern "C" fp8q_status_t moe_balance(const void* logits, fp8q_out_t logits_dtype, int64_t T, int64_t E, int64_t ld_l,

@@ -497,7 +497,8 @@ fp8q_status_t fp8_rms_norm(const uint16_t* x, int64_t rows, int64_t cols, int64_
  * stream h from elsewhere, or null.
  *   dy, dh, dx [rows][ld] of grad_dtype; dx may be dy or dh itself (the same pointer and leading
  *   dimension)
- *   workspace  fp8_rms_norm_backward_workspace_size bytes, any content, 16-byte aligned
+ *   workspace  fp8_rms_norm_backward_workspace_size bytes, any content, 16-byte aligned; that of more
+ *              rows will do
  * Sums in fp32, every one in a fixed order.  rows < 2^31, cols <= 2^27 - 32 (FP8Q_ERR_UNSUPPORTED
  * beyond).
  * rows == 0 gives a dweight of zeros. */
@@ -522,7 +523,7 @@ fp8q_status_t fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* d
  *   ids int32 [T][top_k]; an id outside [0, E) counts nowhere, one named twice counts twice
  *   loss fp32 [S], counts int32 [S][E]
  *   workspace  moe_balance_workspace_size bytes, any content, 16-byte aligned; it may be null where that
- *              is 0 (no or few tokens)
+ *              is 0 (no or few tokens); that of more tokens and sequences will do
  * Sums in fp32, every one in a fixed order; counts are whole numbers.
  *
  * moe_route_backward: dlogits [T][ld_d] of logits_dtype, of the sum of

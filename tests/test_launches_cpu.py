@@ -51,3 +51,44 @@ def test_norm_backward_starts_nothing_that_it_cannot_finish(rows, cols):
     else:
         assert status == OK and len(made) == (2 if rows else 1)
         assert all(l.grid[0] * l.block[0] < 1 << 32 and l.grid[1:] == l.block[1:] == [1, 1] for l in made)
+
+
+def test_a_workspace_serves_fewer_rows_too():
+    """A program that holds one workspace for its largest batch: no smaller one is refused."""
+    rows = sorted({r + d for r in (1, 16, 255, 256, 257, 512, 4095, 4096, 4097, 8192, 65536, 131072, 1 << 20) for d in (-1, 0, 1)} | set(range(0, 1100)))
+    for cols in (7, 64, 512, 513, 1024, 7168, 8192, 8193, 16384, 20000):
+        sizes = [fq.fp8_rms_norm_backward_workspace_size(r, cols) for r in rows if r]
+        assert sizes == sorted(sizes) and sizes[-1] <= 256 * cols * 4
+    for E in (1, 8, 16, 17, 64, 65, 256, 300, 1024):
+        last = None
+        for S in (1, 2, 5, 9, 16, 64, 65, 1000):
+            sizes = [fq.moe_balance_workspace_size(r, E, S) for r in rows]
+            assert sizes == sorted(sizes)
+            assert last is None or all(a <= b for a, b in zip(last, sizes))
+            last = sizes
+
+
+def test_the_launches_stay_inside_the_workspace():
+    """What the kernels take of it, by the launches' own numbers: blocks of sums in the norm's backward, places in the
+    balance's (the argument's pointers to the masses, the counts and the groups' parts, and the rows of a chunk)."""
+    sizes = [(T, E, S) for T in (513, 4096, 4097, 5000, 65536, 300000) for E in (8, 64, 300, 1024) for S in (1, 3, 9, 70)]
+    calls = [balance(T, E, S, P, fq.moe_balance_workspace_size(T, E, S)) for T, E, S in sizes]
+    word = lambda l, at: int.from_bytes(l.arg[at:at + 8], "little")
+    for (T, E, S), (status, made) in zip(sizes, launches(*calls)):
+        need = fq.moe_balance_workspace_size(T, E, S)
+        assert status == OK
+        sums, join = made[0], made[1] if len(made) > 1 else None
+        if join is None:
+            assert need == 0
+            continue
+        mass, part, groups, rows = (word(join, 88 + 8 * i) for i in range(4))
+        places = -(-T // rows) + S
+        assert sums.grid[0] == places - S and mass == P and part == P + 4 * places * E and part + 4 * places * E <= P + need
+        if groups:
+            assert groups == P + 8 * places * E and groups + 4 * S * join.grid[1] <= P + need
+        else:
+            assert join.grid == [S, 1, 1]
+    for rows, cols in ((1, 64), (257, 64), (300, 7168), (257, 7168), (5000, 16384), (1000, 20000)):
+        need = fq.fp8_rms_norm_backward_workspace_size(rows, cols)
+        (status, made), = launches(("fp8_rms_norm_backward", (P, cols, None, 0, 0, P, rows, cols, cols, P, P, 0, P, cols, P, P, need)))
+        assert status == OK and made[0].grid[0] * cols * 4 <= need
