@@ -1108,23 +1108,28 @@ class AdamWStates:
         self._all_seen = [t for pair in self._seen for t in pair]
 
     def _places(self):
-        """Where all of them lie now."""
-        lists = [self.params, self.exp_avg, self.exp_avg_sq]
-        if self.bits == 8:
-            lists += [self.exp_avg_scales, self.exp_avg_sq_scales]
-        places = [[*map(torch.Tensor.data_ptr, tensors)] for tensors in lists]
-        places.append([None if m is None else m.data_ptr() for m in self.masters])
-        return places
+        """Where the masters and all others lie now, list by list."""
+        scales = (*self.exp_avg_scales, *self.exp_avg_sq_scales) if self.bits == 8 else ()
+        return ([m if m is None else m.data_ptr() for m in self.masters],
+                [*map(torch.Tensor.data_ptr, (*self.params, *self.exp_avg, *self.exp_avg_sq, *scales))])
 
     def _stepped_moved(self, grads) -> bool:
         """Whether a list has another length, or a tensor that is stepped lies elsewhere than in the table."""
-        return any(len(now) != len(made) or any(a != b and g is not None for a, b, g in zip(now, made, grads))
-                   for now, made in zip(self._places(), self._made_for))
+        n = len(grads)
+        lists = [self.masters, self.params, self.exp_avg, self.exp_avg_sq, self.exp_avg_scales, self.exp_avg_sq_scales]
+        return any(len(tensors) != n for tensors in lists) or any(
+            a != b and grads[i % n] is not None for now, made in zip(self._places(), self._made_for) for i, (a, b) in enumerate(zip(now, made)))
 
     def _flat(self, t, what, dtypes, n):
         _want(t.is_cuda and t.device == self.device, f"{what} must be on the first parameter's GPU")
         _want(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
         _want(t.numel() == n and t.is_contiguous(), f"{what} must be contiguous, of {n} elements")
+
+
+def _one_of(t, name, dtype, dev) -> int:
+    """Address of a device tensor of one element."""
+    _want(t.is_cuda and t.device == dev and t.dtype is dtype and t.numel() == 1, f"{name} must be one {dtype} on the parameters' GPU")
+    return t.data_ptr()
 
 
 def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -1143,9 +1148,11 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
               seed=seed & 0xFFFFFFFF)
     moved = "a parameter, master or state has other memory than the states were made for"
     _want(states._places() == states._made_for or not states._stepped_moved(grads), moved)
+    all_of_them = True
     for g, (row, p, shape) in zip(grads, states._rows):
         if g is None:
             row.grad = None
+            all_of_them = False
             continue
         if not (p.shape == shape and p.is_contiguous()):
             raise ValueError(moved)
@@ -1153,24 +1160,24 @@ def adamw_step(states: AdamWStates, grads, step, lr, betas=(0.9, 0.999), eps: fl
             raise ValueError("a gradient must be contiguous, bfloat16 or float32, of its parameter's shape and on "
                              "its GPU")
         row.grad, row.grad_dtype = g.data_ptr(), _OUT[g.dtype]
-    for name, t, dtype in (("step", step, torch.int32), ("lr", lr, torch.float32), ("grad_scale", grad_scale, torch.float32)):
-        if isinstance(t, torch.Tensor):
-            _want(t.is_cuda and t.device == dev and t.dtype is dtype and t.numel() == 1,
-                  f"{name} must be one {dtype} on the parameters' GPU")
-            setattr(h, name if name == "grad_scale" else name + "_device", t.data_ptr())
-        elif name == "lr":
-            h.lr = lr
-        elif name == "step":
-            _want(step >= 1, "step counts from 1")
-            h.step = step
-        else:
-            _want(t is None, "grad_scale must be a device tensor")
+    if isinstance(step, torch.Tensor):
+        h.step_device = _one_of(step, "step", torch.int32, dev)
+    else:
+        _want(step >= 1, "step counts from 1")
+        h.step = step
+    if isinstance(lr, torch.Tensor):
+        h.lr_device = _one_of(lr, "lr", torch.float32, dev)
+    else:
+        h.lr = lr
+    if grad_scale is not None:
+        _want(isinstance(grad_scale, torch.Tensor), "grad_scale must be a device tensor")
+        h.grad_scale = _one_of(grad_scale, "grad_scale", torch.float32, dev)
     if not grads:
         return
     _call("adamw_step", dev, ctypes.addressof(states._table), len(grads), ctypes.addressof(h))
     # what torch has saved of a parameter's value is no longer that, and torch is told so
     changed = states._all_seen
-    if any(g is None for g in grads):
+    if not all_of_them:
         changed = [t for g, pair in zip(grads, states._seen) if g is not None for t in pair]
     if changed:
         torch.autograd.graph.increment_version(changed)
