@@ -112,9 +112,9 @@ struct NormShape {
 };
 static inline NormShape pick_norm(int64_t rows, int64_t cols) {
     if (cols < 8 || cols > 32768) return {4, 0};
-    // A few rows, two a CU or less, by 16 waves each: 1 x 7168 3.1 us against 4.0 in 4 waves, 256 x 7168 5.4
-    // against 6.2, 64 x 2048 3.6 against 5.0; with 1024 rows it turns (13.6 against 12.5, 2048 wide 8.7
-    // against 6.4).
+    // A few rows, two a CU or less, by 16 waves each (residual, bf16 and blocks): 1 x 7168 3.4 us against 4.1
+    // in 4 waves, 256 x 7168 5.6 against 6.4, 64 x 2048 3.8 against 5.1; with 1024 rows it turns (12.2 against
+    // 11.2, 2048 wide 8.6 against 6.5).
     if (rows <= 512 && cols > 1024 && cols <= 8192) return {16, 1};
     if (cols <= 512) return {1, 1};
     if (cols <= 1024) return {1, 2};
@@ -146,7 +146,8 @@ static inline NormBackPlan pick_norm_back(int64_t rows, int64_t cols) {
         p.rows = 16 / p.waves;
     }
     // At most 256 blocks, each as often as the others: one for a CU at a time, and every block's sums of dw are
-    // written and read once more (16384 x 7168 152 us, with 512 blocks 159; 2048 x 2064 fp32 15 and 17).
+    // written and read once more (16384 x 7168 152 us, with 512 blocks 159; 2048 x 2064 fp32 15 and 17).  The
+    // workspace's size goes by them, so they do not depend on the device.
     const int64_t groups = plan_up(rows, p.rows), turns = plan_up(groups, 256);
     p.blocks = turns ? plan_up(groups, turns) : 0;
     return p;

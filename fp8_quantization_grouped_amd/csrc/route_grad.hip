@@ -571,8 +571,9 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteGradArgs p) 
 template <int L, int NV, bool F32, bool SIG>
 static void launch_route_grad(RouteGradArgs& p, bool back, hipStream_t stream) {
     constexpr int ROWS = 4 * (64 / L);
-    // as many blocks of the gradient as 256 CUs hold at once, 4 each with 16 experts a lane (65536 x 256 bf16
-    // sigmoid, on one input: 25.2 us; 512 blocks 28.4, 768 29.2, 2048 28.3)
+    // four blocks of the gradient for each of 256 CUs: as many as these hold at once of sigmoids with 16 experts a
+    // lane (115 to 126 registers; 65536 x 256 bf16 sigmoid, on one input: 25.2 us; 512 blocks 28.4, 768 29.2, 2048
+    // 28.3).  A softmax's (81 to 95) would fit five, few experts' (54 to 77) six to eight: not measured apart.
     constexpr int64_t AT_ONCE = 1024 * ROWS;
     if (back) p.rows = p.T <= AT_ONCE ? ROWS : (p.T + AT_ONCE - 1) / AT_ONCE * ROWS;
     const unsigned blocks = (unsigned)((p.T + p.rows - 1) / p.rows);
