@@ -87,13 +87,13 @@ class Launch(NamedTuple):
 
 
 @functools.lru_cache(None)
-def stub() -> str:
-    d = tempfile.mkdtemp()
-    src, lib = os.path.join(d, "launches.cpp"), os.path.join(d, "launches.so")
+def stub():
+    d = tempfile.TemporaryDirectory()
+    src, lib = os.path.join(d.name, "launches.cpp"), os.path.join(d.name, "launches.so")
     with open(src, "w") as f:
         f.write(SOURCE)
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", src, "-o", lib], check=True)
-    return lib
+    return lib, d  # the folder goes with the process
 
 
 def launches(*calls):
@@ -104,6 +104,6 @@ def launches(*calls):
         args = [getattr(a, "value", a) for a in args] + [None]
         assert len(args) == len(types), name
         given.append([name, result._type_, [t._type_ for t in types], args])
-    run = subprocess.run([sys.executable, "-c", CHILD, stub(), fq.LIB_PATH], input=json.dumps(given), capture_output=True, text=True)
+    run = subprocess.run([sys.executable, "-c", CHILD, stub()[0], fq.LIB_PATH], input=json.dumps(given), capture_output=True, text=True)
     assert run.returncode == 0, run.stderr
     return [(status, [Launch(k, g, b, s, bytes.fromhex(a)) for k, g, b, s, a in made]) for status, made in json.loads(run.stdout)]
